@@ -10,7 +10,8 @@ from . import build as _build
 
 FR_OK = 0
 STATUS_NAMES = {0: "FR_OK", 1: "FR_ERR_INVALID_ARG", 2: "FR_ERR_UNSUPPORTED",
-                3: "FR_ERR_WORKSPACE", 4: "FR_ERR_CUDA", 5: "FR_ERR_DEVICE_TIMEOUT"}
+                3: "FR_ERR_WORKSPACE", 4: "FR_ERR_CUDA", 5: "FR_ERR_DEVICE_TIMEOUT",
+                6: "FR_ERR_DEVICE_INPUT"}
 
 
 class FrError(RuntimeError):
@@ -21,6 +22,10 @@ class FrError(RuntimeError):
 
 FR_ROPE_EXACT = 0
 FR_ROPE_GGML_F32 = 1
+FR_KV_F16 = 0
+FR_KV_E4M3 = 1
+FR_ROWS_F32 = 0
+FR_ROWS_F16 = 1
 
 
 class FrRopeParams(ctypes.Structure):
@@ -41,6 +46,14 @@ class FrAttnPlan(ctypes.Structure):
     _fields_ = [("engine", ctypes.c_int), ("row_tiles", ctypes.c_int), ("splits", ctypes.c_int),
                 ("cluster", ctypes.c_int), ("merge_kernel", ctypes.c_int), ("launches", ctypes.c_int),
                 ("keys_on_m", ctypes.c_int), ("layout", ctypes.c_int), ("row_slices", ctypes.c_int)]
+
+
+class FrPagedKV(ctypes.Structure):
+    _fields_ = [("opaque", ctypes.c_uint64 * 64)]
+
+
+class FrPagedBatch(ctypes.Structure):
+    _fields_ = [("opaque", ctypes.c_uint64 * 16)]
 
 
 _P = ctypes.c_void_p
@@ -66,6 +79,11 @@ SIGNATURES = {
     "fr_decode_attn_noalloc_check": (_I, [_P]),
     "fr_kv_append": (_I, [_P, _I64, _P, _I64, _P, _I, _I, _RP, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64,
                           _P, _P, _P]),
+    "fr_paged_kv_init": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I]),
+    "fr_paged_batch_init": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I]),
+    "fr_kv_append_paged": (_I, [_P, _P, _I, _P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "fr_paged_attn_workspace_size": (_SZ, [_I, _I, _I]),
+    "fr_paged_attn": (_I, [_P, _P, _P, _I64, _I, _I, _I, _F, _P, _P, _SZ, _P]),
     "fr_decode_attn_plan": (_I, [_I, _I, _I, _I, _I, _SZ, ctypes.POINTER(FrAttnOpts),
                                  ctypes.POINTER(FrAttnPlan)]),
 }

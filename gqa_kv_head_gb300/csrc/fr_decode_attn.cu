@@ -27,6 +27,7 @@
 
 #include "fr_attn.h"
 #include "fr_common.cuh"
+#include "fr_paged.h"
 
 namespace fr {
 
@@ -893,7 +894,8 @@ extern "C" fr_status fr_workspace_check(void* ws, cudaStream_t stream) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return FR_ERR_CUDA;
     if (word == 0) return FR_OK;
     if (cudaMemsetAsync(ws, 0, sizeof(word), stream) != cudaSuccess) return FR_ERR_CUDA;
-    return FR_ERR_DEVICE_TIMEOUT;
+    // the paged calls' bad-input bit; every other bit is a wait that gave up
+    return word & ~paged::kStatusInput ? FR_ERR_DEVICE_TIMEOUT : FR_ERR_DEVICE_INPUT;
 }
 
 extern "C" fr_status fr_decode_attn(const uint16_t* q16, const float* q, int64_t q_tok_stride,

@@ -1,0 +1,329 @@
+// fr_paged.cu -- the paged-cache entry points: descriptors of a cache and of a
+// step's batch, argument checks, the attention's launch choices and the kernel
+// that merges the states of split segments.
+#include <math.h>
+#include <string.h>
+
+#include <cudaTypedefs.h>
+
+#include "fr_paged.h"
+#include "fr_sm100.cuh"
+
+namespace fr {
+namespace paged {
+
+using sm100::ex2;
+
+// The states (m, l, O) of one split segment's row become its output row:
+//   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p,
+// in the order of the pieces, whatever order they were computed in. One block
+// per (segment, row): thread = (4 columns, group of states). Latency-bound: the
+// loads of the first kAhead states of each group go out before the weights are
+// known. Blocks of unsplit segments leave at once.
+constexpr int kAhead = 4;
+
+__global__ void __launch_bounds__(1024)
+paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_split, const float* __restrict__ part_o,
+                   const float2* __restrict__ part_ml, float* __restrict__ out, int row_tile, int hd, int group,
+                   int n_kv_head) {
+    __shared__ float wt[kMaxCtas], red_l[32], red_m[32];
+    __shared__ float4 red[1024];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, row = blockIdx.y;
+    if ((int)blockIdx.x >= *n_split) return;
+    const Split s = split[blockIdx.x];
+    if (s.last < s.first || row >= s.rows) return;
+    const int n = s.last - s.first + 1, cols = hd / 4, groups = blockDim.x / cols, c = tid % cols, gi = tid / cols;
+    auto slot = [&](int p) { return (int64_t)(2 * (s.first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int p = gi + i * groups;
+        ahead[i] = p < n ? *reinterpret_cast<const float4*>(part_o + slot(p) * hd + c * 4) : make_float4(0, 0, 0, 0);
+    }
+    float m = -INFINITY;
+    for (int p = tid; p < n; p += blockDim.x) m = fmaxf(m, part_ml[slot(p)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (lane == 0) red_m[warp] = m;
+    __syncthreads();
+    m = red_m[0];
+    for (int w = 1; w < warps; ++w) m = fmaxf(m, red_m[w]);
+    float l = 0.f;
+    for (int p = tid; p < n; p += blockDim.x) {
+        const float2 ml = part_ml[slot(p)];
+        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+        wt[p] = w;
+        l += w == 0.f ? 0.f : w * ml.y;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    if (lane == 0) red_l[warp] = l;
+    __syncthreads();
+    l = 0.f;
+    for (int w = 0; w < warps; ++w) l += red_l[w];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int p, const float4& y) {
+        const float w = wt[p];
+        if (w == 0.f) return;                   // an empty state may hold anything
+        x.x += w * y.x;
+        x.y += w * y.y;
+        x.z += w * y.z;
+        x.w += w * y.w;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (gi + i * groups < n) add(gi + i * groups, ahead[i]);
+#pragma unroll 8
+    for (int p = gi + kAhead * groups; p < n; p += groups)
+        add(p, *reinterpret_cast<const float4*>(part_o + slot(p) * hd + c * 4));
+    red[tid] = x;
+    __syncthreads();
+    if (gi) return;
+    for (int i = 1; i < groups; ++i) {
+        const float4 y = red[i * cols + c];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+    }
+    const float inv = m == -INFINITY ? 0.f : 1.f / l;
+    const int i = (s.row0 + row) / group, hh = s.row0 + row - i * group;
+    float* dst = out + ((int64_t)(s.tok0 + i) * n_kv_head * group + s.head * group + hh) * hd + c * 4;
+    *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+}
+
+// ---- descriptors ---------------------------------------------------------------
+
+static PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        else
+            (void)cudaGetLastError();
+    }
+    return fn;
+}
+
+// Strides of a [n_pages][n_kv_head][page_size][hd] view: 16-byte multiples, and
+// no two elements at one address (an expanded view would be written twice).
+static bool strides_ok(const int64_t* st, int n_pages, int n_head, int page_size, int hd, int elem) {
+    struct D { int64_t stride; int n; } d[3] = {{st[0], n_pages}, {st[1], n_head}, {st[2], page_size}};
+    for (int i = 0; i < 3; ++i) {
+        if (d[i].n == 1) continue;                 // the stride of a size-1 dimension is never used
+        if (d[i].stride <= 0 || (d[i].stride * elem) % 16 != 0 || d[i].stride > (int64_t{1} << 40) / elem - 1) return false;
+    }
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if ((d[j].n == 1 ? 0 : d[j].stride) < (d[i].n == 1 ? 0 : d[i].stride)) {
+                const D t = d[i];
+                d[i] = d[j];
+                d[j] = t;
+            }
+    int64_t extent = hd;
+    for (int i = 0; i < 3; ++i) {
+        if (d[i].n == 1) continue;
+        if (d[i].stride < extent) return false;
+        extent += d[i].stride * (d[i].n - 1);
+    }
+    return true;
+}
+
+static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, int64_t page, int64_t head, int64_t row) {
+    auto enc = get_encoder();
+    if (!enc) return false;
+    const bool e4 = d.type == FR_KV_E4M3;
+    const int elem = e4 ? 1 : 2, row_bytes = d.hd * elem, box_bytes = row_bytes < 128 ? row_bytes : 128;
+    const cuuint32_t in_box = box_bytes / elem;
+    cuuint64_t dims[5] = {in_box, (cuuint64_t)d.page_size, (cuuint64_t)(row_bytes / box_bytes), (cuuint64_t)d.n_kv_head,
+                          (cuuint64_t)d.n_pages};
+    // the stride of a size-1 dimension is never used, but has to be valid
+    cuuint64_t strides[4] = {(cuuint64_t)row * elem, (cuuint64_t)box_bytes, (cuuint64_t)(d.n_kv_head > 1 ? head * elem : 16),
+                             (cuuint64_t)(d.n_pages > 1 ? page * elem : 16)};
+    cuuint32_t box[5] = {in_box, 16, (cuuint32_t)(row_bytes / box_bytes), 1, 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    CUtensorMap m;
+    if (enc(&m, e4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), dims,
+            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    memcpy(dst, &m, sizeof(m));
+    return true;
+}
+
+static int max_row_tile(int hd) { return hd == 256 ? 16 : 32; }
+static size_t ws_bytes(int hd) {
+    return kWsHeader + sizeof(Split) * kMaxCtas + (size_t)2 * kMaxCtas * max_row_tile(hd) * (sizeof(float2) + 4 * (size_t)hd);
+}
+
+}  // namespace paged
+}  // namespace fr
+
+using namespace fr;
+using namespace fr::paged;
+
+extern "C" fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const int64_t* k_strides, void* v,
+                                      const int64_t* v_strides, float* k_scale, float* v_scale, int n_pages,
+                                      int page_size, int n_kv_head, int hd) {
+    if (!kv || !k || !v || !k_strides || !v_strides) return FR_ERR_INVALID_ARG;
+    memset(kv, 0, sizeof(*kv));
+    if (type != FR_KV_F16 && type != FR_KV_E4M3) return FR_ERR_INVALID_ARG;
+    if (n_pages < 1 || n_kv_head < 1 || page_size < 1 || hd < 1) return FR_ERR_INVALID_ARG;
+    if (hd != 64 && hd != 128 && hd != 256) return FR_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return FR_ERR_UNSUPPORTED;
+    if (n_kv_head > 65535) return FR_ERR_UNSUPPORTED;
+    const bool e4 = type == FR_KV_E4M3;
+    if (e4 ? !k_scale || !v_scale : k_scale || v_scale) return FR_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return FR_ERR_INVALID_ARG;
+    const int elem = e4 ? 1 : 2;
+    if (!strides_ok(k_strides, n_pages, n_kv_head, page_size, hd, elem) ||
+        !strides_ok(v_strides, n_pages, n_kv_head, page_size, hd, elem))
+        return FR_ERR_INVALID_ARG;
+    KvDesc d;
+    memset(&d, 0, sizeof(d));
+    if (cudaGetDevice(&d.dev) != cudaSuccess) return FR_ERR_CUDA;
+    if (!device_ptr_ok(k, d.dev) || !device_ptr_ok(v, d.dev) || (e4 && (!device_ptr_ok(k_scale, d.dev) ||
+                                                                       !device_ptr_ok(v_scale, d.dev))))
+        return FR_ERR_INVALID_ARG;
+    d.k = k;
+    d.v = v;
+    d.k_scale = k_scale;
+    d.v_scale = v_scale;
+    d.k_page = k_strides[0];
+    d.k_head = k_strides[1];
+    d.k_row = k_strides[2];
+    d.v_page = v_strides[0];
+    d.v_head = v_strides[1];
+    d.v_row = v_strides[2];
+    d.n_pages = n_pages;
+    d.page_size = page_size;
+    d.page_shift = __builtin_ctz((unsigned)page_size);
+    d.n_kv_head = n_kv_head;
+    d.hd = hd;
+    d.type = type;
+    d.magic = kKvMagic;
+    if (!encode_pages(d.k_map, d, k, d.k_page, d.k_head, d.k_row) || !encode_pages(d.v_map, d, v, d.v_page, d.v_head, d.v_row))
+        return FR_ERR_CUDA;
+    memcpy(kv, &d, sizeof(d));
+    return FR_OK;
+}
+
+extern "C" fr_status fr_paged_batch_init(fr_paged_batch* batch, const int32_t* tok_start, const int32_t* kv_len,
+                                         const int32_t* page_table, int64_t page_table_stride, int n_seq, int n_tok,
+                                         int max_pages) {
+    if (!batch || !tok_start || !kv_len || !page_table) return FR_ERR_INVALID_ARG;
+    memset(batch, 0, sizeof(*batch));
+    if (n_seq < 1 || n_tok < 1 || max_pages < 1 || page_table_stride < max_pages) return FR_ERR_INVALID_ARG;
+    if (n_seq > kMaxSeq || n_tok > (1 << 20) || max_pages > (1 << 22)) return FR_ERR_UNSUPPORTED;
+    if (((uintptr_t)tok_start | (uintptr_t)kv_len | (uintptr_t)page_table) & 3) return FR_ERR_INVALID_ARG;
+    BatchDesc d;
+    memset(&d, 0, sizeof(d));
+    if (cudaGetDevice(&d.dev) != cudaSuccess) return FR_ERR_CUDA;
+    if (!device_ptr_ok(tok_start, d.dev) || !device_ptr_ok(kv_len, d.dev) || !device_ptr_ok(page_table, d.dev))
+        return FR_ERR_INVALID_ARG;
+    d.tok_start = tok_start;
+    d.kv_len = kv_len;
+    d.table = page_table;
+    d.table_stride = page_table_stride;
+    d.n_seq = n_seq;
+    d.n_tok = n_tok;
+    d.max_pages = max_pages;
+    d.magic = kBatchMagic;
+    memcpy(batch, &d, sizeof(d));
+    return FR_OK;
+}
+
+extern "C" size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd) {
+    if (n_head < 1 || n_kv_head < 1 || n_head % n_kv_head) return 0;
+    if (hd != 64 && hd != 128 && hd != 256) return 0;
+    return ws_bytes(hd);
+}
+
+extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch* batch_, const uint16_t* q16,
+                                   int64_t q_tok_stride, int n_head, int causal, int window, float kq_scale, float* out,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const KvDesc* kv = kv_desc(kv_);
+    const BatchDesc* bt = batch_desc(batch_);
+    if (!kv || !bt || !q16 || !out || !workspace) return FR_ERR_INVALID_ARG;
+    if (n_head < 1 || n_head % kv->n_kv_head) return FR_ERR_INVALID_ARG;
+    if (n_head > (1 << 16)) return FR_ERR_UNSUPPORTED;
+    if (q_tok_stride < (int64_t)n_head * kv->hd || (q_tok_stride & 7)) return FR_ERR_INVALID_ARG;
+    if (window < 0 || (window > 0 && !causal) || !isfinite(kq_scale)) return FR_ERR_INVALID_ARG;
+    if (!aligned16(q16) || !aligned16(out) || !aligned16(workspace)) return FR_ERR_INVALID_ARG;
+    if (((int64_t)bt->max_pages << kv->page_shift) > 0x7fff0000) return FR_ERR_UNSUPPORTED;
+    if (workspace_bytes < ws_bytes(kv->hd)) return FR_ERR_WORKSPACE;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FR_ERR_CUDA;
+    if (dev != kv->dev || dev != bt->dev) return FR_ERR_INVALID_ARG;
+    if (!device_ptr_ok(q16, dev) || !device_ptr_ok(out, dev) || !device_ptr_ok(workspace, dev)) return FR_ERR_INVALID_ARG;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return FR_ERR_CUDA;
+
+    const int G = n_head / kv->n_kv_head;
+    // Row tile: 8 rows for each MMA column block, as many blocks as an average
+    // sequence of the batch fills (a longer one takes several row tiles)
+    const int64_t avg = (int64_t)G * ((bt->n_tok + bt->n_seq - 1) / bt->n_seq);
+    const int nt = avg <= 8 ? 1 : avg <= 16 || kv->hd == 256 ? 2 : 4;
+    const int rt = 8 * nt;
+    // at most this many segments, and units of work, whatever the lengths say
+    const int64_t per_tok = (int64_t)bt->n_tok * ((G + rt - 1) / rt), per_seq = bt->n_seq + (int64_t)bt->n_tok * G / rt;
+    const int64_t segs = (per_tok < per_seq ? per_tok : per_seq) * kv->n_kv_head;
+    const int64_t cap_units = (((int64_t)bt->max_pages << kv->page_shift) + kUnit - 1) / kUnit;
+    int64_t ctas = (int64_t)kCtasPerSm * sms;
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    if (segs * cap_units < ctas) ctas = segs * cap_units;
+
+    char* w = reinterpret_cast<char*>(workspace);
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q16 = reinterpret_cast<const __half*>(q16);
+    a.q_stride = q_tok_stride;
+    a.out = out;
+    a.tok_start = bt->tok_start;
+    a.kv_len = bt->kv_len;
+    a.table = bt->table;
+    a.table_stride = bt->table_stride;
+    a.k_scale = kv->k_scale;
+    a.v_scale = kv->v_scale;
+    a.status = reinterpret_cast<unsigned*>(w);
+    a.n_split = reinterpret_cast<int*>(w + 64);
+    a.split = reinterpret_cast<Split*>(w + kWsHeader);
+    a.part_ml = reinterpret_cast<float2*>(w + kWsHeader + sizeof(Split) * kMaxCtas);
+    a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * kMaxCtas * max_row_tile(kv->hd));
+    a.n_seq = bt->n_seq;
+    a.n_tok = bt->n_tok;
+    a.max_pages = bt->max_pages;
+    a.n_pages = kv->n_pages;
+    a.page_shift = kv->page_shift;
+    a.n_kv_head = kv->n_kv_head;
+    a.group = G;
+    a.causal = causal ? 1 : 0;
+    a.window = window;
+    a.split_by_segment = segs <= ctas ? 1 : 0;
+    a.scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
+    const fr_status st = kv->type == FR_KV_E4M3 ? launch_attn_e4m3(*kv, a, nt, (int)ctas, stream)
+                                                : launch_attn_f16(*kv, a, nt, (int)ctas, stream);
+    if (st != FR_OK) return st;
+
+    const int64_t rows = (int64_t)G * bt->n_tok < rt ? (int64_t)G * bt->n_tok : rt;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(a.split_by_segment ? segs : ctas), (unsigned)rows);
+    // few segments: each has many states, read by 1024 threads; many: few states each
+    cfg.blockDim = dim3(a.split_by_segment ? 1024 : 256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_merge_kernel, (const Split*)a.split, (const int*)a.n_split,
+                                             (const float*)a.part_o, (const float2*)a.part_ml, out, rt, kv->hd, G,
+                                             kv->n_kv_head);
+    return e == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+}

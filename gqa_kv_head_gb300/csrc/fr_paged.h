@@ -1,0 +1,103 @@
+// fr_paged.h -- host-side pieces shared by the paged-cache entry points
+// (fr_paged.cu: descriptors, checks and the merge kernel; fr_paged_append.cu:
+// the append; fr_paged_attn_*.cu: the attention kernels).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fr_common.cuh"
+
+namespace fr {
+namespace paged {
+
+constexpr int kWarps = 4;            // warps per attention CTA
+constexpr int kTile = 16;            // keys per warp tile (the MMA's M)
+constexpr int kUnit = kWarps * kTile;  // keys of one unit of work: a tile for each warp
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 320;        // attention CTAs at most: the workspace holds two split states for each
+constexpr int kMaxRowTile = 32;      // query rows of one row tile at most
+constexpr int kMaxSeq = 65536;
+constexpr size_t kWsHeader = 1024;   // [0, 4): status word, as in the other workspaces
+
+// What fr_paged_kv holds, in the library's own terms.
+struct KvDesc {
+    // 5-D CUtensorMap bytes (dim in box, row, box, head, page) of the attention's
+    // tile loads; copied to an aligned place at the launch
+    unsigned char k_map[sizeof(CUtensorMap)], v_map[sizeof(CUtensorMap)];
+    void *k, *v;
+    float *k_scale, *v_scale;        // e4m3: [n_pages][n_kv_head]
+    int64_t k_page, k_head, k_row;   // strides in elements
+    int64_t v_page, v_head, v_row;
+    int n_pages, page_size, page_shift, n_kv_head, hd, type, dev;
+    uint32_t magic;
+};
+struct BatchDesc {
+    const int32_t *tok_start, *kv_len, *table;
+    int64_t table_stride;
+    int n_seq, n_tok, max_pages, dev;
+    uint32_t magic;
+};
+constexpr uint32_t kKvMagic = 0x46525056u, kBatchMagic = 0x46525042u;
+static_assert(sizeof(KvDesc) <= sizeof(fr_paged_kv), "fr_paged_kv is too small");
+static_assert(sizeof(BatchDesc) <= sizeof(fr_paged_batch), "fr_paged_batch is too small");
+
+// One segment whose keys went to several CTAs: the merge kernel's work item.
+struct alignas(16) Split {
+    int first, last;                 // CTAs with a state of it (last < first: nothing to merge)
+    int tok0, row0, rows, head;      // query rows row0 .. row0 + rows - 1 of KV head `head`, first token tok0
+    int pad[2];
+};
+
+struct AttnArgs {
+    const __half* q16;
+    int64_t q_stride;
+    float* out;
+    const int32_t *tok_start, *kv_len, *table;
+    int64_t table_stride;
+    const float *k_scale, *v_scale;
+    float* part_o;                   // [2 * CTAs][row tile][hd]: unnormalised sums
+    float2* part_ml;                 // [2 * CTAs][row tile]: reference maximum (log2 units), sum of weights
+    Split* split;                    // [kMaxCtas]
+    int* n_split;                    // entries of it that the call wrote
+    unsigned* status;
+    int n_seq, n_tok, max_pages, n_pages, page_shift, n_kv_head, group, causal, window;
+    int split_by_segment;            // split[] is indexed by the segment's number, else by its first CTA
+    float scale_log2;                // kq_scale * log2(e)
+};
+
+// Sizes of one sequence, bad input cut to what memory holds.
+struct SeqInfo {
+    int tok0, n_q, n_kv;
+    bool bad;
+};
+__device__ __forceinline__ SeqInfo seq_info(const int32_t* tok_start, const int32_t* kv_len, int b, int n_tok,
+                                            int max_pages, int page_shift) {
+    SeqInfo s;
+    const int t0 = __ldg(tok_start + b), t1 = __ldg(tok_start + b + 1), n = __ldg(kv_len + b);
+    const int64_t most = (int64_t)max_pages << page_shift;
+    s.bad = t0 < 0 || t1 < t0 || t1 > n_tok || n < 0 || n > most;
+    s.tok0 = t0;
+    s.n_q = s.bad ? 0 : t1 - t0;
+    s.n_kv = s.bad ? 0 : n;
+    return s;
+}
+
+// bits of a workspace's status word (1, 2 and 4 are waits that gave up)
+constexpr unsigned kStatusTimeout = 1u, kStatusInput = 0x100u;
+
+fr_status launch_attn_f16(const KvDesc& kv, const AttnArgs& a, int row_tiles8, int ctas, cudaStream_t st);
+fr_status launch_attn_e4m3(const KvDesc& kv, const AttnArgs& a, int row_tiles8, int ctas, cudaStream_t st);
+// Pointer checks shared by the entry points.
+inline const KvDesc* kv_desc(const fr_paged_kv* p) {
+    const KvDesc* d = reinterpret_cast<const KvDesc*>(p);
+    return p && d->magic == kKvMagic ? d : nullptr;
+}
+inline const BatchDesc* batch_desc(const fr_paged_batch* p) {
+    const BatchDesc* d = reinterpret_cast<const BatchDesc*>(p);
+    return p && d->magic == kBatchMagic ? d : nullptr;
+}
+
+}  // namespace paged
+}  // namespace fr

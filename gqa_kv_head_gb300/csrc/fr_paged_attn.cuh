@@ -1,0 +1,826 @@
+// fr_paged_attn.cuh -- attention of a step's query rows over a paged K/V cache
+// (f16 pages, or e4m3 pages with a scale for each page and head).
+//
+// For a sequence's KV head, the G query heads that share it and the sequence's
+// n_q new tokens give rows r = i*G + g. With x_rj = scale * <q_r, k_j> in log2
+// units, masked keys at -inf,
+//   out_r = sum_j 2^(x_rj - m_r) v_j / sum_j 2^(x_rj - m_r)
+// in one pass over the keys with a running reference m_r.
+//
+// Few rows and many keys: bound by the bytes of K and V. Keys are the MMA's M
+// and query rows its N (S^T = K Q^T, O^T = V^T P^T by mma.sync m16n8k16), so a
+// K or V element enters one MMA for up to 8 rows, and every warp works alone
+// on 16-key tiles: its own ring of TMA-filled slots, its own running state, no
+// block barrier until a piece of a sequence ends. mma.sync and not tcgen05:
+// the rows of a decode step fill N = 8..32, the tensor time is a fraction of
+// the load time either way, and S^T and P^T stay in the registers of one warp
+// where a tcgen05 kernel passes them through TMEM and shared memory and
+// synchronises the CTA on every tile.
+//
+// Work split: the keys of all (sequence, KV head, row tile) segments form one
+// list of 64-key units; each CTA (two per SM) takes an equal contiguous share
+// of it, read from kv_len on the device, so uneven lengths balance and a
+// captured graph follows the lengths. A segment inside one CTA is normalised
+// and written there; one cut by a share's end leaves (m, l, O) states in the
+// workspace for the merge kernel (fr_paged.cu).
+//
+// P enters the PV product as two f16 terms P_hi + P_lo (22 bits), scaled by
+// 2^7 to keep P_lo off f16's subnormals: the result carries fp32 accuracy like
+// fr_decode_attn's. e4m3 codes become f16 in registers, which is exact; K's
+// scale joins the score's factor, V's scale the weights, relative to the
+// largest V scale met so far (the same kind of running reference as m).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <string.h>
+
+#include "fr_paged.h"
+#include "fr_sm100.cuh"
+
+namespace fr {
+namespace paged {
+
+using namespace sm100;
+
+constexpr float kTau = 8.0f;           // a reference maximum moves when a score exceeds it by 2^8
+constexpr float kPShift = 7.0f;        // weights are held times 2^7: at most 2^15 in f16
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int head, int page,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+        "[%7];"
+        :: "r"(dst), "l"((uint64_t)map), "r"(0), "r"(row), "r"(0), "r"(head), "r"(page), "r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// Two e4m3 codes (the low or the high half of x) as f16x2, exact.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+    uint32_t y;
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, a; }" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+    uint32_t y;
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, b; }" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int HD, int TYPE, int NT>
+struct Cfg {
+    static constexpr bool E4 = TYPE == FR_KV_E4M3;
+    static constexpr int RT = 8 * NT;                       // query rows of a row tile
+    static constexpr int ROWB = HD * (E4 ? 1 : 2);          // bytes of a K or V row
+    static constexpr int PITCH = ROWB < 128 ? ROWB : 128;   // bytes of a row in one box
+    static constexpr int BOXES = ROWB / PITCH;
+    static constexpr int SLOT = kTile * ROWB;
+    static constexpr int MT = HD / 16;                      // 16-dim blocks of O^T, and k steps of S^T
+    // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
+    static constexpr bool QREG = HD * NT <= 256;
+    static constexpr int QPITCH = HD * 2 + (E4 ? 32 : 16);  // bytes: rows on different banks
+    static constexpr int QBYTES = QREG ? 0 : RT * QPITCH;
+    // dims of O that the warps' states are added over at a time
+    static constexpr int CD = HD * NT >= 512 ? 16 : HD * NT >= 256 ? 32 : 64;
+    static constexpr int RED = kWarps * RT * (CD + 4) * 4;
+    static constexpr int STATE = kWarps * RT * 8;
+    // alignment slack, buffers above, then tile entries, barriers and the scan's words
+    static constexpr int FIXED = 1024 + RED + QBYTES + STATE + kWarps * (256 + 128) + 128;
+    static constexpr int NS_ = (115712 - FIXED) / (kWarps * SLOT);
+    static constexpr int NS = NS_ > 16 ? 16 : NS_;          // slots of a warp's ring
+    static constexpr int SMEM = FIXED + NS * kWarps * SLOT;
+    static_assert(NS >= 3, "ring");
+    static_assert(SMEM <= 115712, "two CTAs per SM");
+};
+
+// One (sequence, KV head, row tile): its rows, and its keys as 16-key tiles.
+struct Seg {
+    int b, h, rt, n_rt;
+    int tok0, n_q, n_kv;
+    int tile0, n_tiles, n_units;
+};
+
+template <int RT>
+__device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
+    const int r0 = s.rt * RT, r1 = min(s.n_q * a.group, r0 + RT) - 1;
+    int hi = s.n_kv, lo = 0;
+    if (a.causal) {
+        const int first = s.n_kv - s.n_q;
+        hi = min(hi, first + r1 / a.group + 1);
+        if (a.window > 0) lo = max(0, first + r0 / a.group - a.window + 1);
+    }
+    s.tile0 = lo / kTile;
+    s.n_tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
+    s.n_units = max(1, (s.n_tiles + kWarps - 1) / kWarps);   // rows without keys still get their zeros
+}
+template <int RT>
+__device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
+    const SeqInfo q = seq_info(a.tok_start, a.kv_len, b, a.n_tok, a.max_pages, a.page_shift);
+    s.b = b;
+    s.tok0 = q.tok0;
+    s.n_q = q.n_q;
+    s.n_kv = q.n_kv;
+    s.n_rt = (q.n_q * a.group + RT - 1) / RT;
+    return q.bad;
+}
+// The next segment in order (row tile fastest, then KV head, then sequence).
+template <int RT>
+__device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
+    if (++s.rt == s.n_rt) {
+        s.rt = 0;
+        if (++s.h == a.n_kv_head) {
+            s.h = 0;
+            int b = s.b;
+            do {
+                if (++b >= a.n_seq) return;
+                seg_seq<RT>(s, a, b);
+            } while (s.n_rt == 0);
+        }
+    }
+    seg_keys<RT>(s, a);
+}
+// Units of all segments of sequence b for one KV head.
+template <int RT>
+__device__ __forceinline__ int64_t seq_units(const AttnArgs& a, int b, int& n_rt, bool& bad) {
+    Seg s;
+    bad = seg_seq<RT>(s, a, b);
+    n_rt = s.n_rt;
+    int64_t u = 0;
+    for (s.rt = 0; s.rt < s.n_rt; ++s.rt) {
+        seg_keys<RT>(s, a);
+        u += s.n_units;
+    }
+    return u;
+}
+
+// A walk over a CTA's share of the units: the pieces of segments it holds, and
+// inside a piece the tiles of one warp.
+template <int RT>
+struct Walk {
+    Seg s;
+    int64_t left;       // units of the share from this piece on
+    int ua, ub;         // this piece's units within the segment
+    int t, t_end;       // the warp's next tile of the segment, and the piece's end
+    __device__ __forceinline__ void piece(int warp) {
+        ub = (int)min((int64_t)s.n_units, ua + left);
+        t = ua * kWarps + warp;
+        t_end = min(ub * kWarps, s.n_tiles);
+    }
+    // on to the next piece; false at the share's end
+    __device__ __forceinline__ bool next(const AttnArgs& a, int warp) {
+        left -= ub - ua;
+        if (left <= 0) return false;
+        seg_next<RT>(s, a);
+        ua = 0;
+        piece(warp);
+        return true;
+    }
+};
+
+template <int HD, int TYPE, int NT>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using C = Cfg<HD, TYPE, NT>;
+    constexpr int RT = C::RT, MT = C::MT, NS = C::NS;
+    constexpr bool E4 = C::E4;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    unsigned char* ring = base + warp * NS * C::SLOT;
+    unsigned char* after = base + kWarps * NS * C::SLOT;
+    float* red = reinterpret_cast<float*>(after);                                       // [warp][RT][CD + 4]
+    unsigned char* q_sm = after + C::RED;                                               // [RT][QPITCH]
+    float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);                        // [warp][RT]
+    float4* meta = reinterpret_cast<float4*>(q_sm + C::QBYTES + C::STATE) + warp * 16;  // k scale, v scale, bad
+    uint64_t* bars = reinterpret_cast<uint64_t*>(q_sm + C::QBYTES + C::STATE + kWarps * 256) + warp * 16;
+    int64_t* scan = reinterpret_cast<int64_t*>(q_sm + C::QBYTES + C::STATE + kWarps * 384);   // [16]
+    const uint32_t ring_u = smem_addr(ring), bars_u = smem_addr(bars);
+
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(bars_u + 8 * i, 1);
+        mbar_fence_init();
+        if (warp == 0) {
+            prefetch_tmap(&k_map);
+            prefetch_tmap(&v_map);
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- this CTA's share of the units ------------------------------------
+    const int cta = blockIdx.x;
+    int64_t mine = 0;
+    int mine_s = 0;              // segments
+    bool bad_any = false;
+    for (int b = tid; b < a.n_seq; b += kWarps * 32) {
+        int n_rt;
+        bool bad;
+        mine += seq_units<RT>(a, b, n_rt, bad);
+        mine_s += n_rt;
+        bad_any |= bad;
+    }
+    if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        mine += __shfl_xor_sync(~0u, mine, o);
+        mine_s += __shfl_xor_sync(~0u, mine_s, o);
+    }
+    if (lane == 0) {
+        scan[warp] = mine;
+        scan[4 + warp] = mine_s;
+    }
+    __syncthreads();
+    const int64_t total = (scan[0] + scan[1] + scan[2] + scan[3]) * a.n_kv_head;
+    const int64_t n_cta = min((int64_t)gridDim.x, total);
+    if (cta == 0 && tid == 0)    // entries of split[] that this call writes
+        *a.n_split = (int)min((int64_t)kMaxCtas, a.split_by_segment ?
+                              (scan[4] + scan[5] + scan[6] + scan[7]) * a.n_kv_head : n_cta);
+    if (cta >= n_cta) return;
+    const int64_t u0 = total * cta / n_cta, u1 = total * (cta + 1) / n_cta;
+    Walk<RT> cw;                 // what is consumed
+    int seg_no = 0;              // the segment's number in the whole list
+    int64_t base_u = 0;
+    int base_seg = 0;
+    for (int b0 = 0;; b0 += kWarps * 32) {
+        const int b = b0 + tid;
+        int n_rt = 0;
+        bool bad;
+        const int64_t u = b < a.n_seq ? seq_units<RT>(a, b, n_rt, bad) * a.n_kv_head : 0;
+        int64_t inc = u;
+        int inc_s = n_rt * a.n_kv_head;
+        const int own_s = inc_s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, inc, o);
+            const int y = __shfl_up_sync(~0u, inc_s, o);
+            if (lane >= o) {
+                inc += x;
+                inc_s += y;
+            }
+        }
+        __syncthreads();
+        if (lane == 31) {
+            scan[warp] = inc;
+            scan[4 + warp] = inc_s;
+        }
+        __syncthreads();
+        int64_t off = base_u;
+        int off_s = base_seg;
+        for (int w = 0; w < warp; ++w) {
+            off += scan[w];
+            off_s += (int)scan[4 + w];
+        }
+        inc += off;
+        inc_s += off_s;
+        if (u > 0 && u0 >= inc - u && u0 < inc) {
+            scan[8] = b;
+            scan[9] = u0 - (inc - u);
+            scan[10] = inc_s - own_s;
+        }
+        base_u += scan[0] + scan[1] + scan[2] + scan[3];
+        base_seg += (int)(scan[4] + scan[5] + scan[6] + scan[7]);
+        __syncthreads();
+        if (u0 < base_u) break;
+    }
+    {
+        int64_t rem = scan[9];
+        int n_rt;
+        bool bad;
+        const int b = (int)scan[8];
+        const int64_t per_head = seq_units<RT>(a, b, n_rt, bad);
+        seg_seq<RT>(cw.s, a, b);
+        cw.s.h = (int)(rem / per_head);
+        rem -= cw.s.h * per_head;
+        for (cw.s.rt = 0;; ++cw.s.rt) {
+            seg_keys<RT>(cw.s, a);
+            if (rem < cw.s.n_units) break;
+            rem -= cw.s.n_units;
+        }
+        seg_no = (int)scan[10] + cw.s.h * n_rt + cw.s.rt;
+        cw.ua = (int)rem;
+        cw.left = u1 - u0;
+        cw.piece(warp);
+    }
+
+    // ---- the warp's ring: slots q = 0, 1, ... hold K, V, K, V, ... of its tiles ----
+    Walk<RT> pw = cw;            // what is requested
+    bool more = true;
+    int blk = 32;                // entries of the page block used up (32: load a new one)
+    int b_page = 0, p_page = 0, p_row = 0;
+    float b_ks = 1.f, b_vs = 1.f;
+    int i_slot = 0, i_tile = 0;  // ring slot of the next request; its tile's number mod 16
+    bool i_v = false;
+    auto request = [&]() {
+        if (!more) return;
+        if (!i_v) {              // a new tile: its page, and its scales for the consumer
+            while (pw.t >= pw.t_end) {
+                if (!pw.next(a, warp)) {
+                    more = false;
+                    return;
+                }
+                blk = 32;
+            }
+            const int tile = pw.s.tile0 + pw.t;
+            if (blk == 32) {
+                const int tl = pw.t + lane * kWarps;
+                b_page = 0;
+                if (tl < pw.t_end) {
+                    const int idx = (pw.s.tile0 + tl) >> (a.page_shift - 4);
+                    b_page = __ldg(a.table + pw.s.b * a.table_stride + idx);
+                    if (b_page < 0 || b_page >= a.n_pages) {
+                        b_page = -1;
+                        atomicOr(a.status, kStatusInput);
+                        b_ks = b_vs = 0.f;
+                    } else if (E4) {
+                        b_ks = __ldg(a.k_scale + (int64_t)b_page * a.n_kv_head + pw.s.h);
+                        b_vs = __ldg(a.v_scale + (int64_t)b_page * a.n_kv_head + pw.s.h);
+                    }
+                }
+                blk = 0;
+            }
+            p_page = __shfl_sync(~0u, b_page, blk);
+            p_row = (tile << 4) & ((1 << a.page_shift) - 1);
+            const float ks = E4 ? __shfl_sync(~0u, b_ks, blk) : 1.f, vs = E4 ? __shfl_sync(~0u, b_vs, blk) : 1.f;
+            ++blk;
+            if (lane == 0) meta[i_tile] = make_float4(ks, vs, p_page < 0 ? 1.f : 0.f, 0.f);
+        }
+        if (lane == 0) {
+            const uint32_t bar = bars_u + 8 * i_slot;
+            mbar_expect_tx(bar, C::SLOT);
+            // a bad page reads page 0, which exists; its keys are masked
+            tma_load_5d(ring_u + i_slot * C::SLOT, i_v ? &v_map : &k_map, p_row, pw.s.h, max(p_page, 0), bar);
+        }
+        if (++i_slot == NS) i_slot = 0;
+        if (i_v) {
+            pw.t += kWarps;
+            i_tile = (i_tile + 1) & 15;
+        }
+        i_v = !i_v;
+    };
+    __syncwarp();
+    for (int i = 0; i < NS; ++i) request();
+    __syncwarp();                // the tile entries above are read by the whole warp
+
+    int c_slot = 0, c_tile = 0;
+    uint32_t c_phase = 0;
+    bool timeout = false;
+    auto wait_slot = [&]() {
+        // after one wait that gave up the others do so soon: the kernel ends
+        if (!mbar_wait(bars_u + 8 * c_slot, c_phase, timeout ? 20000ull : kWaitNs)) timeout = true;
+    };
+    auto pass_slot = [&]() {     // this slot is used up: request what comes NS slots later
+        __syncwarp();
+        request();
+        if (++c_slot == NS) {
+            c_slot = 0;
+            c_phase ^= 1;
+        }
+    };
+
+    // shared-memory address of 16-byte chunk c of row r in a slot (the TMA's swizzle)
+    auto chunk = [](uint32_t slot, int r, int c) -> uint32_t {
+        if (C::PITCH == 128) return slot + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        return slot + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    };
+
+    for (;;) {
+        // ---- a piece: its rows, their views and their Q fragments -----------
+        const int rows = min(RT, cw.s.n_q * a.group - cw.s.rt * RT), row0 = cw.s.rt * RT;
+        int lim[NT][2], low[NT][2];
+        int min_lim = 0x7fffffff, max_low = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = n * 8 + 2 * t4 + e;
+                lim[n][e] = cw.s.n_kv;
+                low[n][e] = 0;
+                if (r < rows && a.causal) {
+                    const int p = cw.s.n_kv - cw.s.n_q + (row0 + r) / a.group;   // the key of the row's own token
+                    lim[n][e] = min(lim[n][e], p + 1);
+                    if (a.window > 0) low[n][e] = max(0, p + 1 - a.window);
+                }
+                min_lim = min(min_lim, lim[n][e]);
+                max_low = max(max_low, low[n][e]);
+            }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            min_lim = min(min_lim, __shfl_xor_sync(~0u, min_lim, o));
+            max_low = max(max_low, __shfl_xor_sync(~0u, max_low, o));
+        }
+        auto q_row = [&](int r) {
+            const int i = (row0 + r) / a.group, hh = (row0 + r) - i * a.group;
+            return a.q16 + (int64_t)(cw.s.tok0 + i) * a.q_stride + (int64_t)(cw.s.h * a.group + hh) * HD;
+        };
+        uint32_t qf[C::QREG ? MT : 1][NT][2];
+        if (C::QREG) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int r = n * 8 + g;
+                const __half* src = q_row(min(r, rows - 1));
+#pragma unroll
+                for (int kk = 0; kk < MT; ++kk) {
+                    if (E4) {
+                        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + kk * 16 + 4 * t4));
+                        qf[kk][n][0] = r < rows ? x.x : 0u;
+                        qf[kk][n][1] = r < rows ? x.y : 0u;
+                    } else {
+                        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * t4));
+                        const uint32_t y = __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * t4));
+                        qf[kk][n][0] = r < rows ? x : 0u;
+                        qf[kk][n][1] = r < rows ? y : 0u;
+                    }
+                }
+            }
+        } else {
+            for (int w = tid; w < RT * (HD / 8); w += kWarps * 32) {
+                const int r = w / (HD / 8), c = w - r * (HD / 8);
+                const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4*>(q_row(r) + c * 8)) : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(q_sm + r * C::QPITCH + c * 16) = x;
+            }
+            __syncthreads();
+        }
+        auto q_frag = [&](int kk, int n, uint32_t& b0, uint32_t& b1) {
+            if (C::QREG) {
+                b0 = qf[kk][n][0];
+                b1 = qf[kk][n][1];
+            } else {
+                const unsigned char* src = q_sm + (n * 8 + g) * C::QPITCH + kk * 32;
+                if (E4) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(src + t4 * 8);
+                    b0 = x.x;
+                    b1 = x.y;
+                } else {
+                    b0 = *reinterpret_cast<const uint32_t*>(src + t4 * 4);
+                    b1 = *reinterpret_cast<const uint32_t*>(src + 16 + t4 * 4);
+                }
+            }
+        };
+
+        float o[MT][NT][4];
+        float mref[NT][2], l[NT][2];
+        float vref = 0.f;                            // largest V scale so far
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            mref[n][0] = mref[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
+        }
+
+        for (; cw.t < cw.t_end; cw.t += kWarps) {
+            // ---- S^T = K Q^T ------------------------------------------------
+            wait_slot();
+            const float4 mt_ = meta[c_tile];
+            uint32_t slot = ring_u + c_slot * C::SLOT;
+            float s[NT][4], s2[NT][4];               // two chains of MMAs
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
+            if (E4) {
+#pragma unroll
+                for (int kk = 0; kk < MT; kk += 2) {
+                    uint32_t r0, r1, r2, r3;
+                    ldsm_x4(chunk(slot, (lane & 7) + ((lane >> 3) & 1) * 8, kk + (lane >> 4)), r0, r1, r2, r3);
+                    const uint32_t a0[4] = {e4m3_lo(r0), e4m3_lo(r1), e4m3_hi(r0), e4m3_hi(r1)};
+                    const uint32_t a1[4] = {e4m3_lo(r2), e4m3_lo(r3), e4m3_hi(r2), e4m3_hi(r3)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t b0, b1;
+                        q_frag(kk, n, b0, b1);
+                        mma_16816(s[n], a0, b0, b1);
+                        q_frag(kk + 1, n, b0, b1);
+                        mma_16816(s2[n], a1, b0, b1);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < MT; ++kk) {
+                    uint32_t af[4];
+                    ldsm_x4(chunk(slot, (lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)), af[0], af[1], af[2],
+                            af[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t b0, b1;
+                        q_frag(kk, n, b0, b1);
+                        mma_16816(kk & 1 ? s2[n] : s[n], af, b0, b1);
+                    }
+                }
+            }
+            pass_slot();
+
+            // ---- softmax weights ---------------------------------------------
+            const int key0 = (cw.s.tile0 + cw.t) * kTile;
+            const bool bad = mt_.z != 0.f;
+            const bool edge = bad || key0 + kTile > min_lim || key0 < max_low;
+            const float sc = a.scale_log2 * mt_.x;
+            bool up = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = (s[n][e] + s2[n][e]) * sc;
+                    if (edge) {
+                        const int j = key0 + g + (e >> 1) * 8;
+                        if (bad || j >= lim[n][e & 1] || j < low[n][e & 1]) x = -INFINITY;
+                    }
+                    s[n][e] = x;
+                    up |= x > mref[n][e & 1] + kTau;
+                }
+            float vs = 1.f;                          // this tile's V scale over vref
+            const bool vup = E4 && fabsf(mt_.y) > vref;
+            if (__any_sync(~0u, up) || vup) {
+                float va = 1.f;
+                if (vup) {
+                    va = vref / fabsf(mt_.y);
+                    vref = fabsf(mt_.y);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float al[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(s[n][e], s[n][e + 2]);
+#pragma unroll
+                        for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
+                        m = fmaxf(m, mref[n][e]);
+                        al[e] = m == -INFINITY ? 1.f : ex2(mref[n][e] - m);
+                        mref[n][e] = m;
+                        l[n][e] *= al[e];
+                        al[e] *= va;
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        o[m][n][0] *= al[0];
+                        o[m][n][1] *= al[1];
+                        o[m][n][2] *= al[0];
+                        o[m][n][3] *= al[1];
+                    }
+                }
+            }
+            if (E4) vs = mt_.y == 0.f ? 0.f : mt_.y / vref;
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float m = mref[n][e & 1];
+                    const float p = ex2(s[n][e] - (m == -INFINITY ? 0.f : m) + kPShift);
+                    l[n][e & 1] += p;
+                    w[e] = E4 ? p * vs : p;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const __half2 h = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
+                    const float2 hf = __half22float2(h);
+                    ph[n][e] = movm(*reinterpret_cast<const uint32_t*>(&h));
+                    pl[n][e] = movm(pack_half2(w[2 * e] - hf.x, w[2 * e + 1] - hf.y));
+                }
+            }
+
+            // ---- O^T += V^T P^T ------------------------------------------------
+            wait_slot();
+            slot = ring_u + c_slot * C::SLOT;
+            if (edge) {
+                // A masked key has weight 0, but 0 * inf and 0 * NaN are NaN: rows
+                // of V that no query row sees are cleared (they may lie behind the
+                // sequence's end), and non-finite rows seen by some rows only are
+                // added here for those rows and then cleared.
+                unsigned seen[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    bool any = false;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            any |= n * 8 + 2 * t4 + c < rows && s[n][2 * e + c] != -INFINITY;
+                    seen[e] = __ballot_sync(~0u, any);
+                }
+                unsigned char* sp = ring + c_slot * C::SLOT;
+                for (int j = 0; j < kTile; ++j) {
+                    const bool dead = ((seen[j >> 3] >> (4 * (j & 7))) & 15u) == 0u;
+                    bool weird = false;
+                    if (!dead) {
+                        for (int c = lane; c < C::ROWB / 4; c += 32) {
+                            const uint32_t x = *reinterpret_cast<const uint32_t*>(sp + (c * 4) / C::PITCH * (kTile * C::PITCH) +
+                                                                                  j * C::PITCH + (c * 4) % C::PITCH);
+                            if (E4) {
+                                const uint32_t y = x & 0x7f7f7f7fu;
+                                weird |= (y & 0xffu) == 0x7fu || (y >> 8 & 0xffu) == 0x7fu || (y >> 16 & 0xffu) == 0x7fu ||
+                                         y >> 24 == 0x7fu;
+                            } else {
+                                weird |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
+                            }
+                        }
+                        weird = __any_sync(~0u, weird);
+                    }
+                    if (weird) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float x = __shfl_sync(~0u, j < 8 ? s[n][c] : s[n][2 + c], (j & 7) * 4 + t4);
+                                if (x == -INFINITY) continue;
+                                const float m = mref[n][c];
+                                const float p = ex2(x - (m == -INFINITY ? 0.f : m) + kPShift) * vs;
+#pragma unroll
+                                for (int m2 = 0; m2 < MT; ++m2)
+#pragma unroll
+                                    for (int u = 0; u < 2; ++u) {
+                                        const int d = m2 * 16 + (E4 ? 2 * g + u : g + 8 * u), by = d * (E4 ? 1 : 2);
+                                        const unsigned char* e = ring + (chunk(slot, j, by >> 4) - ring_u) + (by & 15);
+                                        float v;
+                                        if (E4) {
+                                            const uint32_t hv = e4m3_lo(*e);
+                                            v = __half2float(__ushort_as_half((unsigned short)hv));
+                                        } else {
+                                            v = __half2float(*reinterpret_cast<const __half*>(e));
+                                        }
+                                        o[m2][n][2 * u + c] += p * v;
+                                    }
+                            }
+                    }
+                    __syncwarp();
+                    if (dead || weird)
+                        for (int c = lane; c < C::ROWB / 4; c += 32)
+                            *reinterpret_cast<uint32_t*>(sp + (c * 4) / C::PITCH * (kTile * C::PITCH) + j * C::PITCH +
+                                                         (c * 4) % C::PITCH) = 0u;
+                }
+                fence_proxy_async_cta();             // the slot's next fill comes by TMA
+                __syncwarp();
+            }
+            if (E4) {
+#pragma unroll
+                for (int m = 0; m < MT; m += 2) {
+                    uint32_t r0, r1, r2, r3;
+                    ldsm_x4_t(chunk(slot, (lane & 7) + ((lane >> 3) & 1) * 8, m + (lane >> 4)), r0, r1, r2, r3);
+                    r0 = __byte_perm(r0, 0, 0x3120);
+                    r1 = __byte_perm(r1, 0, 0x3120);
+                    r2 = __byte_perm(r2, 0, 0x3120);
+                    r3 = __byte_perm(r3, 0, 0x3120);
+                    const uint32_t a0[4] = {e4m3_lo(r0), e4m3_hi(r0), e4m3_lo(r1), e4m3_hi(r1)};
+                    const uint32_t a1[4] = {e4m3_lo(r2), e4m3_hi(r2), e4m3_lo(r3), e4m3_hi(r3)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_16816(o[m][n], a0, ph[n][0], ph[n][1]);
+                        mma_16816(o[m + 1][n], a1, ph[n][0], ph[n][1]);
+                        mma_16816(o[m][n], a0, pl[n][0], pl[n][1]);
+                        mma_16816(o[m + 1][n], a1, pl[n][0], pl[n][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t af[4];
+                    ldsm_x4_t(chunk(slot, (lane & 7) + (lane >> 4) * 8, 2 * m + ((lane >> 3) & 1)), af[0], af[1], af[2],
+                              af[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16816(o[m][n], af, ph[n][0], ph[n][1]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16816(o[m][n], af, pl[n][0], pl[n][1]);
+                }
+            }
+            pass_slot();
+            c_tile = (c_tile + 1) & 15;
+        }
+
+        // ---- the piece's end: the four warps' states become one ---------------
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], w);
+                // only NaN scores so far: a state all the same, so that they reach the result
+                if (mref[n][e] == -INFINITY && !(l[n][e] == 0.f)) mref[n][e] = 0.f;
+                if (g == 0) state[warp * RT + n * 8 + 2 * t4 + e] = make_float2(mref[n][e], l[n][e]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, state[w * RT + n * 8 + 2 * t4 + e].x);
+                // a warp without a visible key has no state: factor 0
+                const float f = (mref[n][e] == -INFINITY ? 0.f : ex2(mref[n][e] - m)) * (E4 ? vref : 1.f);
+#pragma unroll
+                for (int mm = 0; mm < MT; ++mm) {
+                    o[mm][n][e] = f == 0.f ? 0.f : o[mm][n][e] * f;
+                    o[mm][n][2 + e] = f == 0.f ? 0.f : o[mm][n][2 + e] * f;
+                }
+            }
+        const bool whole = cw.ua == 0 && cw.ub == cw.s.n_units;
+        // state slot: 2*cta + 1 for a segment that goes on in the next CTA from its start here, else 2*cta
+        const int part = 2 * cta + (cw.ua == 0 && !whole ? 1 : 0);
+#pragma unroll
+        for (int c0 = 0; c0 < HD; c0 += C::CD) {
+            if (c0) __syncthreads();
+#pragma unroll
+            for (int mm = 0; mm < C::CD / 16; ++mm)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = mm * 16 + (E4 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
+                        red[(warp * RT + n * 8 + 2 * t4 + (e & 1)) * (C::CD + 4) + d] = o[c0 / 16 + mm][n][e];
+                    }
+            __syncthreads();
+            for (int w = tid; w < rows * (C::CD / 4); w += kWarps * 32) {
+                const int r = w / (C::CD / 4), d = (w - r * (C::CD / 4)) * 4;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                float m = -INFINITY, lsum = 0.f;
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v) m = fmaxf(m, state[v * RT + r].x);
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v) {
+                    const float4 y = *reinterpret_cast<const float4*>(&red[(v * RT + r) * (C::CD + 4) + d]);
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                    const float2 st = state[v * RT + r];
+                    if (st.x != -INFINITY) lsum += st.y * ex2(st.x - m);
+                }
+                if (whole) {
+                    const float inv = m == -INFINITY ? 0.f : 1.f / lsum;
+                    x.x *= inv;
+                    x.y *= inv;
+                    x.z *= inv;
+                    x.w *= inv;
+                    const int i = (row0 + r) / a.group, hh = (row0 + r) - i * a.group;
+                    float* dst = a.out + ((int64_t)(cw.s.tok0 + i) * a.n_kv_head * a.group + cw.s.h * a.group + hh) * HD;
+                    *reinterpret_cast<float4*>(dst + c0 + d) = x;
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + ((int64_t)part * RT + r) * HD + c0 + d) = x;
+                    if (c0 == 0 && d == 0) a.part_ml[part * RT + r] = make_float2(m, lsum);
+                }
+            }
+        }
+        // the merge kernel's entry: who holds states of this segment
+        if (tid == 0) {
+            const bool starts = cw.ua == 0, cut = starts && !whole;
+            if (starts && (a.split_by_segment || (cut || cw.left <= cw.ub - cw.ua))) {
+                const int64_t last_u = u1 - cw.left + cw.s.n_units - 1;      // the segment's last unit
+                const int last = cut ? (int)(((last_u + 1) * n_cta - 1) / total) : -1;
+                const int at = a.split_by_segment ? seg_no : cta;
+                if (at < kMaxCtas) a.split[at] = Split{cta, last, cw.s.tok0, row0, rows, cw.s.h, {0, 0}};
+            } else if (!a.split_by_segment && cw.left <= cw.ub - cw.ua) {
+                a.split[cta] = Split{0, -1, 0, 0, 0, 0, {0, 0}};
+            }
+        }
+        __syncthreads();
+        ++seg_no;
+        if (!cw.next(a, warp)) break;
+    }
+    if (timeout) atomicOr(a.status, kStatusTimeout);
+}
+
+// Programmatic launch: set-up overlaps the kernel before it on the stream.
+template <int HD, int TYPE, int NT>
+static fr_status launch_one(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
+    using C = Cfg<HD, TYPE, NT>;
+    static unsigned long long done = 0ull;           // devices whose shared-memory limit is raised
+    if (kv.dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> kv.dev & 1ull)) {
+        if (cudaFuncSetAttribute(paged_attn_kernel<HD, TYPE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::SMEM) != cudaSuccess)
+            return FR_ERR_CUDA;
+        if (kv.dev < 64) __atomic_fetch_or(&done, 1ull << kv.dev, __ATOMIC_RELEASE);
+    }
+    CUtensorMap km, vm;
+    memcpy(&km, kv.k_map, sizeof(km));
+    memcpy(&vm, kv.v_map, sizeof(vm));
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<HD, TYPE, NT>, a, km, vm) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+}
+
+template <int TYPE>
+static fr_status launch_type(const KvDesc& kv, const AttnArgs& a, int nt, int ctas, cudaStream_t st) {
+    switch (kv.hd) {
+        case 64: return nt == 1 ? launch_one<64, TYPE, 1>(kv, a, ctas, st)
+                      : nt == 2 ? launch_one<64, TYPE, 2>(kv, a, ctas, st) : launch_one<64, TYPE, 4>(kv, a, ctas, st);
+        case 128: return nt == 1 ? launch_one<128, TYPE, 1>(kv, a, ctas, st)
+                       : nt == 2 ? launch_one<128, TYPE, 2>(kv, a, ctas, st) : launch_one<128, TYPE, 4>(kv, a, ctas, st);
+        default: return nt == 1 ? launch_one<256, TYPE, 1>(kv, a, ctas, st) : launch_one<256, TYPE, 2>(kv, a, ctas, st);
+    }
+}
+
+}  // namespace paged
+}  // namespace fr

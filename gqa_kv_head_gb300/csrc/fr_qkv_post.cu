@@ -315,11 +315,12 @@ extern "C" const char* fr_status_string(fr_status s) {
         case FR_ERR_WORKSPACE: return "FR_ERR_WORKSPACE: workspace missing or too small";
         case FR_ERR_CUDA: return "FR_ERR_CUDA: a CUDA call or kernel launch failed";
         case FR_ERR_DEVICE_TIMEOUT: return "FR_ERR_DEVICE_TIMEOUT: a bounded device wait gave up";
+        case FR_ERR_DEVICE_INPUT: return "FR_ERR_DEVICE_INPUT: a bad page, length or token range on the device";
     }
     return "unknown fr_status";
 }
 
-extern "C" int fr_abi_version(void) { return (4 << 16) | 0; }
+extern "C" int fr_abi_version(void) { return (4 << 16) | 1; }
 
 extern "C" fr_status fr_qkv_post(const float* q, int64_t q_tok_stride, const int32_t* pos,
                                  int n_tok, int n_head, int hd, const fr_rope_params* rp,

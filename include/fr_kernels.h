@@ -59,7 +59,8 @@ typedef enum fr_status {
     FR_ERR_UNSUPPORTED = 2,    /* valid but outside the supported shapes (hd, n_tok, M) */
     FR_ERR_WORKSPACE = 3,      /* workspace missing or smaller than required */
     FR_ERR_CUDA = 4,           /* a CUDA runtime call or a launch failed */
-    FR_ERR_DEVICE_TIMEOUT = 5  /* a bounded device-side wait gave up (see fr_workspace_check) */
+    FR_ERR_DEVICE_TIMEOUT = 5, /* a bounded device-side wait gave up (see fr_workspace_check) */
+    FR_ERR_DEVICE_INPUT = 6    /* a paged call met a bad page or length on the device (see fr_workspace_check) */
 } fr_status;
 
 /* RoPE parameters, NEOX mode, with the YaRN terms as ggml's rope_ext takes
@@ -186,7 +187,9 @@ fr_status fr_workspace_init(void* workspace, size_t workspace_bytes, cudaStream_
 /*
  * Reads the workspace's device status word (synchronises `stream`), clears it
  * and returns FR_ERR_DEVICE_TIMEOUT if a bounded device-side wait of an
- * earlier call on this workspace gave up, else FR_OK.
+ * earlier call on this workspace gave up, FR_ERR_DEVICE_INPUT if an earlier
+ * paged call found a page number, length or token range that its buffers do
+ * not hold, else FR_OK.
  */
 fr_status fr_workspace_check(void* workspace, cudaStream_t stream);
 
@@ -338,6 +341,110 @@ fr_status fr_decode_attn_noalloc(const uint16_t* q16,
  * nothing. The pages have no counterpart to this entry point.
  */
 fr_status fr_decode_attn_noalloc_check(cudaStream_t stream);
+
+/*
+ * ---- Paged K/V cache -------------------------------------------------------
+ * The step of a serving host with several sequences: their K and V rows lie in
+ * fixed-size pages of one pool, and page tables and lengths are device arrays,
+ * so a captured graph follows the lengths. The FlashRT pages, whose adapter
+ * serves one sequence over one contiguous f16 KV head, have no counterpart.
+ *
+ * Two descriptors, filled once by the caller and passed to every call, hold
+ * checked pointers and layouts (and the cache's TMA tile descriptors). They
+ * are plain memory of the caller's: copy or drop them freely; the buffers
+ * stay the caller's and are read afresh by every call. A descriptor belongs
+ * to the GPU that was current when it was filled: calls with another current
+ * GPU return FR_ERR_INVALID_ARG.
+ */
+#define FR_KV_F16 0    /* f16 pages */
+#define FR_KV_E4M3 1   /* e4m3 codes, one f32 scale for each page and KV head: value = scale * code */
+
+typedef struct fr_paged_kv { uint64_t opaque[64]; } fr_paged_kv;
+typedef struct fr_paged_batch { uint64_t opaque[16]; } fr_paged_batch;
+
+/*
+ * fr_paged_kv_init -- describe a cache.
+ *   k, v        element (page, head, row, d) at base[page*strides[0] +
+ *               head*strides[1] + row*strides[2] + d], strides in elements and
+ *               multiples of 16 bytes; no two elements may share an address.
+ *   k_scale, v_scale  FR_KV_E4M3: f32 [n_pages][n_kv_head], finite; else NULL.
+ * Supported: hd in {64, 128, 256}, page_size in {16, 32, 64, 128, 256} rows.
+ */
+fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const int64_t* k_strides, void* v,
+                           const int64_t* v_strides, float* k_scale, float* v_scale, int n_pages, int page_size,
+                           int n_kv_head, int hd);
+
+/*
+ * fr_paged_batch_init -- describe a step: n_seq sequences that bring n_tok new
+ * tokens at most.
+ *   tok_start   int32 [n_seq + 1]: sequence b's new tokens are rows
+ *               tok_start[b] .. tok_start[b+1] - 1 of the step's rows (none,
+ *               one or many). Rows from tok_start[n_seq] to n_tok are padding:
+ *               not read, and left as they were in outputs.
+ *   kv_len      int32 [n_seq]: keys of sequence b, its new tokens included.
+ *   page_table  int32 [n_seq][max_pages], row stride page_table_stride: page
+ *               of the sequence's rows i*page_size .. Entries behind the
+ *               sequence's last page are not read.
+ * Sequences may share pages that no call writes. The arrays are read on the
+ * device by every call. A sequence whose numbers do not fit (tokens outside
+ * 0..n_tok, kv_len outside 0..max_pages*page_size, or fewer keys than new
+ * tokens in an append) is skipped; keys of a page outside 0..n_pages-1 are
+ * treated as masked, and rows for it are not written. Both set the status word
+ * that fr_workspace_check reports as FR_ERR_DEVICE_INPUT.
+ */
+fr_status fr_paged_batch_init(fr_paged_batch* batch, const int32_t* tok_start, const int32_t* kv_len,
+                              const int32_t* page_table, int64_t page_table_stride, int n_seq, int n_tok,
+                              int max_pages);
+
+/*
+ * fr_kv_append_paged -- write a step's new K and V rows into their pages.
+ * Token i of sequence b goes to cache row kv_len[b] - n_b + i:
+ *   K = mscale * NEOX-RoPE(k_new, pos)  with fr_kv_append's arithmetic,  V = v_new,
+ *   f16 pages: rounded once to f16 (K bit-identical to fr_kv_append's);
+ *   e4m3 pages: codes round(x / s), with s per page and head a power of two.
+ *     A call that writes a page's first row starts its scale anew: the
+ *     smallest power of two >= 2^-100 with |x| <= 448 s for the rows written.
+ *     Later rows may make s grow; the page's earlier codes are then stored
+ *     again, rounded at the new scale. Infinities and NaN set no scale and are
+ *     stored as the largest code and as NaN.
+ * Nothing else is touched. No two sequences may write into one page.
+ *   row_type    FR_ROWS_F32 or FR_ROWS_F16: type of k_new and v_new
+ *   k_new, v_new  element (t, h, d) at t*stride + h*hd + d; strides >=
+ *               n_kv_head*hd, multiples of 16 bytes
+ *   pos         int32 [n_tok] positions for the rotation
+ *   workspace   nullable: any workspace (fr_workspace_init), whose status word
+ *               reports bad input; nothing else of it is used
+ */
+#define FR_ROWS_F32 0
+#define FR_ROWS_F16 1
+fr_status fr_kv_append_paged(const fr_paged_kv* kv, const fr_paged_batch* batch, int row_type, const void* k_new,
+                             int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* pos,
+                             const fr_rope_params* rp, void* workspace, cudaStream_t stream);
+
+/* Workspace bytes of fr_paged_attn, for any batch (0 for unsupported heads). */
+size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
+
+/*
+ * fr_paged_attn -- attention of the step's query rows over the paged cache.
+ * Query head h reads KV head h / (n_head / n_kv_head). For token i of sequence
+ * b, at p = kv_len[b] - n_b + i:
+ *   s_j = kq_scale * <Q16[t, h], K[j]>,  out[t, h] = sum_j softmax_j(s) V[j]
+ * over the keys j < kv_len[b], with causal j <= p, and with window > 0 (causal
+ * only) j > p - window. fp32 accumulation, softmax and output. A row that sees
+ * no key yields 0; keys out of a row's view do not reach it, whatever they hold.
+ *   q16         f16, element (t, h, d) at t*q_tok_stride + h*hd + d
+ *               (q_tok_stride >= n_head*hd, a multiple of 8), rotated and
+ *               scaled rows as fr_qkv_post leaves them
+ *   out         f32 [n_tok][n_head][hd] contiguous
+ *   workspace   >= fr_paged_attn_workspace_size bytes, zeroed once
+ *               (fr_workspace_init); one for each concurrently running call
+ * Made for few query rows a sequence (decode, speculative tokens): each 32 rows
+ * (16 at hd 256) of a sequence's KV head read its keys once.
+ * The result does not depend on timing: same inputs, same bits.
+ */
+fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
+                        int64_t q_tok_stride, int n_head, int causal, int window, float kq_scale, float* out,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
