@@ -31,9 +31,9 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, row = blockIdx.y;
-    if ((int)blockIdx.x >= *n_split) return;
+    const int n_entries = *n_split;
     const Split s = split[blockIdx.x];
-    if (s.last < s.first || row >= s.rows) return;
+    if ((int)blockIdx.x >= n_entries || s.last < s.first || row >= s.rows) return;
     const int n = s.last - s.first + 1, cols = hd / 4, groups = blockDim.x / cols, c = tid % cols, gi = tid / cols;
     auto slot = [&](int p) { return (int64_t)(2 * (s.first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
     float4 ahead[kAhead];
@@ -276,7 +276,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     const int64_t cap_units = (((int64_t)bt->max_pages << kv->page_shift) + kUnit - 1) / kUnit;
     int64_t ctas = (int64_t)kCtasPerSm * sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
-    if (segs * cap_units < ctas) ctas = segs * cap_units;
+    if (segs * (cap_units + 1) < ctas) ctas = segs * (cap_units + 1);
 
     char* w = reinterpret_cast<char*>(workspace);
     AttnArgs a;
@@ -314,8 +314,11 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)(a.split_by_segment ? segs : ctas), (unsigned)rows);
-    // few segments: each has many states, read by 1024 threads; many: few states each
-    cfg.blockDim = dim3(a.split_by_segment ? 1024 : 256);
+    // threads for the states that a segment has when all are as long: kAhead for each group of hd/4
+    const int64_t usual = bt->n_tok < bt->n_seq ? bt->n_tok : bt->n_seq * ((avg + rt - 1) / rt);
+    const int64_t states = ctas / (usual * kv->n_kv_head) + 2;
+    int64_t threads = (states + kAhead - 1) / kAhead * (kv->hd / 4);
+    cfg.blockDim = dim3((unsigned)(threads < 64 ? 64 : threads > 1024 ? 1024 : threads));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

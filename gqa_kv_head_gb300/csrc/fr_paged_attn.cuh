@@ -114,7 +114,9 @@ __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
     }
     s.tile0 = lo / kTile;
     s.n_tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
-    s.n_units = max(1, (s.n_tiles + kWarps - 1) / kWarps);   // rows without keys still get their zeros
+    // a segment's start and end cost about as much as a unit of its keys: it
+    // counts one more, ahead of them (rows without keys still get their zeros)
+    s.n_units = 1 + (s.n_tiles + kWarps - 1) / kWarps;
 }
 template <int RT>
 __device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
@@ -166,8 +168,8 @@ struct Walk {
     int t, t_end;       // the warp's next tile of the segment, and the piece's end
     __device__ __forceinline__ void piece(int warp) {
         ub = (int)min((int64_t)s.n_units, ua + left);
-        t = ua * kWarps + warp;
-        t_end = min(ub * kWarps, s.n_tiles);
+        t = max(ua - 1, 0) * kWarps + warp;
+        t_end = min(max(ub - 1, 0) * kWarps, s.n_tiles);
     }
     // on to the next piece; false at the share's end
     __device__ __forceinline__ bool next(const AttnArgs& a, int warp) {
@@ -591,22 +593,35 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                 // of V that no query row sees are cleared (they may lie behind the
                 // sequence's end), and non-finite rows seen by some rows only are
                 // added here for those rows and then cleared.
-                unsigned seen[2];
+                unsigned dead[2], part[2];               // bit 4g: key g (+ 8) unseen; seen by some rows only
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    bool any = false;
+                    bool vis = false, msk = false;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-                            any |= n * 8 + 2 * t4 + c < rows && s[n][2 * e + c] != -INFINITY;
-                    seen[e] = __ballot_sync(~0u, any);
+                            if (n * 8 + 2 * t4 + c < rows) {
+                                const int j = key0 + g + e * 8;
+                                const bool m = bad || j >= lim[n][c] || j < low[n][c];
+                                vis |= !m;
+                                msk |= m;
+                            }
+                    unsigned v = __ballot_sync(~0u, vis), m = __ballot_sync(~0u, msk);
+                    v |= v >> 2;
+                    v |= v >> 1;
+                    m |= m >> 2;
+                    m |= m >> 1;
+                    dead[e] = ~v & 0x11111111u;
+                    part[e] = v & m & 0x11111111u;
                 }
                 unsigned char* sp = ring + c_slot * C::SLOT;
-                for (int j = 0; j < kTile; ++j) {
-                    const bool dead = ((seen[j >> 3] >> (4 * (j & 7))) & 15u) == 0u;
-                    bool weird = false;
-                    if (!dead) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    while (part[e]) {
+                        const int bit = __ffs(part[e]) - 1, j = (bit >> 2) + e * 8;
+                        part[e] &= part[e] - 1;
+                        bool weird = false;
                         for (int c = lane; c < C::ROWB / 4; c += 32) {
                             const uint32_t x = *reinterpret_cast<const uint32_t*>(sp + (c * 4) / C::PITCH * (kTile * C::PITCH) +
                                                                                   j * C::PITCH + (c * 4) % C::PITCH);
@@ -618,14 +633,13 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                                 weird |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
                             }
                         }
-                        weird = __any_sync(~0u, weird);
-                    }
-                    if (weird) {
+                        if (!__any_sync(~0u, weird)) continue;
+                        dead[e] |= 1u << bit;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
-                                const float x = __shfl_sync(~0u, j < 8 ? s[n][c] : s[n][2 + c], (j & 7) * 4 + t4);
+                                const float x = __shfl_sync(~0u, s[n][2 * e + c], (j & 7) * 4 + t4);
                                 if (x == -INFINITY) continue;
                                 const float m = mref[n][c];
                                 const float p = ex2(x - (m == -INFINITY ? 0.f : m) + kPShift) * vs;
@@ -634,24 +648,24 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
 #pragma unroll
                                     for (int u = 0; u < 2; ++u) {
                                         const int d = m2 * 16 + (E4 ? 2 * g + u : g + 8 * u), by = d * (E4 ? 1 : 2);
-                                        const unsigned char* e = ring + (chunk(slot, j, by >> 4) - ring_u) + (by & 15);
+                                        const unsigned char* at = ring + (chunk(slot, j, by >> 4) - ring_u) + (by & 15);
                                         float v;
                                         if (E4) {
-                                            const uint32_t hv = e4m3_lo(*e);
+                                            const uint32_t hv = e4m3_lo(*at);
                                             v = __half2float(__ushort_as_half((unsigned short)hv));
                                         } else {
-                                            v = __half2float(*reinterpret_cast<const __half*>(e));
+                                            v = __half2float(*reinterpret_cast<const __half*>(at));
                                         }
                                         o[m2][n][2 * u + c] += p * v;
                                     }
                             }
                     }
-                    __syncwarp();
-                    if (dead || weird)
-                        for (int c = lane; c < C::ROWB / 4; c += 32)
-                            *reinterpret_cast<uint32_t*>(sp + (c * 4) / C::PITCH * (kTile * C::PITCH) + j * C::PITCH +
-                                                         (c * 4) % C::PITCH) = 0u;
-                }
+                __syncwarp();
+                if (dead[0] | dead[1])
+                    for (int c = lane; c < C::SLOT / 16; c += 32) {
+                        const int j = c * 16 / C::PITCH % kTile;
+                        if (dead[j >> 3] >> (4 * (j & 7)) & 1u) *reinterpret_cast<uint4*>(sp + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 fence_proxy_async_cta();             // the slot's next fill comes by TMA
                 __syncwarp();
             }
