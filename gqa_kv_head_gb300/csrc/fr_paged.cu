@@ -157,9 +157,22 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
     return true;
 }
 
-static int max_row_tile(int hd) { return hd == 256 ? 16 : 32; }
+static int max_nt(int hd) { return hd == 256 ? 2 : 4; }
+// Attention CTAs for row tiles of 8*nt rows on a GPU of sms SMs (the workspace is sized for the most)
+static int ctas_for(int hd, int nt, int sms) {
+    const int per = ctas_per_sm(hd, nt), most = kMaxCtas * per / 4;
+    return per * sms < most ? per * sms : most;
+}
+static size_t ws_rows(int hd) {        // rows of split states, two states for each CTA
+    size_t n = 0;
+    for (int nt = 1; nt <= max_nt(hd); nt *= 2) {
+        const size_t r = (size_t)2 * ctas_for(hd, nt, kMaxCtas) * 8 * nt;
+        if (r > n) n = r;
+    }
+    return n;
+}
 static size_t ws_bytes(int hd) {
-    return kWsHeader + sizeof(Split) * kMaxCtas + (size_t)2 * kMaxCtas * max_row_tile(hd) * (sizeof(float2) + 4 * (size_t)hd);
+    return kWsHeader + sizeof(Split) * kMaxCtas + ws_rows(hd) * (sizeof(float2) + 4 * (size_t)hd);
 }
 
 }  // namespace paged
@@ -268,14 +281,13 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     // Row tile: 8 rows for each MMA column block, as many blocks as an average
     // sequence of the batch fills (a longer one takes several row tiles)
     const int64_t avg = (int64_t)G * ((bt->n_tok + bt->n_seq - 1) / bt->n_seq);
-    const int nt = avg <= 8 ? 1 : avg <= 16 || kv->hd == 256 ? 2 : 4;
+    const int nt = avg <= 8 ? 1 : avg <= 16 ? 2 : max_nt(kv->hd);
     const int rt = 8 * nt;
     // at most this many segments, and units of work, whatever the lengths say
     const int64_t per_tok = (int64_t)bt->n_tok * ((G + rt - 1) / rt), per_seq = bt->n_seq + (int64_t)bt->n_tok * G / rt;
     const int64_t segs = (per_tok < per_seq ? per_tok : per_seq) * kv->n_kv_head;
     const int64_t cap_units = (((int64_t)bt->max_pages << kv->page_shift) + kUnit - 1) / kUnit;
-    int64_t ctas = (int64_t)kCtasPerSm * sms;
-    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    int64_t ctas = ctas_for(kv->hd, nt, sms);
     if (segs * (cap_units + 1) < ctas) ctas = segs * (cap_units + 1);
 
     char* w = reinterpret_cast<char*>(workspace);
@@ -294,7 +306,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     a.n_split = reinterpret_cast<int*>(w + 64);
     a.split = reinterpret_cast<Split*>(w + kWsHeader);
     a.part_ml = reinterpret_cast<float2*>(w + kWsHeader + sizeof(Split) * kMaxCtas);
-    a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * kMaxCtas * max_row_tile(kv->hd));
+    a.part_o = reinterpret_cast<float*>(a.part_ml + ws_rows(kv->hd));
     a.n_seq = bt->n_seq;
     a.n_tok = bt->n_tok;
     a.max_pages = bt->max_pages;

@@ -14,10 +14,11 @@ namespace paged {
 
 constexpr int kWarps = 4;            // warps per attention CTA
 constexpr int kTile = 16;            // keys per warp tile (the MMA's M)
-constexpr int kUnit = kWarps * kTile;  // keys of one unit of work: a tile for each warp
-constexpr int kCtasPerSm = 2;
-constexpr int kMaxCtas = 320;        // attention CTAs at most: the workspace holds two split states for each
-constexpr int kMaxRowTile = 32;      // query rows of one row tile at most
+constexpr int kUnit = kWarps * kTile;  // keys of one unit of work at least: a tile for each warp
+// Attention CTAs per SM: four where the accumulators leave room in 128
+// registers a thread, so that four warps of a scheduler hide each other's waits.
+__host__ __device__ constexpr int ctas_per_sm(int hd, int nt) { return nt == 1 && hd <= 128 ? 4 : 2; }
+constexpr int kMaxCtas = 640;        // attention CTAs at most: the workspace holds two split states for each
 constexpr int kMaxSeq = 65536;
 constexpr size_t kWsHeader = 1024;   // [0, 4): status word, as in the other workspaces
 

@@ -24,8 +24,8 @@
 // and written there; one cut by a share's end leaves (m, l, O) states in the
 // workspace for the merge kernel (fr_paged.cu).
 //
-// P enters the PV product as two f16 terms P_hi + P_lo (22 bits), scaled by
-// 2^7 to keep P_lo off f16's subnormals: the result carries fp32 accuracy like
+// P enters the PV product as two f16 terms P_hi + P_lo (22 bits), held
+// between 2^7 and 2^15 at the maximum to keep P_lo off f16's subnormals: the result carries fp32 accuracy like
 // fr_decode_attn's. e4m3 codes become f16 in registers, which is exact; K's
 // scale joins the score's factor, V's scale the weights, relative to the
 // largest V scale met so far (the same kind of running reference as m).
@@ -42,8 +42,11 @@ namespace paged {
 
 using namespace sm100;
 
-constexpr float kTau = 8.0f;           // a reference maximum moves when a score exceeds it by 2^8
-constexpr float kPShift = 7.0f;        // weights are held times 2^7: at most 2^15 in f16
+// Weights are 2^(x - mref): a row's reference mref is 7 below its maximum when
+// set, and moves when a score exceeds it by 15, so weights reach 2^15 at most in
+// f16 and P_lo stays off f16's subnormals for all weights that matter.
+constexpr float kBelow = 7.0f, kAbove = 15.0f;
+constexpr float kNoRef = -3.402823466e38f;           // a row without a key so far
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int head, int page,
@@ -70,30 +73,41 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
     return y;
 }
 
+// D (16x8 f32) += A (16x16 f16, row) * B (16x8 f16, col); free to be scheduled
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 template <int HD, int TYPE, int NT>
 struct Cfg {
     static constexpr bool E4 = TYPE == FR_KV_E4M3;
     static constexpr int RT = 8 * NT;                       // query rows of a row tile
     static constexpr int ROWB = HD * (E4 ? 1 : 2);          // bytes of a K or V row
     static constexpr int PITCH = ROWB < 128 ? ROWB : 128;   // bytes of a row in one box
-    static constexpr int BOXES = ROWB / PITCH;
-    static constexpr int SLOT = kTile * ROWB;
     static constexpr int MT = HD / 16;                      // 16-dim blocks of O^T, and k steps of S^T
+    static constexpr int CPS = ctas_per_sm(HD, NT);
+    static constexpr int LIMIT = 233472 / CPS - 1024;       // shared memory of one CTA
     // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
     static constexpr bool QREG = HD * NT <= 256;
     static constexpr int QPITCH = HD * 2 + (E4 ? 32 : 16);  // bytes: rows on different banks
     static constexpr int QBYTES = QREG ? 0 : RT * QPITCH;
-    // dims of O that the warps' states are added over at a time
-    static constexpr int CD = HD * NT >= 512 ? 16 : HD * NT >= 256 ? 32 : 64;
+    static constexpr int CD = NT == 4 || HD * NT >= 512 ? 16 : 32;   // dims that the warps' states are added over at a time
     static constexpr int RED = kWarps * RT * (CD + 4) * 4;
     static constexpr int STATE = kWarps * RT * 8;
-    // alignment slack, buffers above, then tile entries, barriers and the scan's words
-    static constexpr int FIXED = 1024 + RED + QBYTES + STATE + kWarps * (256 + 128) + 128;
-    static constexpr int NS_ = (115712 - FIXED) / (kWarps * SLOT);
-    static constexpr int NS = NS_ > 16 ? 16 : NS_;          // slots of a warp's ring
+    static constexpr int ENTRIES = 8;                       // tiles requested and not used up, at most
+    static constexpr int META = kWarps * ENTRIES * 32;
+    // alignment slack, buffers above, then barriers and the scan's words
+    static constexpr int FIXED = 1024 + RED + QBYTES + STATE + META + kWarps * 64 + 128;
+    // 32 keys a slot where three slots of them fit (K, V and the next K), else 16
+    static constexpr int SUB = 3 * kWarps * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
+    static constexpr int KT = kTile * SUB;                  // keys of a warp's tile
+    static constexpr int SUBB = kTile * ROWB, SLOT = SUB * SUBB;
+    static constexpr int NS_ = (LIMIT - FIXED) / (kWarps * SLOT);
+    static constexpr int NS = NS_ > 8 ? 8 : NS_;            // slots of a warp's ring
     static constexpr int SMEM = FIXED + NS * kWarps * SLOT;
     static_assert(NS >= 3, "ring");
-    static_assert(SMEM <= 115712, "two CTAs per SM");
 };
 
 // One (sequence, KV head, row tile): its rows, and its keys as 16-key tiles.
@@ -103,7 +117,7 @@ struct Seg {
     int tile0, n_tiles, n_units;
 };
 
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
     const int r0 = s.rt * RT, r1 = min(s.n_q * a.group, r0 + RT) - 1;
     int hi = s.n_kv, lo = 0;
@@ -112,8 +126,8 @@ __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
         hi = min(hi, first + r1 / a.group + 1);
         if (a.window > 0) lo = max(0, first + r0 / a.group - a.window + 1);
     }
-    s.tile0 = lo / kTile;
-    s.n_tiles = hi > lo ? (hi + kTile - 1) / kTile - s.tile0 : 0;
+    s.tile0 = lo / KT;
+    s.n_tiles = hi > lo ? (hi + KT - 1) / KT - s.tile0 : 0;
     // a segment's start and end cost about as much as a unit of its keys: it
     // counts one more, ahead of them (rows without keys still get their zeros)
     s.n_units = 1 + (s.n_tiles + kWarps - 1) / kWarps;
@@ -129,7 +143,7 @@ __device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
     return q.bad;
 }
 // The next segment in order (row tile fastest, then KV head, then sequence).
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
     if (++s.rt == s.n_rt) {
         s.rt = 0;
@@ -142,17 +156,17 @@ __device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
             } while (s.n_rt == 0);
         }
     }
-    seg_keys<RT>(s, a);
+    seg_keys<RT, KT>(s, a);
 }
 // Units of all segments of sequence b for one KV head.
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ int64_t seq_units(const AttnArgs& a, int b, int& n_rt, bool& bad) {
     Seg s;
     bad = seg_seq<RT>(s, a, b);
     n_rt = s.n_rt;
     int64_t u = 0;
     for (s.rt = 0; s.rt < s.n_rt; ++s.rt) {
-        seg_keys<RT>(s, a);
+        seg_keys<RT, KT>(s, a);
         u += s.n_units;
     }
     return u;
@@ -160,7 +174,7 @@ __device__ __forceinline__ int64_t seq_units(const AttnArgs& a, int b, int& n_rt
 
 // A walk over a CTA's share of the units: the pieces of segments it holds, and
 // inside a piece the tiles of one warp.
-template <int RT>
+template <int RT, int KT>
 struct Walk {
     Seg s;
     int64_t left;       // units of the share from this piece on
@@ -175,7 +189,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttnArgs& a, int warp) {
         left -= ub - ua;
         if (left <= 0) return false;
-        seg_next<RT>(s, a);
+        seg_next<RT, KT>(s, a);
         ua = 0;
         piece(warp);
         return true;
@@ -183,10 +197,10 @@ struct Walk {
 };
 
 template <int HD, int TYPE, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(HD, NT))
 paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = Cfg<HD, TYPE, NT>;
-    constexpr int RT = C::RT, MT = C::MT, NS = C::NS;
+    constexpr int RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
     constexpr bool E4 = C::E4;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -196,9 +210,11 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
     float* red = reinterpret_cast<float*>(after);                                       // [warp][RT][CD + 4]
     unsigned char* q_sm = after + C::RED;                                               // [RT][QPITCH]
     float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);                        // [warp][RT]
-    float4* meta = reinterpret_cast<float4*>(q_sm + C::QBYTES + C::STATE) + warp * 16;  // k scale, v scale, bad
-    uint64_t* bars = reinterpret_cast<uint64_t*>(q_sm + C::QBYTES + C::STATE + kWarps * 256) + warp * 16;
-    int64_t* scan = reinterpret_cast<int64_t*>(q_sm + C::QBYTES + C::STATE + kWarps * 384);   // [16]
+    struct Entry { float ks[2], vs[2]; uint32_t bad, pad[3]; };                          // of a tile's 16-key halves
+    unsigned char* misc = q_sm + C::QBYTES + C::STATE;
+    Entry* meta = reinterpret_cast<Entry*>(misc) + warp * C::ENTRIES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(misc + C::META) + warp * 8;
+    int64_t* scan = reinterpret_cast<int64_t*>(misc + C::META + kWarps * 64);            // [16]
     const uint32_t ring_u = smem_addr(ring), bars_u = smem_addr(bars);
 
     if (lane == 0) {
@@ -220,7 +236,7 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
     for (int b = tid; b < a.n_seq; b += kWarps * 32) {
         int n_rt;
         bool bad;
-        mine += seq_units<RT>(a, b, n_rt, bad);
+        mine += seq_units<RT, KT>(a, b, n_rt, bad);
         mine_s += n_rt;
         bad_any |= bad;
     }
@@ -242,7 +258,7 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                               (scan[4] + scan[5] + scan[6] + scan[7]) * a.n_kv_head : n_cta);
     if (cta >= n_cta) return;
     const int64_t u0 = total * cta / n_cta, u1 = total * (cta + 1) / n_cta;
-    Walk<RT> cw;                 // what is consumed
+    Walk<RT, KT> cw;                 // what is consumed
     int seg_no = 0;              // the segment's number in the whole list
     int64_t base_u = 0;
     int base_seg = 0;
@@ -250,7 +266,7 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
         const int b = b0 + tid;
         int n_rt = 0;
         bool bad;
-        const int64_t u = b < a.n_seq ? seq_units<RT>(a, b, n_rt, bad) * a.n_kv_head : 0;
+        const int64_t u = b < a.n_seq ? seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head : 0;
         int64_t inc = u;
         int inc_s = n_rt * a.n_kv_head;
         const int own_s = inc_s;
@@ -292,12 +308,12 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
         int n_rt;
         bool bad;
         const int b = (int)scan[8];
-        const int64_t per_head = seq_units<RT>(a, b, n_rt, bad);
+        const int64_t per_head = seq_units<RT, KT>(a, b, n_rt, bad);
         seg_seq<RT>(cw.s, a, b);
         cw.s.h = (int)(rem / per_head);
         rem -= cw.s.h * per_head;
         for (cw.s.rt = 0;; ++cw.s.rt) {
-            seg_keys<RT>(cw.s, a);
+            seg_keys<RT, KT>(cw.s, a);
             if (rem < cw.s.n_units) break;
             rem -= cw.s.n_units;
         }
@@ -308,34 +324,34 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
     }
 
     // ---- the warp's ring: slots q = 0, 1, ... hold K, V, K, V, ... of its tiles ----
-    Walk<RT> pw = cw;            // what is requested
+    Walk<RT, KT> pw = cw;            // what is requested
     bool more = true;
-    int blk = 32;                // entries of the page block used up (32: load a new one)
-    int b_page = 0, p_page = 0, p_row = 0;
+    constexpr int BLK = 32 / SUB;  // tiles of a page block: a lane for each 16 keys
+    int blk = BLK;               // tiles of the page block used up (BLK: load a new one)
+    int b_page = 0, p_page[SUB] = {};
     float b_ks = 1.f, b_vs = 1.f;
-    int i_slot = 0, i_tile = 0;  // ring slot of the next request; its tile's number mod 16
+    int i_slot = 0, i_tile = 0;  // ring slot of the next request; its tile's number mod ENTRIES
     bool i_v = false;
     auto request = [&]() {
         if (!more) return;
-        if (!i_v) {              // a new tile: its page, and its scales for the consumer
+        if (!i_v) {              // a new tile: its pages, and its scales for the consumer
             while (pw.t >= pw.t_end) {
                 if (!pw.next(a, warp)) {
                     more = false;
                     return;
                 }
-                blk = 32;
+                blk = BLK;
             }
-            const int tile = pw.s.tile0 + pw.t;
-            if (blk == 32) {
-                const int tl = pw.t + lane * kWarps;
-                b_page = 0;
-                if (tl < pw.t_end) {
-                    const int idx = (pw.s.tile0 + tl) >> (a.page_shift - 4);
-                    b_page = __ldg(a.table + pw.s.b * a.table_stride + idx);
+            if (blk == BLK) {
+                const int tl = pw.t + lane / SUB * kWarps;
+                const int key = (pw.s.tile0 + tl) * KT + lane % SUB * kTile;
+                b_page = -1;
+                b_ks = b_vs = 0.f;
+                if (tl < pw.t_end && key < pw.s.n_kv) {
+                    b_page = __ldg(a.table + pw.s.b * a.table_stride + (key >> a.page_shift));
                     if (b_page < 0 || b_page >= a.n_pages) {
                         b_page = -1;
                         atomicOr(a.status, kStatusInput);
-                        b_ks = b_vs = 0.f;
                     } else if (E4) {
                         b_ks = __ldg(a.k_scale + (int64_t)b_page * a.n_kv_head + pw.s.h);
                         b_vs = __ldg(a.v_scale + (int64_t)b_page * a.n_kv_head + pw.s.h);
@@ -343,22 +359,45 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                 }
                 blk = 0;
             }
-            p_page = __shfl_sync(~0u, b_page, blk);
-            p_row = (tile << 4) & ((1 << a.page_shift) - 1);
-            const float ks = E4 ? __shfl_sync(~0u, b_ks, blk) : 1.f, vs = E4 ? __shfl_sync(~0u, b_vs, blk) : 1.f;
+            Entry e;
+            e.bad = 0u;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                p_page[u] = __shfl_sync(~0u, b_page, blk * SUB + u);
+                if (E4) {
+                    e.ks[u] = __shfl_sync(~0u, b_ks, blk * SUB + u);
+                    e.vs[u] = __shfl_sync(~0u, b_vs, blk * SUB + u);
+                }
+                // no such page: page 0, which exists, is read in its place and its keys are masked
+                if (p_page[u] < 0) e.bad |= 1u << u;
+                p_page[u] = max(p_page[u], 0);
+            }
             ++blk;
-            if (lane == 0) meta[i_tile] = make_float4(ks, vs, p_page < 0 ? 1.f : 0.f, 0.f);
+            if (lane == 0) {
+                Entry& m = meta[i_tile];
+                if (E4) {
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        m.ks[u] = e.ks[u];
+                        m.vs[u] = e.vs[u];
+                    }
+                }
+                m.bad = e.bad;
+            }
         }
         if (lane == 0) {
             const uint32_t bar = bars_u + 8 * i_slot;
+            const int key = (pw.s.tile0 + pw.t) * KT, rows = (1 << a.page_shift) - 1;
             mbar_expect_tx(bar, C::SLOT);
-            // a bad page reads page 0, which exists; its keys are masked
-            tma_load_5d(ring_u + i_slot * C::SLOT, i_v ? &v_map : &k_map, p_row, pw.s.h, max(p_page, 0), bar);
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+                tma_load_5d(ring_u + i_slot * C::SLOT + u * C::SUBB, i_v ? &v_map : &k_map, (key + u * kTile) & rows,
+                            pw.s.h, p_page[u], bar);
         }
         if (++i_slot == NS) i_slot = 0;
         if (i_v) {
             pw.t += kWarps;
-            i_tile = (i_tile + 1) & 15;
+            i_tile = (i_tile + 1) % C::ENTRIES;
         }
         i_v = !i_v;
     };
@@ -382,10 +421,17 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
         }
     };
 
-    // shared-memory address of 16-byte chunk c of row r in a slot (the TMA's swizzle)
-    auto chunk = [](uint32_t slot, int r, int c) -> uint32_t {
-        if (C::PITCH == 128) return slot + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        return slot + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    // Addresses of this lane's 16-byte chunks for ldmatrix, in the TMA's swizzle:
+    // row r of a 16-row box, chunk c + h with h this lane's bit and c even, is at
+    // (base + lane part) ^ (c << 4), the slots being aligned beyond those bits.
+    auto swz = [](int r) { return C::PITCH == 128 ? r & 7 : (r >> 1) & 3; };
+    constexpr int CPB = C::PITCH / 16;               // chunks of a row in a box
+    const int k_r = (lane & 7) + ((lane >> 3) & 1) * 8, k_h = lane >> 4;
+    const int v_r = E4 ? k_r : (lane & 7) + (lane >> 4) * 8, v_h = E4 ? k_h : (lane >> 3) & 1;
+    const uint32_t k_lane = ring_u + k_r * C::PITCH + ((k_h ^ swz(k_r)) << 4);
+    const uint32_t v_lane = ring_u + v_r * C::PITCH + ((v_h ^ swz(v_r)) << 4);
+    auto at_chunk = [](uint32_t base, int sub, int c) {
+        return (base ^ ((c % CPB) << 4)) + sub * C::SUBB + c / CPB * (kTile * C::PITCH);
     };
 
     for (;;) {
@@ -467,7 +513,7 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
         float vref = 0.f;                            // largest V scale so far
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            mref[n][0] = mref[n][1] = -INFINITY;
+            mref[n][0] = mref[n][1] = kNoRef;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int m = 0; m < MT; ++m) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
@@ -476,84 +522,108 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
         for (; cw.t < cw.t_end; cw.t += kWarps) {
             // ---- S^T = K Q^T ------------------------------------------------
             wait_slot();
-            const float4 mt_ = meta[c_tile];
-            uint32_t slot = ring_u + c_slot * C::SLOT;
-            float s[NT][4], s2[NT][4];               // two chains of MMAs
+            const Entry& en = meta[c_tile];
+            const uint32_t bad = en.bad;
+            uint32_t base = k_lane + c_slot * C::SLOT;
+            float s[SUB][NT][4], s2[SUB][NT][4];     // s2: a second chain of MMAs where there is one tile
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
-            if (E4) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int kk = 0; kk < MT; kk += 2) {
-                    uint32_t r0, r1, r2, r3;
-                    ldsm_x4(chunk(slot, (lane & 7) + ((lane >> 3) & 1) * 8, kk + (lane >> 4)), r0, r1, r2, r3);
-                    const uint32_t a0[4] = {e4m3_lo(r0), e4m3_lo(r1), e4m3_hi(r0), e4m3_hi(r1)};
-                    const uint32_t a1[4] = {e4m3_lo(r2), e4m3_lo(r3), e4m3_hi(r2), e4m3_hi(r3)};
+                    for (int e = 0; e < 4; ++e) s[u][n][e] = s2[u][n][e] = 0.f;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t b0, b1;
-                        q_frag(kk, n, b0, b1);
-                        mma_16816(s[n], a0, b0, b1);
-                        q_frag(kk + 1, n, b0, b1);
-                        mma_16816(s2[n], a1, b0, b1);
-                    }
+            for (int kk = 0; kk < MT; kk += E4 ? 2 : 1) {
+                uint32_t qa[NT][2], qb[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    q_frag(kk, n, qa[n][0], qa[n][1]);
+                    if (E4) q_frag(kk + 1, n, qb[n][0], qb[n][1]);
                 }
-            } else {
 #pragma unroll
-                for (int kk = 0; kk < MT; ++kk) {
-                    uint32_t af[4];
-                    ldsm_x4(chunk(slot, (lane & 7) + ((lane >> 3) & 1) * 8, 2 * kk + (lane >> 4)), af[0], af[1], af[2],
-                            af[3]);
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t r[4];
+                    ldsm_x4(at_chunk(base, u, E4 ? kk : 2 * kk), r[0], r[1], r[2], r[3]);
+                    if (E4) {
+                        const uint32_t a0[4] = {e4m3_lo(r[0]), e4m3_lo(r[1]), e4m3_hi(r[0]), e4m3_hi(r[1])};
+                        const uint32_t a1[4] = {e4m3_lo(r[2]), e4m3_lo(r[3]), e4m3_hi(r[2]), e4m3_hi(r[3])};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t b0, b1;
-                        q_frag(kk, n, b0, b1);
-                        mma_16816(kk & 1 ? s2[n] : s[n], af, b0, b1);
+                        for (int n = 0; n < NT; ++n) {
+                            mma(s[u][n], a0, qa[n][0], qa[n][1]);
+                            mma(SUB == 1 ? s2[u][n] : s[u][n], a1, qb[n][0], qb[n][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma(SUB == 1 && (kk & 1) ? s2[u][n] : s[u][n], r, qa[n][0], qa[n][1]);
                     }
                 }
             }
+            if (SUB == 1) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[0][n][e] += s2[0][n][e];
+            }
+            float sc[SUB], vs[SUB], vmax = 0.f;
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                sc[u] = E4 ? a.scale_log2 * en.ks[u] : a.scale_log2;
+                vs[u] = E4 ? en.vs[u] : 1.f;
+                vmax = fmaxf(vmax, fabsf(vs[u]));
+            }
             pass_slot();
 
-            // ---- softmax weights ---------------------------------------------
-            const int key0 = (cw.s.tile0 + cw.t) * kTile;
-            const bool bad = mt_.z != 0.f;
-            const bool edge = bad || key0 + kTile > min_lim || key0 < max_low;
-            const float sc = a.scale_log2 * mt_.x;
+            // ---- softmax weights: exponents x - mref first -------------------
+            const int key0 = (cw.s.tile0 + cw.t) * KT;
+            const bool edge = bad != 0u || key0 + KT > min_lim || key0 < max_low;
             bool up = false;
+            float y[SUB][NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = (s[n][e] + s2[n][e]) * sc;
-                    if (edge) {
-                        const int j = key0 + g + (e >> 1) * 8;
-                        if (bad || j >= lim[n][e & 1] || j < low[n][e & 1]) x = -INFINITY;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(s[u][n][e], sc[u], -mref[n][e & 1]);
+                        if (edge) {
+                            const int j = key0 + u * kTile + g + (e >> 1) * 8;
+                            if ((bad >> u & 1u) || j >= lim[n][e & 1] || j < low[n][e & 1]) x = -INFINITY;
+                        }
+                        y[u][n][e] = x;
+                        up |= x > kAbove;
                     }
-                    s[n][e] = x;
-                    up |= x > mref[n][e & 1] + kTau;
-                }
-            float vs = 1.f;                          // this tile's V scale over vref
-            const bool vup = E4 && fabsf(mt_.y) > vref;
+            const bool vup = E4 && vmax > vref;
             if (__any_sync(~0u, up) || vup) {
                 float va = 1.f;
                 if (vup) {
-                    va = vref / fabsf(mt_.y);
-                    vref = fabsf(mt_.y);
+                    const float v = fmaxf(vmax, 0x1p-120f);      // its reciprocal stays finite
+                    va = vref / v;
+                    vref = v;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float al[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(s[n][e], s[n][e + 2]);
+                    for (int c = 0; c < 2; ++c) {
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int e = c; e < 4; e += 2)
+                                m = fmaxf(m, y[u][n][e] == -INFINITY ? -INFINITY : s[u][n][e] * sc[u]);
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
-                        m = fmaxf(m, mref[n][e]);
-                        al[e] = m == -INFINITY ? 1.f : ex2(mref[n][e] - m);
-                        mref[n][e] = m;
-                        l[n][e] *= al[e];
-                        al[e] *= va;
+                        m = fmaxf(m - kBelow, mref[n][c]);
+                        al[c] = ex2(mref[n][c] - m);
+                        mref[n][c] = m;
+                        l[n][c] *= al[c];
+                        al[c] *= va;
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int e = c; e < 4; e += 2)
+                                y[u][n][e] = y[u][n][e] == -INFINITY ? -INFINITY : fmaf(s[u][n][e], sc[u], -m);
                     }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
@@ -564,144 +634,146 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                     }
                 }
             }
-            if (E4) vs = mt_.y == 0.f ? 0.f : mt_.y / vref;
-            uint32_t ph[NT][2], pl[NT][2];
+            if (E4) {
+                const float inv = vref > 0.f ? 1.f / vref : 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float m = mref[n][e & 1];
-                    const float p = ex2(s[n][e] - (m == -INFINITY ? 0.f : m) + kPShift);
-                    l[n][e & 1] += p;
-                    w[e] = E4 ? p * vs : p;
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const __half2 h = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
-                    const float2 hf = __half22float2(h);
-                    ph[n][e] = movm(*reinterpret_cast<const uint32_t*>(&h));
-                    pl[n][e] = movm(pack_half2(w[2 * e] - hf.x, w[2 * e + 1] - hf.y));
-                }
+                for (int u = 0; u < SUB; ++u) vs[u] *= inv;
             }
+            uint32_t ph[SUB][NT][2], pl[SUB][NT][2];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float w0 = ex2(y[u][n][2 * e]), w1 = ex2(y[u][n][2 * e + 1]);
+                        l[n][0] += w0;
+                        l[n][1] += w1;
+                        if (E4) {
+                            w0 *= vs[u];
+                            w1 *= vs[u];
+                        }
+                        const __half2 h = __floats2half2_rn(w0, w1);
+                        const float2 hf = __half22float2(h);
+                        ph[u][n][e] = movm(*reinterpret_cast<const uint32_t*>(&h));
+                        pl[u][n][e] = movm(pack_half2(w0 - hf.x, w1 - hf.y));
+                    }
 
             // ---- O^T += V^T P^T ------------------------------------------------
             wait_slot();
-            slot = ring_u + c_slot * C::SLOT;
             if (edge) {
                 // A masked key has weight 0, but 0 * inf and 0 * NaN are NaN: rows
                 // of V that no query row sees are cleared (they may lie behind the
                 // sequence's end), and non-finite rows seen by some rows only are
                 // added here for those rows and then cleared.
-                unsigned dead[2], part[2];               // bit 4g: key g (+ 8) unseen; seen by some rows only
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    bool vis = false, msk = false;
+                for (int u = 0; u < SUB; ++u) {
+                    unsigned char* sp = ring + c_slot * C::SLOT + u * C::SUBB;
+                    unsigned dead[2], part[2];           // bit 4g: key g (+ 8) unseen; seen by some rows only
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (n * 8 + 2 * t4 + c < rows) {
-                                const int j = key0 + g + e * 8;
-                                const bool m = bad || j >= lim[n][c] || j < low[n][c];
-                                vis |= !m;
-                                msk |= m;
-                            }
-                    unsigned v = __ballot_sync(~0u, vis), m = __ballot_sync(~0u, msk);
-                    v |= v >> 2;
-                    v |= v >> 1;
-                    m |= m >> 2;
-                    m |= m >> 1;
-                    dead[e] = ~v & 0x11111111u;
-                    part[e] = v & m & 0x11111111u;
-                }
-                unsigned char* sp = ring + c_slot * C::SLOT;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    while (part[e]) {
-                        const int bit = __ffs(part[e]) - 1, j = (bit >> 2) + e * 8;
-                        part[e] &= part[e] - 1;
-                        bool weird = false;
-                        for (int c = lane; c < C::ROWB / 4; c += 32) {
-                            const uint32_t x = *reinterpret_cast<const uint32_t*>(sp + (c * 4) / C::PITCH * (kTile * C::PITCH) +
-                                                                                  j * C::PITCH + (c * 4) % C::PITCH);
-                            if (E4) {
-                                const uint32_t y = x & 0x7f7f7f7fu;
-                                weird |= (y & 0xffu) == 0x7fu || (y >> 8 & 0xffu) == 0x7fu || (y >> 16 & 0xffu) == 0x7fu ||
-                                         y >> 24 == 0x7fu;
-                            } else {
-                                weird |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
-                            }
-                        }
-                        if (!__any_sync(~0u, weird)) continue;
-                        dead[e] |= 1u << bit;
+                    for (int e = 0; e < 2; ++e) {
+                        bool vis = false, msk = false;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const float x = __shfl_sync(~0u, s[n][2 * e + c], (j & 7) * 4 + t4);
-                                if (x == -INFINITY) continue;
-                                const float m = mref[n][c];
-                                const float p = ex2(x - (m == -INFINITY ? 0.f : m) + kPShift) * vs;
+                            for (int c = 0; c < 2; ++c)
+                                if (n * 8 + 2 * t4 + c < rows) {
+                                    const int j = key0 + u * kTile + g + e * 8;
+                                    const bool m = (bad >> u & 1u) || j >= lim[n][c] || j < low[n][c];
+                                    vis |= !m;
+                                    msk |= m;
+                                }
+                        unsigned v = __ballot_sync(~0u, vis), m = __ballot_sync(~0u, msk);
+                        v |= v >> 2;
+                        v |= v >> 1;
+                        m |= m >> 2;
+                        m |= m >> 1;
+                        dead[e] = ~v & 0x11111111u;
+                        part[e] = v & m & 0x11111111u;
+                    }
 #pragma unroll
-                                for (int m2 = 0; m2 < MT; ++m2)
-#pragma unroll
-                                    for (int u = 0; u < 2; ++u) {
-                                        const int d = m2 * 16 + (E4 ? 2 * g + u : g + 8 * u), by = d * (E4 ? 1 : 2);
-                                        const unsigned char* at = ring + (chunk(slot, j, by >> 4) - ring_u) + (by & 15);
-                                        float v;
-                                        if (E4) {
-                                            const uint32_t hv = e4m3_lo(*at);
-                                            v = __half2float(__ushort_as_half((unsigned short)hv));
-                                        } else {
-                                            v = __half2float(*reinterpret_cast<const __half*>(at));
-                                        }
-                                        o[m2][n][2 * u + c] += p * v;
-                                    }
+                    for (int e = 0; e < 2; ++e)
+                        while (part[e]) {
+                            const int bit = __ffs(part[e]) - 1, j = (bit >> 2) + e * 8;
+                            part[e] &= part[e] - 1;
+                            bool weird = false;
+                            for (int c = lane; c < C::ROWB / 4; c += 32) {
+                                const uint32_t x = *reinterpret_cast<const uint32_t*>(
+                                    sp + (c * 4) / C::PITCH * (kTile * C::PITCH) + j * C::PITCH + (c * 4) % C::PITCH);
+                                if (E4) {
+                                    const uint32_t z = x & 0x7f7f7f7fu;
+                                    weird |= (z & 0xffu) == 0x7fu || (z >> 8 & 0xffu) == 0x7fu ||
+                                             (z >> 16 & 0xffu) == 0x7fu || z >> 24 == 0x7fu;
+                                } else {
+                                    weird |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
+                                }
                             }
-                    }
-                __syncwarp();
-                if (dead[0] | dead[1])
-                    for (int c = lane; c < C::SLOT / 16; c += 32) {
-                        const int j = c * 16 / C::PITCH % kTile;
-                        if (dead[j >> 3] >> (4 * (j & 7)) & 1u) *reinterpret_cast<uint4*>(sp + c * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                            if (!__any_sync(~0u, weird)) continue;
+                            dead[e] |= 1u << bit;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const float x = __shfl_sync(~0u, y[u][n][2 * e + c], (j & 7) * 4 + t4);
+                                    if (x == -INFINITY) continue;
+                                    const float w = ex2(x) * vs[u];
+#pragma unroll
+                                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                        for (int i = 0; i < 2; ++i) {
+                                            const int d = m * 16 + (E4 ? 2 * g + i : g + 8 * i), by = d * (E4 ? 1 : 2);
+                                            const unsigned char* at = sp + by / C::PITCH * (kTile * C::PITCH) + j * C::PITCH +
+                                                                      ((by % C::PITCH >> 4 ^ swz(j)) << 4) + (by & 15);
+                                            float v;
+                                            if (E4) {
+                                                const uint32_t hv = e4m3_lo(*at);
+                                                v = __half2float(__ushort_as_half((unsigned short)hv));
+                                            } else {
+                                                v = __half2float(*reinterpret_cast<const __half*>(at));
+                                            }
+                                            o[m][n][2 * i + c] += w * v;
+                                        }
+                                }
+                        }
+                    __syncwarp();
+                    if (dead[0] | dead[1])
+                        for (int c = lane; c < C::SUBB / 16; c += 32) {
+                            const int j = c * 16 / C::PITCH % kTile;
+                            if (dead[j >> 3] >> (4 * (j & 7)) & 1u)
+                                *reinterpret_cast<uint4*>(sp + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                }
                 fence_proxy_async_cta();             // the slot's next fill comes by TMA
                 __syncwarp();
             }
-            if (E4) {
+            base = v_lane + c_slot * C::SLOT;
 #pragma unroll
-                for (int m = 0; m < MT; m += 2) {
-                    uint32_t r0, r1, r2, r3;
-                    ldsm_x4_t(chunk(slot, (lane & 7) + ((lane >> 3) & 1) * 8, m + (lane >> 4)), r0, r1, r2, r3);
-                    r0 = __byte_perm(r0, 0, 0x3120);
-                    r1 = __byte_perm(r1, 0, 0x3120);
-                    r2 = __byte_perm(r2, 0, 0x3120);
-                    r3 = __byte_perm(r3, 0, 0x3120);
-                    const uint32_t a0[4] = {e4m3_lo(r0), e4m3_hi(r0), e4m3_lo(r1), e4m3_hi(r1)};
-                    const uint32_t a1[4] = {e4m3_lo(r2), e4m3_hi(r2), e4m3_lo(r3), e4m3_hi(r3)};
+            for (int m = 0; m < MT; m += E4 ? 2 : 1)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_16816(o[m][n], a0, ph[n][0], ph[n][1]);
-                        mma_16816(o[m + 1][n], a1, ph[n][0], ph[n][1]);
-                        mma_16816(o[m][n], a0, pl[n][0], pl[n][1]);
-                        mma_16816(o[m + 1][n], a1, pl[n][0], pl[n][1]);
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t r[4];
+                    ldsm_x4_t(at_chunk(base, u, E4 ? m : 2 * m), r[0], r[1], r[2], r[3]);
+                    if (E4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
+                        const uint32_t a0[4] = {e4m3_lo(r[0]), e4m3_hi(r[0]), e4m3_lo(r[1]), e4m3_hi(r[1])};
+                        const uint32_t a1[4] = {e4m3_lo(r[2]), e4m3_hi(r[2]), e4m3_lo(r[3]), e4m3_hi(r[3])};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma(o[m][n], a0, ph[u][n][0], ph[u][n][1]);
+                            mma(o[m + 1][n], a1, ph[u][n][0], ph[u][n][1]);
+                            mma(o[m][n], a0, pl[u][n][0], pl[u][n][1]);
+                            mma(o[m + 1][n], a1, pl[u][n][0], pl[u][n][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma(o[m][n], r, ph[u][n][0], ph[u][n][1]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma(o[m][n], r, pl[u][n][0], pl[u][n][1]);
                     }
                 }
-            } else {
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t af[4];
-                    ldsm_x4_t(chunk(slot, (lane & 7) + (lane >> 4) * 8, 2 * m + ((lane >> 3) & 1)), af[0], af[1], af[2],
-                              af[3]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16816(o[m][n], af, ph[n][0], ph[n][1]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16816(o[m][n], af, pl[n][0], pl[n][1]);
-                }
-            }
             pass_slot();
-            c_tile = (c_tile + 1) & 15;
+            c_tile = (c_tile + 1) % C::ENTRIES;
         }
 
         // ---- the piece's end: the four warps' states become one ---------------
@@ -711,8 +783,9 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(~0u, l[n][e], w);
-                // only NaN scores so far: a state all the same, so that they reach the result
-                if (mref[n][e] == -INFINITY && !(l[n][e] == 0.f)) mref[n][e] = 0.f;
+                // no weight: no key seen. Only NaN scores: a state all the same, so that they reach the result
+                if (l[n][e] == 0.f) mref[n][e] = -INFINITY;
+                else if (mref[n][e] == kNoRef) mref[n][e] = 0.f;
                 if (g == 0) state[warp * RT + n * 8 + 2 * t4 + e] = make_float2(mref[n][e], l[n][e]);
             }
         __syncthreads();
