@@ -91,15 +91,16 @@ struct Cfg {
     static constexpr int LIMIT = 233472 / CPS - 1024;       // shared memory of one CTA
     // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
     static constexpr bool QREG = HD * NT <= 256;
-    static constexpr int QPITCH = HD * 2 + (E4 ? 32 : 16);  // bytes: rows on different banks
+    static constexpr int QPITCH = HD * 2 + 16;              // bytes: rows on different banks
     static constexpr int QBYTES = QREG ? 0 : RT * QPITCH;
     static constexpr int CD = NT == 4 || HD * NT >= 512 ? 16 : 32;   // dims that the warps' states are added over at a time
     static constexpr int RED = kWarps * RT * (CD + 4) * 4;
     static constexpr int STATE = kWarps * RT * 8;
     static constexpr int ENTRIES = 8;                       // tiles requested and not used up, at most
     static constexpr int META = kWarps * ENTRIES * 32;
-    // alignment slack, buffers above, then barriers and the scan's words
-    static constexpr int FIXED = 1024 + RED + QBYTES + STATE + META + kWarps * 64 + 128;
+    static constexpr int VIEWS = 2 * RT * 8;
+    // alignment slack, buffers above, then barriers, walks and the scan's words
+    static constexpr int FIXED = 1024 + RED + QBYTES + STATE + META + VIEWS + kWarps * 64 + (kWarps + 2) * 64 + 128;
     // 32 keys a slot where three slots of them fit (K, V and the next K), else 16
     static constexpr int SUB = 3 * kWarps * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
     static constexpr int KT = kTile * SUB;                  // keys of a warp's tile
@@ -172,33 +173,76 @@ __device__ __forceinline__ int64_t seq_units(const AttnArgs& a, int b, int& n_rt
     return u;
 }
 
-// A walk over a CTA's share of the units: the pieces of segments it holds, and
-// inside a piece the tiles of one warp.
-template <int RT, int KT>
+// A walk over a CTA's share of the units: the piece of a segment it is at. In
+// shared memory: one for the CTA, two pieces deep, and one for each warp's
+// requests, which run ahead.
 struct Walk {
     Seg s;
-    int64_t left;       // units of the share from this piece on
+    int left;           // units of the share from this piece on
     int ua, ub;         // this piece's units within the segment
-    int t, t_end;       // the warp's next tile of the segment, and the piece's end
-    __device__ __forceinline__ void piece(int warp) {
-        ub = (int)min((int64_t)s.n_units, ua + left);
-        t = max(ua - 1, 0) * kWarps + warp;
-        t_end = min(max(ub - 1, 0) * kWarps, s.n_tiles);
-    }
-    // on to the next piece; false at the share's end
-    __device__ __forceinline__ bool next(const AttnArgs& a, int warp) {
-        left -= ub - ua;
-        if (left <= 0) return false;
-        seg_next<RT, KT>(s, a);
-        ua = 0;
-        piece(warp);
-        return true;
-    }
+    int more;           // 0: the share has ended
+    int seg_no;         // the segment's number in the whole list
+    int pad;
 };
+static_assert(sizeof(Walk) == 64, "walk");
+__device__ __forceinline__ int2 walk_tiles(const Walk& w, int warp) {
+    return make_int2(max(w.ua - 1, 0) * kWarps + warp, min(max(w.ub - 1, 0) * kWarps, w.s.n_tiles));
+}
+// What happens once a piece stays out of line: the loop over tiles is what the
+// instruction cache has to hold.
+template <int RT, int KT>
+__device__ __noinline__ void walk_next(Walk* w, const AttnArgs* a) {
+    Walk v = *w;
+    v.left -= v.ub - v.ua;
+    v.more = v.left > 0;
+    if (v.more) {
+        seg_next<RT, KT>(v.s, *a);
+        ++v.seg_no;
+        v.ua = 0;
+        v.ub = min(v.s.n_units, v.left);
+    }
+    *w = v;
+}
+// The warp's requests go on to its next piece with tiles: {next tile, end}, {0, 0} at the share's end.
+template <int RT, int KT>
+__device__ __noinline__ int2 request_next(Walk* w, const AttnArgs* a, int warp) {
+    for (;;) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) walk_next<RT, KT>(w, a);
+        __syncwarp();
+        if (!w->more) return make_int2(0, 0);
+        const int2 t = walk_tiles(*w, warp);
+        if (t.x < t.y) return t;
+    }
+}
+// Pages, and their scales, of the next 32 16-key steps of a warp, one a lane;
+// page -1: none, or a bad one (its keys are masked).
+struct Pages { int page; float ks, vs; };
+template <int KT, bool E4>
+__device__ __noinline__ Pages load_pages(const Walk* w, const AttnArgs* a, int t, int t_end) {
+    constexpr int SUB = KT / kTile;
+    const int lane = threadIdx.x & 31, tl = t + lane / SUB * kWarps;
+    const int key = (w->s.tile0 + tl) * KT + lane % SUB * kTile;
+    Pages r{-1, 0.f, 0.f};
+    if (tl < t_end && key < w->s.n_kv) {
+        const int page = __ldg(a->table + w->s.b * a->table_stride + (key >> a->page_shift));
+        if (page < 0 || page >= a->n_pages) {
+            atomicOr(a->status, kStatusInput);
+        } else {
+            r.page = page;
+            if (E4) {
+                r.ks = __ldg(a->k_scale + (int64_t)page * a->n_kv_head + w->s.h);
+                r.vs = __ldg(a->v_scale + (int64_t)page * a->n_kv_head + w->s.h);
+            }
+        }
+    }
+    return r;
+}
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, uint64_t ns) { return mbar_wait(bar, phase, ns); }
 
 template <int HD, int TYPE, int NT>
 __global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(HD, NT))
-paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = Cfg<HD, TYPE, NT>;
     constexpr int RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
     constexpr bool E4 = C::E4;
@@ -214,7 +258,10 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
     unsigned char* misc = q_sm + C::QBYTES + C::STATE;
     Entry* meta = reinterpret_cast<Entry*>(misc) + warp * C::ENTRIES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc + C::META) + warp * 8;
-    int64_t* scan = reinterpret_cast<int64_t*>(misc + C::META + kWarps * 64);            // [16]
+    Walk* cws = reinterpret_cast<Walk*>(misc + C::META + kWarps * 64);                    // [2]
+    Walk* pw = reinterpret_cast<Walk*>(misc + C::META + kWarps * 64 + 128 + warp * 64);
+    int64_t* scan = reinterpret_cast<int64_t*>(misc + C::META + kWarps * 64 + (kWarps + 2) * 64);   // [16]
+    int2* views = reinterpret_cast<int2*>(misc + C::META + kWarps * 64 + (kWarps + 2) * 64 + 128);  // [2][RT]
     const uint32_t ring_u = smem_addr(ring), bars_u = smem_addr(bars);
 
     if (lane == 0) {
@@ -229,147 +276,188 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- this CTA's share of the units ------------------------------------
+    // (the first 128 sequences are scanned as they are counted)
     const int cta = blockIdx.x;
-    int64_t mine = 0;
-    int mine_s = 0;              // segments
-    bool bad_any = false;
-    for (int b = tid; b < a.n_seq; b += kWarps * 32) {
-        int n_rt;
-        bool bad;
-        mine += seq_units<RT, KT>(a, b, n_rt, bad);
-        mine_s += n_rt;
-        bad_any |= bad;
+    int64_t u_b = 0, more_u = 0;
+    int s_b = 0, more_s = 0;     // units and segments of this thread's sequence, and of those behind the first 128
+    {
+        bool bad_any = false;
+        for (int b = tid; b < a.n_seq; b += kWarps * 32) {
+            int n_rt;
+            bool bad;
+            const int64_t u = seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head;
+            if (b == tid) {
+                u_b = u;
+                s_b = n_rt * a.n_kv_head;
+            } else {
+                more_u += u;
+                more_s += n_rt * a.n_kv_head;
+            }
+            bad_any |= bad;
+        }
+        if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
     }
-    if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        mine += __shfl_xor_sync(~0u, mine, o);
-        mine_s += __shfl_xor_sync(~0u, mine_s, o);
-    }
-    if (lane == 0) {
-        scan[warp] = mine;
-        scan[4 + warp] = mine_s;
-    }
-    __syncthreads();
-    const int64_t total = (scan[0] + scan[1] + scan[2] + scan[3]) * a.n_kv_head;
-    const int64_t n_cta = min((int64_t)gridDim.x, total);
-    if (cta == 0 && tid == 0)    // entries of split[] that this call writes
-        *a.n_split = (int)min((int64_t)kMaxCtas, a.split_by_segment ?
-                              (scan[4] + scan[5] + scan[6] + scan[7]) * a.n_kv_head : n_cta);
-    if (cta >= n_cta) return;
-    const int64_t u0 = total * cta / n_cta, u1 = total * (cta + 1) / n_cta;
-    Walk<RT, KT> cw;                 // what is consumed
-    int seg_no = 0;              // the segment's number in the whole list
-    int64_t base_u = 0;
-    int base_seg = 0;
-    for (int b0 = 0;; b0 += kWarps * 32) {
-        const int b = b0 + tid;
-        int n_rt = 0;
-        bool bad;
-        const int64_t u = b < a.n_seq ? seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head : 0;
-        int64_t inc = u;
-        int inc_s = n_rt * a.n_kv_head;
-        const int own_s = inc_s;
+    auto scan_warp = [&](int64_t& u, int& n) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(~0u, inc, o);
-            const int y = __shfl_up_sync(~0u, inc_s, o);
+            const int64_t x = __shfl_up_sync(~0u, u, o);
+            const int y = __shfl_up_sync(~0u, n, o);
             if (lane >= o) {
-                inc += x;
-                inc_s += y;
+                u += x;
+                n += y;
             }
         }
-        __syncthreads();
-        if (lane == 31) {
-            scan[warp] = inc;
-            scan[4 + warp] = inc_s;
-        }
-        __syncthreads();
-        int64_t off = base_u;
-        int off_s = base_seg;
-        for (int w = 0; w < warp; ++w) {
-            off += scan[w];
-            off_s += (int)scan[4 + w];
-        }
-        inc += off;
-        inc_s += off_s;
-        if (u > 0 && u0 >= inc - u && u0 < inc) {
-            scan[8] = b;
-            scan[9] = u0 - (inc - u);
-            scan[10] = inc_s - own_s;
-        }
-        base_u += scan[0] + scan[1] + scan[2] + scan[3];
-        base_seg += (int)(scan[4] + scan[5] + scan[6] + scan[7]);
-        __syncthreads();
-        if (u0 < base_u) break;
+    };
+    int64_t inc = u_b;
+    int inc_s = s_b;
+    scan_warp(inc, inc_s);
+    if (a.n_seq > kWarps * 32) scan_warp(more_u, more_s);
+    if (lane == 31) {
+        scan[warp] = inc;
+        scan[4 + warp] = inc_s;
+        scan[8 + warp] = more_u;
+        scan[12 + warp] = more_s;
     }
+    __syncthreads();
+    const int64_t first_u = scan[0] + scan[1] + scan[2] + scan[3];
+    const int first_s = (int)(scan[4] + scan[5] + scan[6] + scan[7]);
+    const int64_t total = first_u + scan[8] + scan[9] + scan[10] + scan[11];
+    const int n_cta = (int)min((int64_t)gridDim.x, total);
+    if (cta == 0 && tid == 0)    // entries of split[] that this call writes
+        *a.n_split = a.split_by_segment ? (int)min((int64_t)kMaxCtas, first_s + scan[12] + scan[13] + scan[14] + scan[15])
+                                        : n_cta;
+    if (cta >= n_cta) return;
+    // floor(total * i / n_cta), by 32-bit divisions where they do
+    auto share = [&](int i) -> int64_t {
+        if (total >> 31) return total * i / n_cta;
+        const uint32_t t = (uint32_t)total, n = n_cta, q = t / n, r = t - q * n;
+        return (int64_t)q * i + r * i / n;
+    };
+    const int64_t u0 = share(cta), u1 = share(cta + 1);
     {
-        int64_t rem = scan[9];
-        int n_rt;
-        bool bad;
-        const int b = (int)scan[8];
-        const int64_t per_head = seq_units<RT, KT>(a, b, n_rt, bad);
-        seg_seq<RT>(cw.s, a, b);
-        cw.s.h = (int)(rem / per_head);
-        rem -= cw.s.h * per_head;
-        for (cw.s.rt = 0;; ++cw.s.rt) {
-            seg_keys<RT, KT>(cw.s, a);
-            if (rem < cw.s.n_units) break;
-            rem -= cw.s.n_units;
+        for (int w = 0; w < warp; ++w) {
+            inc += scan[w];
+            inc_s += (int)scan[4 + w];
         }
-        seg_no = (int)scan[10] + cw.s.h * n_rt + cw.s.rt;
-        cw.ua = (int)rem;
-        cw.left = u1 - u0;
-        cw.piece(warp);
+        int64_t base_u = first_u;
+        int base_s = first_s;
+        if (tid == 0) cws[0].more = 0;
+        __syncthreads();         // the totals above are read
+        int b = tid;
+        for (;;) {
+            if (u_b > 0 && u0 >= inc - u_b && u0 < inc) {      // one thread of the block: the share starts in its sequence
+                Walk w;
+                int n_rt;
+                bool bad;
+                int64_t rem = u0 - (inc - u_b);
+                const int64_t per_head = u_b / a.n_kv_head;
+                seq_units<RT, KT>(a, b, n_rt, bad);
+                seg_seq<RT>(w.s, a, b);
+                w.s.h = rem >> 31 || per_head >> 31 ? (int)(rem / per_head) : (int)((uint32_t)rem / (uint32_t)per_head);
+                rem -= w.s.h * per_head;
+                for (w.s.rt = 0;; ++w.s.rt) {
+                    seg_keys<RT, KT>(w.s, a);
+                    if (rem < w.s.n_units || w.s.rt + 1 >= w.s.n_rt) break;
+                    rem -= w.s.n_units;
+                }
+                w.seg_no = inc_s - s_b + w.s.h * n_rt + w.s.rt;
+                w.ua = (int)rem;
+                w.left = (int)min(u1 - u0, (int64_t)0x7fffffff);
+                w.ub = min(w.s.n_units, w.ua + w.left);
+                w.more = w.s.n_rt > 0;
+                cws[0] = w;
+                for (int i = 0; i < kWarps; ++i) cws[2 + i] = w;     // the warps' own: they follow
+            }
+            if (u0 < base_u || b - tid >= a.n_seq) break;
+            // behind the first 128 sequences: the next 128
+            b += kWarps * 32;
+            int n_rt = 0;
+            bool bad;
+            u_b = b < a.n_seq ? seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head : 0;
+            s_b = n_rt * a.n_kv_head;
+            inc = u_b;
+            inc_s = s_b;
+            scan_warp(inc, inc_s);
+            __syncthreads();
+            if (lane == 31) {
+                scan[warp] = inc;
+                scan[4 + warp] = inc_s;
+            }
+            __syncthreads();
+            inc += base_u;
+            inc_s += base_s;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) {
+                    inc += scan[w];
+                    inc_s += (int)scan[4 + w];
+                }
+                base_u += scan[w];
+                base_s += (int)scan[4 + w];
+            }
+        }
     }
+    // For a piece's rows: the keys each sees, [y, x), and where it is read, Q rows
+    // to shared memory (positions of a 16-dim group in the order the MMA takes them).
+    auto q_row = [&](const Walk& w, int r) {
+        const int i = (w.s.rt * RT + r) / a.group, hh = w.s.rt * RT + r - i * a.group;
+        return a.q16 + (int64_t)(w.s.tok0 + i) * a.q_stride + (int64_t)(w.s.h * a.group + hh) * HD;
+    };
+    auto open_piece = [&](int which) {
+        const Walk& w = cws[which];
+        if (!w.more) return;
+        const int rows = min(RT, w.s.n_q * a.group - w.s.rt * RT);
+        if (tid < RT) {
+            int hi = w.s.n_kv, lo = 0;
+            if (a.causal) {
+                const int p = w.s.n_kv - w.s.n_q + (w.s.rt * RT + min(tid, rows - 1)) / a.group;
+                hi = min(hi, p + 1);
+                if (a.window > 0) lo = max(0, p + 1 - a.window);
+            }
+            views[which * RT + tid] = make_int2(hi, lo);
+        }
+        if (!C::QREG)
+            for (int i = tid; i < RT * (HD / 8); i += kWarps * 32) {
+                const int r = i / (HD / 8), c = i - r * (HD / 8);
+                const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4*>(q_row(w, r) + c * 8)) : make_uint4(0, 0, 0, 0);
+                unsigned char* dst = q_sm + r * C::QPITCH;
+                if (E4) {
+                    *reinterpret_cast<uint2*>(dst + (c >> 1) * 32 + (c & 1) * 8) = make_uint2(x.x, x.z);
+                    *reinterpret_cast<uint2*>(dst + (c >> 1) * 32 + 16 + (c & 1) * 8) = make_uint2(x.y, x.w);
+                } else {
+                    *reinterpret_cast<uint4*>(dst + c * 16) = x;
+                }
+            }
+    };
+    __syncthreads();
+    if (!cws[0].more) return;    // (only if the lengths change during the call)
 
     // ---- the warp's ring: slots q = 0, 1, ... hold K, V, K, V, ... of its tiles ----
-    Walk<RT, KT> pw = cw;            // what is requested
-    bool more = true;
+    int2 pt = walk_tiles(*pw, warp);   // the next tile to request of the piece, and its end
+    if (pt.x >= pt.y) pt = request_next<RT, KT>(pw, &a, warp);
     constexpr int BLK = 32 / SUB;  // tiles of a page block: a lane for each 16 keys
     int blk = BLK;               // tiles of the page block used up (BLK: load a new one)
-    int b_page = 0, p_page[SUB] = {};
-    float b_ks = 1.f, b_vs = 1.f;
+    Pages pb{};
+    int p_page[SUB] = {};
     int i_slot = 0, i_tile = 0;  // ring slot of the next request; its tile's number mod ENTRIES
     bool i_v = false;
     auto request = [&]() {
-        if (!more) return;
+        if (pt.x >= pt.y) return;                      // the share's end
         if (!i_v) {              // a new tile: its pages, and its scales for the consumer
-            while (pw.t >= pw.t_end) {
-                if (!pw.next(a, warp)) {
-                    more = false;
-                    return;
-                }
-                blk = BLK;
-            }
             if (blk == BLK) {
-                const int tl = pw.t + lane / SUB * kWarps;
-                const int key = (pw.s.tile0 + tl) * KT + lane % SUB * kTile;
-                b_page = -1;
-                b_ks = b_vs = 0.f;
-                if (tl < pw.t_end && key < pw.s.n_kv) {
-                    b_page = __ldg(a.table + pw.s.b * a.table_stride + (key >> a.page_shift));
-                    if (b_page < 0 || b_page >= a.n_pages) {
-                        b_page = -1;
-                        atomicOr(a.status, kStatusInput);
-                    } else if (E4) {
-                        b_ks = __ldg(a.k_scale + (int64_t)b_page * a.n_kv_head + pw.s.h);
-                        b_vs = __ldg(a.v_scale + (int64_t)b_page * a.n_kv_head + pw.s.h);
-                    }
-                }
+                pb = load_pages<KT, E4>(pw, &a, pt.x, pt.y);
                 blk = 0;
             }
-            Entry e;
-            e.bad = 0u;
+            uint32_t bad = 0u;
+            float ks[SUB], vs[SUB];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                p_page[u] = __shfl_sync(~0u, b_page, blk * SUB + u);
+                p_page[u] = __shfl_sync(~0u, pb.page, blk * SUB + u);
                 if (E4) {
-                    e.ks[u] = __shfl_sync(~0u, b_ks, blk * SUB + u);
-                    e.vs[u] = __shfl_sync(~0u, b_vs, blk * SUB + u);
+                    ks[u] = __shfl_sync(~0u, pb.ks, blk * SUB + u);
+                    vs[u] = __shfl_sync(~0u, pb.vs, blk * SUB + u);
                 }
                 // no such page: page 0, which exists, is read in its place and its keys are masked
-                if (p_page[u] < 0) e.bad |= 1u << u;
+                if (p_page[u] < 0) bad |= 1u << u;
                 p_page[u] = max(p_page[u], 0);
             }
             ++blk;
@@ -378,26 +466,29 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                 if (E4) {
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
-                        m.ks[u] = e.ks[u];
-                        m.vs[u] = e.vs[u];
+                        m.ks[u] = ks[u];
+                        m.vs[u] = vs[u];
                     }
                 }
-                m.bad = e.bad;
+                m.bad = bad;
             }
         }
         if (lane == 0) {
             const uint32_t bar = bars_u + 8 * i_slot;
-            const int key = (pw.s.tile0 + pw.t) * KT, rows = (1 << a.page_shift) - 1;
+            const int key = (pw->s.tile0 + pt.x) * KT, in_page = (1 << a.page_shift) - 1, head = pw->s.h;
             mbar_expect_tx(bar, C::SLOT);
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
-                tma_load_5d(ring_u + i_slot * C::SLOT + u * C::SUBB, i_v ? &v_map : &k_map, (key + u * kTile) & rows,
-                            pw.s.h, p_page[u], bar);
+                tma_load_5d(ring_u + i_slot * C::SLOT + u * C::SUBB, i_v ? &v_map : &k_map, (key + u * kTile) & in_page,
+                            head, p_page[u], bar);
         }
         if (++i_slot == NS) i_slot = 0;
         if (i_v) {
-            pw.t += kWarps;
             i_tile = (i_tile + 1) % C::ENTRIES;
+            if ((pt.x += kWarps) >= pt.y) {
+                pt = request_next<RT, KT>(pw, &a, warp);
+                blk = BLK;
+            }
         }
         i_v = !i_v;
     };
@@ -409,8 +500,9 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
     uint32_t c_phase = 0;
     bool timeout = false;
     auto wait_slot = [&]() {
+        if (mbar_test(bars_u + 8 * c_slot, c_phase)) return;
         // after one wait that gave up the others do so soon: the kernel ends
-        if (!mbar_wait(bars_u + 8 * c_slot, c_phase, timeout ? 20000ull : kWaitNs)) timeout = true;
+        if (!wait_long(bars_u + 8 * c_slot, c_phase, timeout ? 20000ull : kWaitNs)) timeout = true;
     };
     auto pass_slot = [&]() {     // this slot is used up: request what comes NS slots later
         __syncwarp();
@@ -434,41 +526,20 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
         return (base ^ ((c % CPB) << 4)) + sub * C::SUBB + c / CPB * (kTile * C::PITCH);
     };
 
-    for (;;) {
-        // ---- a piece: its rows, their views and their Q fragments -----------
-        const int rows = min(RT, cw.s.n_q * a.group - cw.s.rt * RT), row0 = cw.s.rt * RT;
-        int lim[NT][2], low[NT][2];
-        int min_lim = 0x7fffffff, max_low = 0;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = n * 8 + 2 * t4 + e;
-                lim[n][e] = cw.s.n_kv;
-                low[n][e] = 0;
-                if (r < rows && a.causal) {
-                    const int p = cw.s.n_kv - cw.s.n_q + (row0 + r) / a.group;   // the key of the row's own token
-                    lim[n][e] = min(lim[n][e], p + 1);
-                    if (a.window > 0) low[n][e] = max(0, p + 1 - a.window);
-                }
-                min_lim = min(min_lim, lim[n][e]);
-                max_low = max(max_low, low[n][e]);
-            }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            min_lim = min(min_lim, __shfl_xor_sync(~0u, min_lim, o));
-            max_low = max(max_low, __shfl_xor_sync(~0u, max_low, o));
-        }
-        auto q_row = [&](int r) {
-            const int i = (row0 + r) / a.group, hh = (row0 + r) - i * a.group;
-            return a.q16 + (int64_t)(cw.s.tok0 + i) * a.q_stride + (int64_t)(cw.s.h * a.group + hh) * HD;
-        };
+    open_piece(0);
+    __syncthreads();
+    for (int which = 0;; which ^= 1) {
+        // ---- a piece: its rows and their Q fragments --------------------------
+        const Walk& cw = cws[which];
+        const int2* view = views + which * RT;
+        const int rows = min(RT, cw.s.n_q * a.group - cw.s.rt * RT);
+        const int min_lim = view[0].x, max_low = view[RT - 1].y;       // (rows behind the last see what it sees)
         uint32_t qf[C::QREG ? MT : 1][NT][2];
         if (C::QREG) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int r = n * 8 + g;
-                const __half* src = q_row(min(r, rows - 1));
+                const __half* src = q_row(cw, min(r, rows - 1));
 #pragma unroll
                 for (int kk = 0; kk < MT; ++kk) {
                     if (E4) {
@@ -483,28 +554,20 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                     }
                 }
             }
-        } else {
-            for (int w = tid; w < RT * (HD / 8); w += kWarps * 32) {
-                const int r = w / (HD / 8), c = w - r * (HD / 8);
-                const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4*>(q_row(r) + c * 8)) : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4*>(q_sm + r * C::QPITCH + c * 16) = x;
-            }
-            __syncthreads();
         }
-        auto q_frag = [&](int kk, int n, uint32_t& b0, uint32_t& b1) {
+        const uint32_t q_lane = smem_addr(q_sm) + ((lane & 7) + (lane >> 4) * 8) * C::QPITCH + ((lane >> 3) & 1) * 16;
+        // B fragments of step kk for all row blocks
+        auto q_frags = [&](int kk, uint32_t (*b)[2]) {
             if (C::QREG) {
-                b0 = qf[kk][n][0];
-                b1 = qf[kk][n][1];
-            } else {
-                const unsigned char* src = q_sm + (n * 8 + g) * C::QPITCH + kk * 32;
-                if (E4) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(src + t4 * 8);
-                    b0 = x.x;
-                    b1 = x.y;
-                } else {
-                    b0 = *reinterpret_cast<const uint32_t*>(src + t4 * 4);
-                    b1 = *reinterpret_cast<const uint32_t*>(src + 16 + t4 * 4);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    b[n][0] = qf[kk][n][0];
+                    b[n][1] = qf[kk][n][1];
                 }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; n += 2)
+                    ldsm_x4(q_lane + n * 8 * C::QPITCH + kk * 32, b[n][0], b[n][1], b[n + 1][0], b[n + 1][1]);
             }
         };
 
@@ -519,7 +582,9 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
             for (int m = 0; m < MT; ++m) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
         }
 
-        for (; cw.t < cw.t_end; cw.t += kWarps) {
+        const int2 tiles = walk_tiles(cw, warp);
+        const int tile0 = cw.s.tile0;
+        for (int t = tiles.x; t < tiles.y; t += kWarps) {
             // ---- S^T = K Q^T ------------------------------------------------
             wait_slot();
             const Entry& en = meta[c_tile];
@@ -535,11 +600,8 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
 #pragma unroll
             for (int kk = 0; kk < MT; kk += E4 ? 2 : 1) {
                 uint32_t qa[NT][2], qb[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    q_frag(kk, n, qa[n][0], qa[n][1]);
-                    if (E4) q_frag(kk + 1, n, qb[n][0], qb[n][1]);
-                }
+                q_frags(kk, qa);
+                if (E4) q_frags(kk + 1, qb);
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     uint32_t r[4];
@@ -575,7 +637,7 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
             pass_slot();
 
             // ---- softmax weights: exponents x - mref first -------------------
-            const int key0 = (cw.s.tile0 + cw.t) * KT;
+            const int key0 = (tile0 + t) * KT;
             const bool edge = bad != 0u || key0 + KT > min_lim || key0 < max_low;
             bool up = false;
             float y[SUB][NT][4];
@@ -585,14 +647,26 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[u][n][e], sc[u], -mref[n][e & 1]);
-                        if (edge) {
-                            const int j = key0 + u * kTile + g + (e >> 1) * 8;
-                            if ((bad >> u & 1u) || j >= lim[n][e & 1] || j < low[n][e & 1]) x = -INFINITY;
-                        }
-                        y[u][n][e] = x;
-                        up |= x > kAbove;
+                        y[u][n][e] = fmaf(s[u][n][e], sc[u], -mref[n][e & 1]);
+                        up |= y[u][n][e] > kAbove;
                     }
+            if (__builtin_expect(edge, 0)) {
+                up = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int2 see = view[n * 8 + 2 * t4 + c];
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int e = c; e < 4; e += 2) {
+                                const int j = key0 + u * kTile + g + (e >> 1) * 8;
+                                if ((bad >> u & 1u) || j >= see.x || j < see.y) y[u][n][e] = -INFINITY;
+                                up |= y[u][n][e] > kAbove;
+                            }
+                    }
+            }
             const bool vup = E4 && vmax > vref;
             if (__any_sync(~0u, up) || vup) {
                 float va = 1.f;
@@ -661,45 +735,36 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
 
             // ---- O^T += V^T P^T ------------------------------------------------
             wait_slot();
-            if (edge) {
+            if (__builtin_expect(edge, 0)) {
                 // A masked key has weight 0, but 0 * inf and 0 * NaN are NaN: rows
                 // of V that no query row sees are cleared (they may lie behind the
                 // sequence's end), and non-finite rows seen by some rows only are
                 // added here for those rows and then cleared.
-#pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     unsigned char* sp = ring + c_slot * C::SLOT + u * C::SUBB;
-                    unsigned dead[2], part[2];           // bit 4g: key g (+ 8) unseen; seen by some rows only
-#pragma unroll
+                    const bool no_page = bad >> u & 1u;
                     for (int e = 0; e < 2; ++e) {
+                        const int j0 = key0 + u * kTile + e * 8;
                         bool vis = false, msk = false;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                if (n * 8 + 2 * t4 + c < rows) {
-                                    const int j = key0 + u * kTile + g + e * 8;
-                                    const bool m = (bad >> u & 1u) || j >= lim[n][c] || j < low[n][c];
-                                    vis |= !m;
-                                    msk |= m;
-                                }
+                        for (int r = 2 * t4; r < rows; r += (r & 1) ? 7 : 1) {
+                            const int2 see = view[r];
+                            const bool m = no_page || j0 + g >= see.x || j0 + g < see.y;
+                            vis |= !m;
+                            msk |= m;
+                        }
                         unsigned v = __ballot_sync(~0u, vis), m = __ballot_sync(~0u, msk);
                         v |= v >> 2;
                         v |= v >> 1;
                         m |= m >> 2;
                         m |= m >> 1;
-                        dead[e] = ~v & 0x11111111u;
-                        part[e] = v & m & 0x11111111u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        while (part[e]) {
-                            const int bit = __ffs(part[e]) - 1, j = (bit >> 2) + e * 8;
-                            part[e] &= part[e] - 1;
+                        unsigned dead = ~v & 0x11111111u, part = v & m & 0x11111111u;    // bit 4i: key j0 + i
+                        for (; part; part &= part - 1) {
+                            const int j = (__ffs(part) - 1) >> 2;
+                            const unsigned char* row = sp + (j + e * 8) * C::PITCH;
                             bool weird = false;
                             for (int c = lane; c < C::ROWB / 4; c += 32) {
                                 const uint32_t x = *reinterpret_cast<const uint32_t*>(
-                                    sp + (c * 4) / C::PITCH * (kTile * C::PITCH) + j * C::PITCH + (c * 4) % C::PITCH);
+                                    row + c * 4 / C::PITCH * (kTile * C::PITCH) + c * 4 % C::PITCH);
                                 if (E4) {
                                     const uint32_t z = x & 0x7f7f7f7fu;
                                     weird |= (z & 0xffu) == 0x7fu || (z >> 8 & 0xffu) == 0x7fu ||
@@ -709,20 +774,25 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                                 }
                             }
                             if (!__any_sync(~0u, weird)) continue;
-                            dead[e] |= 1u << bit;
+                            dead |= 1u << (4 * j);
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) {
-                                    const float x = __shfl_sync(~0u, y[u][n][2 * e + c], (j & 7) * 4 + t4);
+                                    float x = e ? y[0][n][2 + c] : y[0][n][c], vsc = vs[0];
+                                    if (SUB == 2 && u) {
+                                        x = e ? y[SUB - 1][n][2 + c] : y[SUB - 1][n][c];
+                                        vsc = vs[SUB - 1];
+                                    }
+                                    x = __shfl_sync(~0u, x, j * 4 + t4);
                                     if (x == -INFINITY) continue;
-                                    const float w = ex2(x) * vs[u];
+                                    const float w = ex2(x) * vsc;
 #pragma unroll
                                     for (int m = 0; m < MT; ++m)
 #pragma unroll
                                         for (int i = 0; i < 2; ++i) {
                                             const int d = m * 16 + (E4 ? 2 * g + i : g + 8 * i), by = d * (E4 ? 1 : 2);
-                                            const unsigned char* at = sp + by / C::PITCH * (kTile * C::PITCH) + j * C::PITCH +
+                                            const unsigned char* at = row + by / C::PITCH * (kTile * C::PITCH) +
                                                                       ((by % C::PITCH >> 4 ^ swz(j)) << 4) + (by & 15);
                                             float v;
                                             if (E4) {
@@ -735,13 +805,15 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                                         }
                                 }
                         }
-                    __syncwarp();
-                    if (dead[0] | dead[1])
-                        for (int c = lane; c < C::SUBB / 16; c += 32) {
-                            const int j = c * 16 / C::PITCH % kTile;
-                            if (dead[j >> 3] >> (4 * (j & 7)) & 1u)
-                                *reinterpret_cast<uint4*>(sp + c * 16) = make_uint4(0, 0, 0, 0);
-                        }
+                        __syncwarp();
+                        if (dead)
+                            for (int c = lane; c < C::SUBB / 32; c += 32) {    // the 8 rows of this half, box by box
+                                const int box = c / (C::PITCH / 2), at = c % (C::PITCH / 2) * 16;
+                                if (dead >> (4 * (at / C::PITCH)) & 1u)
+                                    *reinterpret_cast<uint4*>(sp + box * (kTile * C::PITCH) + e * 8 * C::PITCH + at) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
+                    }
                 }
                 fence_proxy_async_cta();             // the slot's next fill comes by TMA
                 __syncwarp();
@@ -788,6 +860,24 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                 else if (mref[n][e] == kNoRef) mref[n][e] = 0.f;
                 if (g == 0) state[warp * RT + n * 8 + 2 * t4 + e] = make_float2(mref[n][e], l[n][e]);
             }
+        const bool whole = cw.ua == 0 && cw.ub == cw.s.n_units;
+        // state slot: 2*cta + 1 for a segment that goes on in the next CTA from its start here, else 2*cta
+        const int part = 2 * cta + (cw.ua == 0 && !whole ? 1 : 0);
+        const int row0 = cw.s.rt * RT, tok0 = cw.s.tok0, head0 = cw.s.h * a.group;
+        if (tid == 0) {
+            // the merge kernel's entry: who holds states of this segment
+            const bool starts = cw.ua == 0, last_piece = cw.left <= cw.ub - cw.ua;
+            Split sp{cta, -1, tok0, row0, rows, cw.s.h, {0, 0}};
+            if (starts && !whole) {
+                const int64_t end_u = u1 - cw.left + cw.s.n_units;     // behind the segment's last unit
+                sp.last = total >> 31 ? (int)((end_u * n_cta - 1) / total)
+                                      : (int)(((uint64_t)end_u * n_cta - 1) / (uint64_t)total);
+            }
+            const int at = a.split_by_segment ? cw.seg_no : cta;
+            if ((a.split_by_segment ? starts : last_piece) && at < kMaxCtas) a.split[at] = sp;
+            cws[which ^ 1] = cw;
+            walk_next<RT, KT>(&cws[which ^ 1], &a);
+        }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -804,9 +894,6 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                     o[mm][n][2 + e] = f == 0.f ? 0.f : o[mm][n][2 + e] * f;
                 }
             }
-        const bool whole = cw.ua == 0 && cw.ub == cw.s.n_units;
-        // state slot: 2*cta + 1 for a segment that goes on in the next CTA from its start here, else 2*cta
-        const int part = 2 * cta + (cw.ua == 0 && !whole ? 1 : 0);
 #pragma unroll
         for (int c0 = 0; c0 < HD; c0 += C::CD) {
             if (c0) __syncthreads();
@@ -843,7 +930,7 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                     x.z *= inv;
                     x.w *= inv;
                     const int i = (row0 + r) / a.group, hh = (row0 + r) - i * a.group;
-                    float* dst = a.out + ((int64_t)(cw.s.tok0 + i) * a.n_kv_head * a.group + cw.s.h * a.group + hh) * HD;
+                    float* dst = a.out + ((int64_t)(tok0 + i) * a.n_kv_head * a.group + head0 + hh) * HD;
                     *reinterpret_cast<float4*>(dst + c0 + d) = x;
                 } else {
                     *reinterpret_cast<float4*>(a.part_o + ((int64_t)part * RT + r) * HD + c0 + d) = x;
@@ -851,21 +938,9 @@ paged_attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map, c
                 }
             }
         }
-        // the merge kernel's entry: who holds states of this segment
-        if (tid == 0) {
-            const bool starts = cw.ua == 0, cut = starts && !whole;
-            if (starts && (a.split_by_segment || (cut || cw.left <= cw.ub - cw.ua))) {
-                const int64_t last_u = u1 - cw.left + cw.s.n_units - 1;      // the segment's last unit
-                const int last = cut ? (int)(((last_u + 1) * n_cta - 1) / total) : -1;
-                const int at = a.split_by_segment ? seg_no : cta;
-                if (at < kMaxCtas) a.split[at] = Split{cta, last, cw.s.tok0, row0, rows, cw.s.h, {0, 0}};
-            } else if (!a.split_by_segment && cw.left <= cw.ub - cw.ua) {
-                a.split[cta] = Split{0, -1, 0, 0, 0, 0, {0, 0}};
-            }
-        }
+        open_piece(which ^ 1);
         __syncthreads();
-        ++seg_no;
-        if (!cw.next(a, warp)) break;
+        if (!cws[which ^ 1].more) break;
     }
     if (timeout) atomicOr(a.status, kStatusTimeout);
 }
