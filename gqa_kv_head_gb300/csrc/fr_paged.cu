@@ -17,33 +17,39 @@ using sm100::ex2;
 // The states (m, l, O) of one split segment's row become its output row:
 //   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p,
 // in the order of the pieces, whatever order they were computed in. One block
-// per (segment, row): thread = (4 columns, group of states). Latency-bound: the
-// loads of the first kAhead states of each group go out before the weights are
-// known. Blocks of unsplit segments leave at once.
-constexpr int kAhead = 4;
+// per (segment, row, 64 dims): thread = (4 dims, group of states). Bound by
+// latency, and by how slowly one SM reads lines that others have just written,
+// so a row is spread over blocks and the first kAhead states of each group are
+// asked for before the weights are known. Blocks of unsplit segments leave at
+// once.
+constexpr int kAhead = 4, kMergeCols = 16, kMergeThreads = 512;
 
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kMergeThreads)
 paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_split, const float* __restrict__ part_o,
                    const float2* __restrict__ part_ml, float* __restrict__ out, int row_tile, int hd, int group,
                    int n_kv_head) {
-    __shared__ float wt[kMaxCtas], red_l[32], red_m[32];
-    __shared__ float4 red[1024];
+    __shared__ float wt[kMaxCtas], red_l[kMergeThreads / 32], red_m[kMergeThreads / 32];
+    __shared__ float4 red[kMergeThreads];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, row = blockIdx.y;
-    const int n_entries = *n_split;
-    const Split s = split[blockIdx.x];
-    if ((int)blockIdx.x >= n_entries || s.last < s.first || row >= s.rows) return;
-    const int n = s.last - s.first + 1, cols = hd / 4, groups = blockDim.x / cols, c = tid % cols, gi = tid / cols;
-    auto slot = [&](int p) { return (int64_t)(2 * (s.first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
+    const int n_entries = __ldcg(n_split);
+    const int4 s0 = __ldcg(reinterpret_cast<const int4*>(split + blockIdx.x));
+    const int2 s1 = __ldcg(reinterpret_cast<const int2*>(split + blockIdx.x) + 2);
+    const int first = s0.x, n = s0.y - first + 1, tok0 = s0.z, row0 = s0.w, rows = s1.x, head = s1.y;
+    if ((int)blockIdx.x >= n_entries || n < 1 || row >= rows) return;
+    const int groups = blockDim.x / kMergeCols, c = blockIdx.z * kMergeCols + tid % kMergeCols, gi = tid / kMergeCols;
+    auto slot = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
     float4 ahead[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
         const int p = gi + i * groups;
-        ahead[i] = p < n ? *reinterpret_cast<const float4*>(part_o + slot(p) * hd + c * 4) : make_float4(0, 0, 0, 0);
+        ahead[i] = p < n ? __ldcg(reinterpret_cast<const float4*>(part_o + slot(p) * hd) + c) : make_float4(0, 0, 0, 0);
     }
-    float m = -INFINITY;
-    for (int p = tid; p < n; p += blockDim.x) m = fmaxf(m, part_ml[slot(p)].x);
+    // every thread that holds a state's (m, l) keeps it; more than one for each only beyond 512 states
+    const float2 mine = tid < n ? __ldcg(part_ml + slot(tid)) : make_float2(-INFINITY, 0.f);
+    float m = mine.x;
+    for (int p = tid + blockDim.x; p < n; p += blockDim.x) m = fmaxf(m, __ldcg(part_ml + slot(p)).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
     if (lane == 0) red_m[warp] = m;
@@ -52,7 +58,7 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
     for (int w = 1; w < warps; ++w) m = fmaxf(m, red_m[w]);
     float l = 0.f;
     for (int p = tid; p < n; p += blockDim.x) {
-        const float2 ml = part_ml[slot(p)];
+        const float2 ml = p == tid ? mine : __ldcg(part_ml + slot(p));
         const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
         wt[p] = w;
         l += w == 0.f ? 0.f : w * ml.y;
@@ -61,8 +67,6 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
     if (lane == 0) red_l[warp] = l;
     __syncthreads();
-    l = 0.f;
-    for (int w = 0; w < warps; ++w) l += red_l[w];
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](int p, const float4& y) {
         const float w = wt[p];
@@ -77,20 +81,22 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
         if (gi + i * groups < n) add(gi + i * groups, ahead[i]);
 #pragma unroll 8
     for (int p = gi + kAhead * groups; p < n; p += groups)
-        add(p, *reinterpret_cast<const float4*>(part_o + slot(p) * hd + c * 4));
+        add(p, __ldcg(reinterpret_cast<const float4*>(part_o + slot(p) * hd) + c));
     red[tid] = x;
     __syncthreads();
     if (gi) return;
+    l = 0.f;
+    for (int w = 0; w < warps; ++w) l += red_l[w];
     for (int i = 1; i < groups; ++i) {
-        const float4 y = red[i * cols + c];
+        const float4 y = red[i * kMergeCols + tid];
         x.x += y.x;
         x.y += y.y;
         x.z += y.z;
         x.w += y.w;
     }
     const float inv = m == -INFINITY ? 0.f : 1.f / l;
-    const int i = (s.row0 + row) / group, hh = s.row0 + row - i * group;
-    float* dst = out + ((int64_t)(s.tok0 + i) * n_kv_head * group + s.head * group + hh) * hd + c * 4;
+    const int i = (row0 + row) / group, hh = row0 + row - i * group;
+    float* dst = out + ((int64_t)(tok0 + i) * n_kv_head * group + head * group + hh) * hd + c * 4;
     *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
 }
 
@@ -288,7 +294,9 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     const int64_t segs = (per_tok < per_seq ? per_tok : per_seq) * kv->n_kv_head;
     const int64_t cap_units = (((int64_t)bt->max_pages << kv->page_shift) + kUnit - 1) / kUnit;
     int64_t ctas = ctas_for(kv->hd, nt, sms);
-    if (segs * (cap_units + 1) < ctas) ctas = segs * (cap_units + 1);
+    const int64_t cap = segs * (cap_units + kSegCost);
+    if (cap > 0x7fffffff) return FR_ERR_UNSUPPORTED;
+    if (cap < ctas) ctas = cap;
 
     char* w = reinterpret_cast<char*>(workspace);
     AttnArgs a;
@@ -318,6 +326,16 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     a.window = window;
     a.split_by_segment = segs <= ctas ? 1 : 0;
     a.scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
+    // The merge kernel leaves the SMs' memory split as the attention kernel needs
+    // it: an SM that still runs merge blocks of the call before would otherwise
+    // take one attention CTA less, for as long as that kernel runs
+    static unsigned long long done = 0ull;
+    if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev & 1ull)) {
+        if (cudaFuncSetAttribute(paged_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+            return FR_ERR_CUDA;
+        if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
+    }
     const fr_status st = kv->type == FR_KV_E4M3 ? launch_attn_e4m3(*kv, a, nt, (int)ctas, stream)
                                                 : launch_attn_f16(*kv, a, nt, (int)ctas, stream);
     if (st != FR_OK) return st;
@@ -325,12 +343,12 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     const int64_t rows = (int64_t)G * bt->n_tok < rt ? (int64_t)G * bt->n_tok : rt;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(a.split_by_segment ? segs : ctas), (unsigned)rows);
-    // threads for the states that a segment has when all are as long: kAhead for each group of hd/4
+    cfg.gridDim = dim3((unsigned)(a.split_by_segment ? segs : ctas), (unsigned)rows, (unsigned)(kv->hd / (4 * kMergeCols)));
+    // threads for the states that a segment has when all are as long: kAhead for each group
     const int64_t usual = bt->n_tok < bt->n_seq ? bt->n_tok : bt->n_seq * ((avg + rt - 1) / rt);
-    const int64_t states = ctas / (usual * kv->n_kv_head) + 2;
-    int64_t threads = (states + kAhead - 1) / kAhead * (kv->hd / 4);
-    cfg.blockDim = dim3((unsigned)(threads < 64 ? 64 : threads > 1024 ? 1024 : threads));
+    const int64_t groups = (ctas / (usual * kv->n_kv_head) + 2 + kAhead - 1) / kAhead;
+    int64_t threads = (groups * kMergeCols + 31) / 32 * 32;
+    cfg.blockDim = dim3((unsigned)(threads > kMergeThreads ? kMergeThreads : threads));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -20,6 +20,7 @@ constexpr int kUnit = kWarps * kTile;  // keys of one unit of work at least: a t
 __host__ __device__ constexpr int ctas_per_sm(int hd, int nt) { return nt == 1 && hd <= 128 ? 4 : 2; }
 constexpr int kMaxCtas = 640;        // attention CTAs at most: the workspace holds two split states for each
 constexpr int kMaxSeq = 65536;
+constexpr int kSegCost = 2;          // units that a segment's start and end count for in the work split
 constexpr size_t kWsHeader = 1024;   // [0, 4): status word, as in the other workspaces
 
 // What fr_paged_kv holds, in the library's own terms.
@@ -76,7 +77,8 @@ struct SeqInfo {
 __device__ __forceinline__ SeqInfo seq_info(const int32_t* tok_start, const int32_t* kv_len, int b, int n_tok,
                                             int max_pages, int page_shift) {
     SeqInfo s;
-    const int t0 = __ldg(tok_start + b), t1 = __ldg(tok_start + b + 1), n = __ldg(kv_len + b);
+    // (past L1: the kernel before may have written them while this one was starting)
+    const int t0 = __ldcg(tok_start + b), t1 = __ldcg(tok_start + b + 1), n = __ldcg(kv_len + b);
     const int64_t most = (int64_t)max_pages << page_shift;
     s.bad = t0 < 0 || t1 < t0 || t1 > n_tok || n < 0 || n > most;
     s.tok0 = t0;

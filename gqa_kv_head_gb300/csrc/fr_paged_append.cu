@@ -147,7 +147,7 @@ kv_append_paged_kernel(const AppendArgs a, const __grid_constant__ RopeTable tb)
     if (!found) return;
     const int b = sc[8], first = sc[10], last = first + sc[12];          // cache rows [first, last) are new
     const int pi = (first >> a.page_shift) + sc[9];                      // page of the sequence
-    const int page = __ldg(a.table + b * a.table_stride + pi);
+    const int page = __ldcg(a.table + b * a.table_stride + pi);
     if (page < 0 || page >= a.n_pages) {
         if (tid == 0 && a.status) atomicOr(a.status, kStatusInput);
         return;

@@ -90,17 +90,16 @@ struct Cfg {
     static constexpr int CPS = ctas_per_sm(HD, NT);
     static constexpr int LIMIT = 233472 / CPS - 1024;       // shared memory of one CTA
     // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
+    // Q rows lie in shared memory; up to 64 registers of fragments are kept from them for a piece
     static constexpr bool QREG = HD * NT <= 256;
     static constexpr int QPITCH = HD * 2 + 16;              // bytes: rows on different banks
-    static constexpr int QBYTES = QREG ? 0 : RT * QPITCH;
-    static constexpr int CD = NT == 4 || HD * NT >= 512 ? 16 : 32;   // dims that the warps' states are added over at a time
-    static constexpr int RED = kWarps * RT * (CD + 4) * 4;
+    static constexpr int QBYTES = RT * QPITCH;
     static constexpr int STATE = kWarps * RT * 8;
     static constexpr int ENTRIES = 8;                       // tiles requested and not used up, at most
     static constexpr int META = kWarps * ENTRIES * 32;
     static constexpr int VIEWS = 2 * RT * 8;
-    // alignment slack, buffers above, then barriers, walks and the scan's words
-    static constexpr int FIXED = 1024 + RED + QBYTES + STATE + META + VIEWS + kWarps * 64 + (kWarps + 2) * 64 + 128;
+    // alignment slack, buffers above, then barriers, walks, scan words and the warps' V scales
+    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + kWarps * 64 + (kWarps + 2) * 64 + 128 + 16;
     // 32 keys a slot where three slots of them fit (K, V and the next K), else 16
     static constexpr int SUB = 3 * kWarps * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
     static constexpr int KT = kTile * SUB;                  // keys of a warp's tile
@@ -109,6 +108,9 @@ struct Cfg {
     static constexpr int NS = NS_ > 8 ? 8 : NS_;            // slots of a warp's ring
     static constexpr int SMEM = FIXED + NS * kWarps * SLOT;
     static_assert(NS >= 3, "ring");
+    // rows of a warp's O^T that one slot holds in fp32: the epilogue's chunk
+    static constexpr int CNT = SLOT / (HD * 32) < NT ? SLOT / (HD * 32) : NT;
+    static_assert(CNT >= 1 && NT % CNT == 0, "epilogue chunk");
 };
 
 // One (sequence, KV head, row tile): its rows, and its keys as 16-key tiles.
@@ -120,18 +122,20 @@ struct Seg {
 
 template <int RT, int KT>
 __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
-    const int r0 = s.rt * RT, r1 = min(s.n_q * a.group, r0 + RT) - 1;
     int hi = s.n_kv, lo = 0;
     if (a.causal) {
+        // the tile's first and last token; one row tile holds all of most sequences
+        const int i0 = s.rt == 0 ? 0 : s.rt * RT / a.group;
+        const int i1 = s.rt == s.n_rt - 1 ? s.n_q - 1 : (s.rt * RT + RT - 1) / a.group;
         const int first = s.n_kv - s.n_q;
-        hi = min(hi, first + r1 / a.group + 1);
-        if (a.window > 0) lo = max(0, first + r0 / a.group - a.window + 1);
+        hi = min(hi, first + i1 + 1);
+        if (a.window > 0) lo = max(0, first + i0 - a.window + 1);
     }
     s.tile0 = lo / KT;
     s.n_tiles = hi > lo ? (hi + KT - 1) / KT - s.tile0 : 0;
-    // a segment's start and end cost about as much as a unit of its keys: it
-    // counts one more, ahead of them (rows without keys still get their zeros)
-    s.n_units = 1 + (s.n_tiles + kWarps - 1) / kWarps;
+    // a segment's start and end cost a CTA as much as about two units of its
+    // keys: it counts those ahead of them (rows without keys still get their zeros)
+    s.n_units = kSegCost + (s.n_tiles + kWarps - 1) / kWarps;
 }
 template <int RT>
 __device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
@@ -161,11 +165,11 @@ __device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
 }
 // Units of all segments of sequence b for one KV head.
 template <int RT, int KT>
-__device__ __forceinline__ int64_t seq_units(const AttnArgs& a, int b, int& n_rt, bool& bad) {
+__device__ __forceinline__ int seq_units(const AttnArgs& a, int b, int& n_rt, bool& bad) {
     Seg s;
     bad = seg_seq<RT>(s, a, b);
     n_rt = s.n_rt;
-    int64_t u = 0;
+    int u = 0;
     for (s.rt = 0; s.rt < s.n_rt; ++s.rt) {
         seg_keys<RT, KT>(s, a);
         u += s.n_units;
@@ -186,7 +190,7 @@ struct Walk {
 };
 static_assert(sizeof(Walk) == 64, "walk");
 __device__ __forceinline__ int2 walk_tiles(const Walk& w, int warp) {
-    return make_int2(max(w.ua - 1, 0) * kWarps + warp, min(max(w.ub - 1, 0) * kWarps, w.s.n_tiles));
+    return make_int2(max(w.ua - kSegCost, 0) * kWarps + warp, min(max(w.ub - kSegCost, 0) * kWarps, w.s.n_tiles));
 }
 // What happens once a piece stays out of line: the loop over tiles is what the
 // instruction cache has to hold.
@@ -215,29 +219,6 @@ __device__ __noinline__ int2 request_next(Walk* w, const AttnArgs* a, int warp) 
         if (t.x < t.y) return t;
     }
 }
-// Pages, and their scales, of the next 32 16-key steps of a warp, one a lane;
-// page -1: none, or a bad one (its keys are masked).
-struct Pages { int page; float ks, vs; };
-template <int KT, bool E4>
-__device__ __noinline__ Pages load_pages(const Walk* w, const AttnArgs* a, int t, int t_end) {
-    constexpr int SUB = KT / kTile;
-    const int lane = threadIdx.x & 31, tl = t + lane / SUB * kWarps;
-    const int key = (w->s.tile0 + tl) * KT + lane % SUB * kTile;
-    Pages r{-1, 0.f, 0.f};
-    if (tl < t_end && key < w->s.n_kv) {
-        const int page = __ldg(a->table + w->s.b * a->table_stride + (key >> a->page_shift));
-        if (page < 0 || page >= a->n_pages) {
-            atomicOr(a->status, kStatusInput);
-        } else {
-            r.page = page;
-            if (E4) {
-                r.ks = __ldg(a->k_scale + (int64_t)page * a->n_kv_head + w->s.h);
-                r.vs = __ldg(a->v_scale + (int64_t)page * a->n_kv_head + w->s.h);
-            }
-        }
-    }
-    return r;
-}
 static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, uint64_t ns) { return mbar_wait(bar, phase, ns); }
 
 template <int HD, int TYPE, int NT>
@@ -251,17 +232,18 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     unsigned char* ring = base + warp * NS * C::SLOT;
     unsigned char* after = base + kWarps * NS * C::SLOT;
-    float* red = reinterpret_cast<float*>(after);                                       // [warp][RT][CD + 4]
-    unsigned char* q_sm = after + C::RED;                                               // [RT][QPITCH]
-    float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);                        // [warp][RT]
+    unsigned char* q_sm = after;                                                         // [RT][QPITCH]
+    float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);                         // [warp][RT]
     struct Entry { float ks[2], vs[2]; uint32_t bad, pad[3]; };                          // of a tile's 16-key halves
     unsigned char* misc = q_sm + C::QBYTES + C::STATE;
     Entry* meta = reinterpret_cast<Entry*>(misc) + warp * C::ENTRIES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(misc + C::META) + warp * 8;
-    Walk* cws = reinterpret_cast<Walk*>(misc + C::META + kWarps * 64);                    // [2]
-    Walk* pw = reinterpret_cast<Walk*>(misc + C::META + kWarps * 64 + 128 + warp * 64);
-    int64_t* scan = reinterpret_cast<int64_t*>(misc + C::META + kWarps * 64 + (kWarps + 2) * 64);   // [16]
-    int2* views = reinterpret_cast<int2*>(misc + C::META + kWarps * 64 + (kWarps + 2) * 64 + 128);  // [2][RT]
+    int2* views = reinterpret_cast<int2*>(misc + C::META);                               // [2][RT]
+    misc += C::META + C::VIEWS;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(misc) + warp * 8;
+    Walk* cws = reinterpret_cast<Walk*>(misc + kWarps * 64);                             // [2]
+    Walk* pw = cws + 2 + warp;
+    int* scan = reinterpret_cast<int*>(cws + 2 + kWarps);                                // [32]
+    float* v_refs = reinterpret_cast<float*>(scan + 32);                                 // [warp]
     const uint32_t ring_u = smem_addr(ring), bars_u = smem_addr(bars);
 
     if (lane == 0) {
@@ -278,16 +260,16 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     // ---- this CTA's share of the units ------------------------------------
     // (the first 128 sequences are scanned as they are counted)
     const int cta = blockIdx.x;
-    int64_t u_b = 0, more_u = 0;
-    int s_b = 0, more_s = 0;     // units and segments of this thread's sequence, and of those behind the first 128
+    int u_b = 0, s_b = 0, n_rt_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind the first 128
     {
         bool bad_any = false;
         for (int b = tid; b < a.n_seq; b += kWarps * 32) {
             int n_rt;
             bool bad;
-            const int64_t u = seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head;
+            const int u = seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head;
             if (b == tid) {
                 u_b = u;
+                n_rt_b = n_rt;
                 s_b = n_rt * a.n_kv_head;
             } else {
                 more_u += u;
@@ -297,19 +279,17 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         }
         if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
     }
-    auto scan_warp = [&](int64_t& u, int& n) {
+    auto scan_warp = [&](int& u, int& n) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(~0u, u, o);
-            const int y = __shfl_up_sync(~0u, n, o);
+            const int x = __shfl_up_sync(~0u, u, o), y = __shfl_up_sync(~0u, n, o);
             if (lane >= o) {
                 u += x;
                 n += y;
             }
         }
     };
-    int64_t inc = u_b;
-    int inc_s = s_b;
+    int inc = u_b, inc_s = s_b;
     scan_warp(inc, inc_s);
     if (a.n_seq > kWarps * 32) scan_warp(more_u, more_s);
     if (lane == 31) {
@@ -318,63 +298,51 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         scan[8 + warp] = more_u;
         scan[12 + warp] = more_s;
     }
+    if (tid == 0) cws[0].more = 0;
     __syncthreads();
-    const int64_t first_u = scan[0] + scan[1] + scan[2] + scan[3];
-    const int first_s = (int)(scan[4] + scan[5] + scan[6] + scan[7]);
-    const int64_t total = first_u + scan[8] + scan[9] + scan[10] + scan[11];
-    const int n_cta = (int)min((int64_t)gridDim.x, total);
+    int base_u = scan[0] + scan[1] + scan[2] + scan[3], base_s = scan[4] + scan[5] + scan[6] + scan[7];
+    // (the host refuses batches whose units could pass 31 bits)
+    const int total = base_u + scan[8] + scan[9] + scan[10] + scan[11];
+    const int n_cta = min((int)gridDim.x, total);
     if (cta == 0 && tid == 0)    // entries of split[] that this call writes
-        *a.n_split = a.split_by_segment ? (int)min((int64_t)kMaxCtas, first_s + scan[12] + scan[13] + scan[14] + scan[15])
-                                        : n_cta;
+        *a.n_split = a.split_by_segment ? min(kMaxCtas, base_s + scan[12] + scan[13] + scan[14] + scan[15]) : n_cta;
     if (cta >= n_cta) return;
-    // floor(total * i / n_cta), by 32-bit divisions where they do
-    auto share = [&](int i) -> int64_t {
-        if (total >> 31) return total * i / n_cta;
-        const uint32_t t = (uint32_t)total, n = n_cta, q = t / n, r = t - q * n;
-        return (int64_t)q * i + r * i / n;
-    };
-    const int64_t u0 = share(cta), u1 = share(cta + 1);
+    // the first `extra` CTAs take one unit more than the others
+    const int per_cta = total / n_cta, extra = total - per_cta * n_cta;
+    const int u0 = per_cta * cta + min(cta, extra), my_units = per_cta + (cta < extra ? 1 : 0);
     {
         for (int w = 0; w < warp; ++w) {
             inc += scan[w];
-            inc_s += (int)scan[4 + w];
+            inc_s += scan[4 + w];
         }
-        int64_t base_u = first_u;
-        int base_s = first_s;
-        if (tid == 0) cws[0].more = 0;
-        __syncthreads();         // the totals above are read
         int b = tid;
         for (;;) {
             if (u_b > 0 && u0 >= inc - u_b && u0 < inc) {      // one thread of the block: the share starts in its sequence
                 Walk w;
-                int n_rt;
-                bool bad;
-                int64_t rem = u0 - (inc - u_b);
-                const int64_t per_head = u_b / a.n_kv_head;
-                seq_units<RT, KT>(a, b, n_rt, bad);
+                int rem = u0 - (inc - u_b);
+                const int per_head = u_b / a.n_kv_head;
                 seg_seq<RT>(w.s, a, b);
-                w.s.h = rem >> 31 || per_head >> 31 ? (int)(rem / per_head) : (int)((uint32_t)rem / (uint32_t)per_head);
+                w.s.h = a.n_kv_head == 1 ? 0 : rem / per_head;
                 rem -= w.s.h * per_head;
                 for (w.s.rt = 0;; ++w.s.rt) {
                     seg_keys<RT, KT>(w.s, a);
                     if (rem < w.s.n_units || w.s.rt + 1 >= w.s.n_rt) break;
                     rem -= w.s.n_units;
                 }
-                w.seg_no = inc_s - s_b + w.s.h * n_rt + w.s.rt;
-                w.ua = (int)rem;
-                w.left = (int)min(u1 - u0, (int64_t)0x7fffffff);
+                w.seg_no = inc_s - s_b + w.s.h * n_rt_b + w.s.rt;
+                w.ua = rem;
+                w.left = my_units;
                 w.ub = min(w.s.n_units, w.ua + w.left);
                 w.more = w.s.n_rt > 0;
                 cws[0] = w;
-                for (int i = 0; i < kWarps; ++i) cws[2 + i] = w;     // the warps' own: they follow
             }
             if (u0 < base_u || b - tid >= a.n_seq) break;
             // behind the first 128 sequences: the next 128
             b += kWarps * 32;
-            int n_rt = 0;
             bool bad;
-            u_b = b < a.n_seq ? seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head : 0;
-            s_b = n_rt * a.n_kv_head;
+            n_rt_b = 0;
+            u_b = b < a.n_seq ? seq_units<RT, KT>(a, b, n_rt_b, bad) * a.n_kv_head : 0;
+            s_b = n_rt_b * a.n_kv_head;
             inc = u_b;
             inc_s = s_b;
             scan_warp(inc, inc_s);
@@ -389,89 +357,102 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) {
                     inc += scan[w];
-                    inc_s += (int)scan[4 + w];
+                    inc_s += scan[4 + w];
                 }
                 base_u += scan[w];
-                base_s += (int)scan[4 + w];
+                base_s += scan[4 + w];
             }
         }
     }
-    // For a piece's rows: the keys each sees, [y, x), and where it is read, Q rows
-    // to shared memory (positions of a 16-dim group in the order the MMA takes them).
-    auto q_row = [&](const Walk& w, int r) {
-        const int i = (w.s.rt * RT + r) / a.group, hh = w.s.rt * RT + r - i * a.group;
-        return a.q16 + (int64_t)(w.s.tok0 + i) * a.q_stride + (int64_t)(w.s.h * a.group + hh) * HD;
-    };
+    // For a piece's rows: the keys each sees, [y, x), and copies of its Q rows to
+    // shared memory (a 16-dim group in the order the MMA takes its dims).
+    constexpr int QN = (RT * HD / 8 + kWarps * 32 - 1) / (kWarps * 32);      // 16-byte chunks of a thread
+    uint4 qx[QN];                // (e4m3: on their way)
     auto open_piece = [&](int which) {
         const Walk& w = cws[which];
         if (!w.more) return;
-        const int rows = min(RT, w.s.n_q * a.group - w.s.rt * RT);
+        const int row0 = w.s.rt * RT, rows = min(RT, w.s.n_q * a.group - row0);
         if (tid < RT) {
             int hi = w.s.n_kv, lo = 0;
             if (a.causal) {
-                const int p = w.s.n_kv - w.s.n_q + (w.s.rt * RT + min(tid, rows - 1)) / a.group;
+                const int p = w.s.n_kv - w.s.n_q + (row0 + min(tid, rows - 1)) / a.group;
                 hi = min(hi, p + 1);
                 if (a.window > 0) lo = max(0, p + 1 - a.window);
             }
             views[which * RT + tid] = make_int2(hi, lo);
         }
-        if (!C::QREG)
-            for (int i = tid; i < RT * (HD / 8); i += kWarps * 32) {
-                const int r = i / (HD / 8), c = i - r * (HD / 8);
-                const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4*>(q_row(w, r) + c * 8)) : make_uint4(0, 0, 0, 0);
-                unsigned char* dst = q_sm + r * C::QPITCH;
-                if (E4) {
-                    *reinterpret_cast<uint2*>(dst + (c >> 1) * 32 + (c & 1) * 8) = make_uint2(x.x, x.z);
-                    *reinterpret_cast<uint2*>(dst + (c >> 1) * 32 + 16 + (c & 1) * 8) = make_uint2(x.y, x.w);
-                } else {
-                    *reinterpret_cast<uint4*>(dst + c * 16) = x;
-                }
+        const uint32_t q_u = smem_addr(q_sm);
+#pragma unroll
+        for (int k = 0; k < QN; ++k) {
+            const int r = (k * kWarps * 32 + tid) / (HD / 8), c = tid % (HD / 8);
+            if (r >= RT) break;
+            const int i = (row0 + min(r, rows - 1)) / a.group, hh = row0 + min(r, rows - 1) - i * a.group;
+            const __half* src = a.q16 + (int64_t)(w.s.tok0 + i) * a.q_stride + (int64_t)(w.s.h * a.group + hh) * HD + c * 8;
+            // rows behind the last are zeros
+            if (E4)
+                qx[k] = r < rows ? __ldcg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+            else
+                cp_async16(q_u + r * C::QPITCH + c * 16, src, r < rows ? 16 : 0);
+        }
+        if (!E4) cp_async_commit();
+    };
+    // The copies have arrived; e4m3's MMA takes dims 4i .. 4i + 3 as two pairs 8 places apart.
+    auto close_open = [&](int which) {
+        if (!E4) {
+            cp_async_wait<0>();
+        } else if (cws[which].more) {
+#pragma unroll
+            for (int k = 0; k < QN; ++k) {
+                const int r = (k * kWarps * 32 + tid) / (HD / 8), c = tid % (HD / 8);
+                if (r >= RT) break;
+                unsigned char* dst = q_sm + r * C::QPITCH + (c >> 1) * 32 + (c & 1) * 8;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(qx[k].x, qx[k].z);
+                *reinterpret_cast<uint2*>(dst + 16) = make_uint2(qx[k].y, qx[k].w);
             }
+        }
     };
     __syncthreads();
     if (!cws[0].more) return;    // (only if the lengths change during the call)
+    if (lane < 16) reinterpret_cast<int*>(pw)[lane] = reinterpret_cast<const int*>(cws)[lane];
+    open_piece(0);               // ahead of the ring's requests, which fill the memory system's queues
+    __syncwarp();
 
     // ---- the warp's ring: slots q = 0, 1, ... hold K, V, K, V, ... of its tiles ----
     int2 pt = walk_tiles(*pw, warp);   // the next tile to request of the piece, and its end
     if (pt.x >= pt.y) pt = request_next<RT, KT>(pw, &a, warp);
     constexpr int BLK = 32 / SUB;  // tiles of a page block: a lane for each 16 keys
-    int blk = BLK;               // tiles of the page block used up (BLK: load a new one)
-    Pages pb{};
-    int p_page[SUB] = {};
+    int blk = 0;                 // tiles of the page block used up
+    int b_page = -1, p_page[SUB] = {};
+    float b_ks = 0.f, b_vs = 0.f;
     int i_slot = 0, i_tile = 0;  // ring slot of the next request; its tile's number mod ENTRIES
-    bool i_v = false;
+    bool i_v = false, fresh = false, b_has = false;
+    // Page numbers of the warp's next 32 16-key steps, one a lane; -1: none. Asked
+    // for one request ahead of their use.
+    auto load_pages = [&]() {
+        blk = 0;
+        const int tl = pt.x + lane / SUB * kWarps, key = (pw->s.tile0 + tl) * KT + lane % SUB * kTile;
+        b_has = tl < pt.y && key < pw->s.n_kv;
+        b_page = -1;
+        if (b_has) b_page = __ldcg(a.table + pw->s.b * a.table_stride + (key >> a.page_shift));
+        fresh = true;
+    };
+    load_pages();
     auto request = [&]() {
         if (pt.x >= pt.y) return;                      // the share's end
-        if (!i_v) {              // a new tile: its pages, and its scales for the consumer
-            if (blk == BLK) {
-                pb = load_pages<KT, E4>(pw, &a, pt.x, pt.y);
-                blk = 0;
+        if (!i_v) {              // a new tile: its pages
+            if (fresh && b_has && (b_page < 0 || b_page >= a.n_pages)) {
+                atomicOr(a.status, kStatusInput);
+                b_page = -1;
             }
             uint32_t bad = 0u;
-            float ks[SUB], vs[SUB];
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
-                p_page[u] = __shfl_sync(~0u, pb.page, blk * SUB + u);
-                if (E4) {
-                    ks[u] = __shfl_sync(~0u, pb.ks, blk * SUB + u);
-                    vs[u] = __shfl_sync(~0u, pb.vs, blk * SUB + u);
-                }
+                p_page[u] = __shfl_sync(~0u, b_page, blk * SUB + u);
                 // no such page: page 0, which exists, is read in its place and its keys are masked
                 if (p_page[u] < 0) bad |= 1u << u;
                 p_page[u] = max(p_page[u], 0);
             }
-            ++blk;
-            if (lane == 0) {
-                Entry& m = meta[i_tile];
-                if (E4) {
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        m.ks[u] = ks[u];
-                        m.vs[u] = vs[u];
-                    }
-                }
-                m.bad = bad;
-            }
+            if (lane == 0) meta[i_tile].bad = bad;
         }
         if (lane == 0) {
             const uint32_t bar = bars_u + 8 * i_slot;
@@ -483,12 +464,38 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                             head, p_page[u], bar);
         }
         if (++i_slot == NS) i_slot = 0;
-        if (i_v) {
+        if (!i_v) {
+            if (E4 && fresh) {   // the block's scales, awaited with the V request
+                b_ks = b_vs = 0.f;
+                if (b_page >= 0) {
+                    b_ks = __ldcg(a.k_scale + (int64_t)b_page * a.n_kv_head + pw->s.h);
+                    b_vs = __ldcg(a.v_scale + (int64_t)b_page * a.n_kv_head + pw->s.h);
+                }
+            }
+            fresh = false;
+        } else {
+            if (E4) {            // the tile's scales, for the consumer
+                float ks[SUB], vs[SUB];
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    ks[u] = __shfl_sync(~0u, b_ks, blk * SUB + u);
+                    vs[u] = __shfl_sync(~0u, b_vs, blk * SUB + u);
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        meta[i_tile].ks[u] = ks[u];
+                        meta[i_tile].vs[u] = vs[u];
+                    }
+                }
+            }
             i_tile = (i_tile + 1) % C::ENTRIES;
+            ++blk;
             if ((pt.x += kWarps) >= pt.y) {
                 pt = request_next<RT, KT>(pw, &a, warp);
                 blk = BLK;
             }
+            if (blk == BLK) load_pages();
         }
         i_v = !i_v;
     };
@@ -504,9 +511,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         // after one wait that gave up the others do so soon: the kernel ends
         if (!wait_long(bars_u + 8 * c_slot, c_phase, timeout ? 20000ull : kWaitNs)) timeout = true;
     };
-    auto pass_slot = [&]() {     // this slot is used up: request what comes NS slots later
+    auto pass_slot = [&](bool hold) {    // this slot is used up: request what comes NS slots later, unless it is held
         __syncwarp();
-        request();
+        if (!hold) request();
         if (++c_slot == NS) {
             c_slot = 0;
             c_phase ^= 1;
@@ -526,7 +533,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         return (base ^ ((c % CPB) << 4)) + sub * C::SUBB + c / CPB * (kTile * C::PITCH);
     };
 
-    open_piece(0);
+    close_open(0);
     __syncthreads();
     for (int which = 0;; which ^= 1) {
         // ---- a piece: its rows and their Q fragments --------------------------
@@ -534,28 +541,23 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         const int2* view = views + which * RT;
         const int rows = min(RT, cw.s.n_q * a.group - cw.s.rt * RT);
         const int min_lim = view[0].x, max_low = view[RT - 1].y;       // (rows behind the last see what it sees)
+        const uint32_t q_lane = smem_addr(q_sm) + ((lane & 7) + (NT > 1 ? lane >> 4 : 0) * 8) * C::QPITCH +
+                                (NT > 1 ? (lane >> 3) & 1 : lane >> 3) * 16;
         uint32_t qf[C::QREG ? MT : 1][NT][2];
         if (C::QREG) {
+            if (NT == 1) {                           // four matrices: two k steps of one row block
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int r = n * 8 + g;
-                const __half* src = q_row(cw, min(r, rows - 1));
+                for (int kk = 0; kk < MT; kk += 2)
+                    ldsm_x4(q_lane + kk * 32, qf[kk][0][0], qf[kk][0][1], qf[kk + 1][0][0], qf[kk + 1][0][1]);
+            } else {
 #pragma unroll
-                for (int kk = 0; kk < MT; ++kk) {
-                    if (E4) {
-                        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + kk * 16 + 4 * t4));
-                        qf[kk][n][0] = r < rows ? x.x : 0u;
-                        qf[kk][n][1] = r < rows ? x.y : 0u;
-                    } else {
-                        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * t4));
-                        const uint32_t y = __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + 2 * t4));
-                        qf[kk][n][0] = r < rows ? x : 0u;
-                        qf[kk][n][1] = r < rows ? y : 0u;
-                    }
-                }
+                for (int kk = 0; kk < MT; ++kk)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2)
+                        ldsm_x4(q_lane + n * 8 * C::QPITCH + kk * 32, qf[kk][n][0], qf[kk][n][1], qf[kk][(n + 1) % NT][0],
+                                qf[kk][(n + 1) % NT][1]);
             }
         }
-        const uint32_t q_lane = smem_addr(q_sm) + ((lane & 7) + (lane >> 4) * 8) * C::QPITCH + ((lane >> 3) & 1) * 16;
         // B fragments of step kk for all row blocks
         auto q_frags = [&](int kk, uint32_t (*b)[2]) {
             if (C::QREG) {
@@ -567,7 +569,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             } else {
 #pragma unroll
                 for (int n = 0; n < NT; n += 2)
-                    ldsm_x4(q_lane + n * 8 * C::QPITCH + kk * 32, b[n][0], b[n][1], b[n + 1][0], b[n + 1][1]);
+                    ldsm_x4(q_lane + n * 8 * C::QPITCH + kk * 32, b[n][0], b[n][1], b[(n + 1) % NT][0], b[(n + 1) % NT][1]);
             }
         };
 
@@ -589,7 +591,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             wait_slot();
             const Entry& en = meta[c_tile];
             const uint32_t bad = en.bad;
-            uint32_t base = k_lane + c_slot * C::SLOT;
+            const uint32_t k_base = k_lane + c_slot * C::SLOT;
             float s[SUB][NT][4], s2[SUB][NT][4];     // s2: a second chain of MMAs where there is one tile
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
@@ -605,7 +607,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     uint32_t r[4];
-                    ldsm_x4(at_chunk(base, u, E4 ? kk : 2 * kk), r[0], r[1], r[2], r[3]);
+                    ldsm_x4(at_chunk(k_base, u, E4 ? kk : 2 * kk), r[0], r[1], r[2], r[3]);
                     if (E4) {
                         const uint32_t a0[4] = {e4m3_lo(r[0]), e4m3_lo(r[1]), e4m3_hi(r[0]), e4m3_hi(r[1])};
                         const uint32_t a1[4] = {e4m3_lo(r[2]), e4m3_lo(r[3]), e4m3_hi(r[2]), e4m3_hi(r[3])};
@@ -634,7 +636,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 vs[u] = E4 ? en.vs[u] : 1.f;
                 vmax = fmaxf(vmax, fabsf(vs[u]));
             }
-            pass_slot();
+            pass_slot(false);
 
             // ---- softmax weights: exponents x - mref first -------------------
             const int key0 = (tile0 + t) * KT;
@@ -818,13 +820,13 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 fence_proxy_async_cta();             // the slot's next fill comes by TMA
                 __syncwarp();
             }
-            base = v_lane + c_slot * C::SLOT;
+            const uint32_t v_base = v_lane + c_slot * C::SLOT;
 #pragma unroll
             for (int m = 0; m < MT; m += E4 ? 2 : 1)
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     uint32_t r[4];
-                    ldsm_x4_t(at_chunk(base, u, E4 ? m : 2 * m), r[0], r[1], r[2], r[3]);
+                    ldsm_x4_t(at_chunk(v_base, u, E4 ? m : 2 * m), r[0], r[1], r[2], r[3]);
                     if (E4) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
@@ -844,11 +846,13 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         for (int n = 0; n < NT; ++n) mma(o[m][n], r, pl[u][n][0], pl[u][n][1]);
                     }
                 }
-            pass_slot();
+            pass_slot(t + kWarps >= tiles.y);        // the piece's last slot takes O first
             c_tile = (c_tile + 1) % C::ENTRIES;
         }
 
         // ---- the piece's end: the four warps' states become one ---------------
+        const bool had = tiles.x < tiles.y;          // a warp without a tile has no state, and holds no slot
+        const int held = c_slot == 0 ? NS - 1 : c_slot - 1;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -860,6 +864,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 else if (mref[n][e] == kNoRef) mref[n][e] = 0.f;
                 if (g == 0) state[warp * RT + n * 8 + 2 * t4 + e] = make_float2(mref[n][e], l[n][e]);
             }
+        if (E4 && lane == 0) v_refs[warp] = vref;
         const bool whole = cw.ua == 0 && cw.ub == cw.s.n_units;
         // state slot: 2*cta + 1 for a segment that goes on in the next CTA from its start here, else 2*cta
         const int part = 2 * cta + (cw.ua == 0 && !whole ? 1 : 0);
@@ -869,59 +874,54 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             const bool starts = cw.ua == 0, last_piece = cw.left <= cw.ub - cw.ua;
             Split sp{cta, -1, tok0, row0, rows, cw.s.h, {0, 0}};
             if (starts && !whole) {
-                const int64_t end_u = u1 - cw.left + cw.s.n_units;     // behind the segment's last unit
-                sp.last = total >> 31 ? (int)((end_u * n_cta - 1) / total)
-                                      : (int)(((uint64_t)end_u * n_cta - 1) / (uint64_t)total);
+                const int x = u0 + my_units - cw.left + cw.s.n_units - 1, wide = extra * (per_cta + 1);   // its last unit
+                sp.last = min(n_cta - 1, x < wide ? x / (per_cta + 1) : extra + (x - wide) / per_cta);
             }
             const int at = a.split_by_segment ? cw.seg_no : cta;
             if ((a.split_by_segment ? starts : last_piece) && at < kMaxCtas) a.split[at] = sp;
             cws[which ^ 1] = cw;
             walk_next<RT, KT>(&cws[which ^ 1], &a);
         }
-        __syncthreads();
+        // O^T as fp32 rows in the slot that the warp held back, in chunks of CNT
+        // row blocks; dims of a row are moved by its number against bank conflicts
+        auto o_at = [](int r, int d) { return r * HD + (d ^ ((r >> 1 & 3) << 3)); };
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n0 = 0; n0 < NT; n0 += C::CNT) {
+            if (n0) __syncthreads();
+            if (had) {
+                float* dst = reinterpret_cast<float*>(ring + held * C::SLOT);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float m = -INFINITY;
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, state[w * RT + n * 8 + 2 * t4 + e].x);
-                // a warp without a visible key has no state: factor 0
-                const float f = (mref[n][e] == -INFINITY ? 0.f : ex2(mref[n][e] - m)) * (E4 ? vref : 1.f);
+                    for (int n = 0; n < C::CNT; ++n)
 #pragma unroll
-                for (int mm = 0; mm < MT; ++mm) {
-                    o[mm][n][e] = f == 0.f ? 0.f : o[mm][n][e] * f;
-                    o[mm][n][2 + e] = f == 0.f ? 0.f : o[mm][n][2 + e] * f;
-                }
+                        for (int e = 0; e < 4; ++e)
+                            dst[o_at(n * 8 + 2 * t4 + (e & 1), m * 16 + (E4 ? 2 * g + (e >> 1) : g + 8 * (e >> 1)))] =
+                                o[m][n0 + n][e];
+                if (lane == 0) reinterpret_cast<const float**>(scan)[warp] = dst;
             }
-#pragma unroll
-        for (int c0 = 0; c0 < HD; c0 += C::CD) {
-            if (c0) __syncthreads();
-#pragma unroll
-            for (int mm = 0; mm < C::CD / 16; ++mm)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int d = mm * 16 + (E4 ? 2 * g + (e >> 1) : g + 8 * (e >> 1));
-                        red[(warp * RT + n * 8 + 2 * t4 + (e & 1)) * (C::CD + 4) + d] = o[c0 / 16 + mm][n][e];
-                    }
             __syncthreads();
-            for (int w = tid; w < rows * (C::CD / 4); w += kWarps * 32) {
-                const int r = w / (C::CD / 4), d = (w - r * (C::CD / 4)) * 4;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (n0 == 0) open_piece(which ^ 1);      // the next piece's Q rows come while this one is written
+            const int chunk_rows = min(C::CNT * 8, rows - n0 * 8);
+            for (int w = tid; w < chunk_rows * (HD / 4); w += kWarps * 32) {
+                const int rr = w / (HD / 4), r = n0 * 8 + rr, d = (w - rr * (HD / 4)) * 4;
                 float m = -INFINITY, lsum = 0.f;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int v = 0; v < kWarps; ++v) m = fmaxf(m, state[v * RT + r].x);
 #pragma unroll
                 for (int v = 0; v < kWarps; ++v) {
-                    const float4 y = *reinterpret_cast<const float4*>(&red[(v * RT + r) * (C::CD + 4) + d]);
-                    x.x += y.x;
-                    x.y += y.y;
-                    x.z += y.z;
-                    x.w += y.w;
                     const float2 st = state[v * RT + r];
-                    if (st.x != -INFINITY) lsum += st.y * ex2(st.x - m);
+                    if (st.x == -INFINITY) continue;             // no key seen, or no tile
+                    float f = ex2(st.x - m);
+                    lsum += st.y * f;
+                    if (E4) f *= v_refs[v];
+                    const float* src = reinterpret_cast<const float* const*>(scan)[v];
+                    const float4 y = *reinterpret_cast<const float4*>(src + o_at(rr, d));
+                    x.x += f * y.x;
+                    x.y += f * y.y;
+                    x.z += f * y.z;
+                    x.w += f * y.w;
                 }
                 if (whole) {
                     const float inv = m == -INFINITY ? 0.f : 1.f / lsum;
@@ -931,15 +931,17 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                     x.w *= inv;
                     const int i = (row0 + r) / a.group, hh = (row0 + r) - i * a.group;
                     float* dst = a.out + ((int64_t)(tok0 + i) * a.n_kv_head * a.group + head0 + hh) * HD;
-                    *reinterpret_cast<float4*>(dst + c0 + d) = x;
+                    *reinterpret_cast<float4*>(dst + d) = x;
                 } else {
-                    *reinterpret_cast<float4*>(a.part_o + ((int64_t)part * RT + r) * HD + c0 + d) = x;
-                    if (c0 == 0 && d == 0) a.part_ml[part * RT + r] = make_float2(m, lsum);
+                    *reinterpret_cast<float4*>(a.part_o + ((int64_t)part * RT + r) * HD + d) = x;
+                    if (d == 0) a.part_ml[part * RT + r] = make_float2(m, lsum);
                 }
             }
         }
-        open_piece(which ^ 1);
+        close_open(which ^ 1);
+        fence_proxy_async_cta();                     // the held slot's next fill comes by TMA
         __syncthreads();
+        if (had) request();
         if (!cws[which ^ 1].more) break;
     }
     if (timeout) atomicOr(a.status, kStatusTimeout);
