@@ -28,76 +28,83 @@ __global__ void __launch_bounds__(kMergeThreads)
 paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_split, const float* __restrict__ part_o,
                    const float2* __restrict__ part_ml, float* __restrict__ out, int row_tile, int hd, int group,
                    int n_kv_head) {
-    __shared__ float wt[kMaxCtas], red_l[kMergeThreads / 32], red_m[kMergeThreads / 32];
-    __shared__ float4 red[kMergeThreads];
+    __shared__ float red_l[kMergeThreads / 32], red_m[kMergeThreads / 32];
+    extern __shared__ float4 red[];                 // [threads], then the states' weights
+    float* wt = reinterpret_cast<float*>(red + blockDim.x);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, row = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int n_entries = __ldcg(n_split);
     const int4 s0 = __ldcg(reinterpret_cast<const int4*>(split + blockIdx.x));
     const int2 s1 = __ldcg(reinterpret_cast<const int2*>(split + blockIdx.x) + 2);
     const int first = s0.x, n = s0.y - first + 1, tok0 = s0.z, row0 = s0.w, rows = s1.x, head = s1.y;
-    if ((int)blockIdx.x >= n_entries || n < 1 || row >= rows) return;
+    if ((int)blockIdx.x >= n_entries || n < 1) return;
     const int groups = blockDim.x / kMergeCols, c = blockIdx.z * kMergeCols + tid % kMergeCols, gi = tid / kMergeCols;
-    auto slot = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
-    float4 ahead[kAhead];
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        auto slot = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
+        float4 ahead[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-        const int p = gi + i * groups;
-        ahead[i] = p < n ? __ldcg(reinterpret_cast<const float4*>(part_o + slot(p) * hd) + c) : make_float4(0, 0, 0, 0);
-    }
-    // every thread that holds a state's (m, l) keeps it; more than one for each only beyond 512 states
-    const float2 mine = tid < n ? __ldcg(part_ml + slot(tid)) : make_float2(-INFINITY, 0.f);
-    float m = mine.x;
-    for (int p = tid + blockDim.x; p < n; p += blockDim.x) m = fmaxf(m, __ldcg(part_ml + slot(p)).x);
+        for (int i = 0; i < kAhead; ++i) {
+            const int p = gi + i * groups;
+            ahead[i] = p < n ? __ldcg(reinterpret_cast<const float4*>(part_o + slot(p) * hd) + c) : make_float4(0, 0, 0, 0);
+        }
+        const float2 mine = tid < n ? __ldcg(part_ml + slot(tid)) : make_float2(-INFINITY, 0.f);
+        float m = mine.x;
+        for (int p = tid + blockDim.x; p < n; p += blockDim.x) m = fmaxf(m, __ldcg(part_ml + slot(p)).x);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    if (lane == 0) red_m[warp] = m;
-    __syncthreads();
-    m = red_m[0];
-    for (int w = 1; w < warps; ++w) m = fmaxf(m, red_m[w]);
-    float l = 0.f;
-    for (int p = tid; p < n; p += blockDim.x) {
-        const float2 ml = p == tid ? mine : __ldcg(part_ml + slot(p));
-        const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-        wt[p] = w;
-        l += w == 0.f ? 0.f : w * ml.y;
-    }
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if (lane == 0) red_m[warp] = m;
+        __syncthreads();
+        m = red_m[0];
+        for (int w = 1; w < warps; ++w) m = fmaxf(m, red_m[w]);
+        float l = 0.f;
+        for (int p = tid; p < n; p += blockDim.x) {
+            const float2 ml = p == tid ? mine : __ldcg(part_ml + slot(p));
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            wt[p] = w;
+            l += w == 0.f ? 0.f : w * ml.y;
+        }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (lane == 0) red_l[warp] = l;
-    __syncthreads();
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](int p, const float4& y) {
-        const float w = wt[p];
-        if (w == 0.f) return;                   // an empty state may hold anything
-        x.x += w * y.x;
-        x.y += w * y.y;
-        x.z += w * y.z;
-        x.w += w * y.w;
-    };
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        if (lane == 0) red_l[warp] = l;
+        __syncthreads();
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](int p, const float4& y) {
+            const float w = wt[p];
+            if (w == 0.f) return;                   // an empty state may hold anything
+            x.x += w * y.x;
+            x.y += w * y.y;
+            x.z += w * y.z;
+            x.w += w * y.w;
+        };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (gi + i * groups < n) add(gi + i * groups, ahead[i]);
+        for (int i = 0; i < kAhead; ++i)
+            if (gi + i * groups < n) add(gi + i * groups, ahead[i]);
 #pragma unroll 8
-    for (int p = gi + kAhead * groups; p < n; p += groups)
-        add(p, __ldcg(reinterpret_cast<const float4*>(part_o + slot(p) * hd) + c));
-    red[tid] = x;
-    __syncthreads();
-    if (gi) return;
-    l = 0.f;
-    for (int w = 0; w < warps; ++w) l += red_l[w];
-    for (int i = 1; i < groups; ++i) {
-        const float4 y = red[i * kMergeCols + tid];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+        for (int p = gi + kAhead * groups; p < n; p += groups)
+            add(p, __ldcg(reinterpret_cast<const float4*>(part_o + slot(p) * hd) + c));
+        red[tid] = x;
+        __syncthreads();
+        if (gi == 0) {
+            l = 0.f;
+            for (int w = 0; w < warps; ++w) l += red_l[w];
+            for (int i = 1; i < groups; ++i) {
+                const float4 y = red[i * kMergeCols + tid];
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+            }
+            const float inv = m == -INFINITY ? 0.f : 1.f / l;
+            const int i = (row0 + row) / group, hh = row0 + row - i * group;
+            float* dst = out + ((int64_t)(tok0 + i) * n_kv_head * group + head * group + hh) * hd + c * 4;
+            *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        }
+        if (row + (int)gridDim.y < rows) __syncthreads();   // the shared arrays are read
     }
-    const float inv = m == -INFINITY ? 0.f : 1.f / l;
-    const int i = (row0 + row) / group, hh = row0 + row - i * group;
-    float* dst = out + ((int64_t)(tok0 + i) * n_kv_head * group + head * group + hh) * hd + c * 4;
-    *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    // The next kernel on the stream may start now, and not before: attention
+    // CTAs that find merge blocks in their SM's shared memory may not fit beside
+    // them and would start only when another one ends.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---- descriptors ---------------------------------------------------------------
@@ -326,21 +333,12 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     a.window = window;
     a.split_by_segment = segs <= ctas ? 1 : 0;
     a.scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
-    // The merge kernel leaves the SMs' memory split as the attention kernel needs
-    // it: an SM that still runs merge blocks of the call before would otherwise
-    // take one attention CTA less, for as long as that kernel runs
-    static unsigned long long done = 0ull;
-    if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev & 1ull)) {
-        if (cudaFuncSetAttribute(paged_merge_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
-            return FR_ERR_CUDA;
-        if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
-    }
     const fr_status st = kv->type == FR_KV_E4M3 ? launch_attn_e4m3(*kv, a, nt, (int)ctas, stream)
                                                 : launch_attn_f16(*kv, a, nt, (int)ctas, stream);
     if (st != FR_OK) return st;
 
-    const int64_t rows = (int64_t)G * bt->n_tok < rt ? (int64_t)G * bt->n_tok : rt;
+    const int64_t rows = a.split_by_segment ? ((int64_t)G * bt->n_tok < rt ? (int64_t)G * bt->n_tok : rt)
+                                            : (avg < rt ? avg : rt);      // (a block goes on to the rows behind)
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)(a.split_by_segment ? segs : ctas), (unsigned)rows, (unsigned)(kv->hd / (4 * kMergeCols)));
@@ -349,6 +347,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     const int64_t groups = (ctas / (usual * kv->n_kv_head) + 2 + kAhead - 1) / kAhead;
     int64_t threads = (groups * kMergeCols + 31) / 32 * 32;
     cfg.blockDim = dim3((unsigned)(threads > kMergeThreads ? kMergeThreads : threads));
+    cfg.dynamicSmemBytes = cfg.blockDim.x * sizeof(float4) + kMaxCtas * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -87,27 +87,27 @@ struct Cfg {
     static constexpr int ROWB = HD * (E4 ? 1 : 2);          // bytes of a K or V row
     static constexpr int PITCH = ROWB < 128 ? ROWB : 128;   // bytes of a row in one box
     static constexpr int MT = HD / 16;                      // 16-dim blocks of O^T, and k steps of S^T
-    static constexpr int CPS = ctas_per_sm(HD, NT);
-    static constexpr int LIMIT = 233472 / CPS - 1024;       // shared memory of one CTA
+    static constexpr int W = cta_warps(HD, NT);
+    static constexpr int LIMIT = cta_smem(HD, NT);          // shared memory of one CTA
     // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
     // Q rows lie in shared memory; up to 64 registers of fragments are kept from them for a piece
     static constexpr bool QREG = HD * NT <= 256;
     static constexpr int QPITCH = HD * 2 + 16;              // bytes: rows on different banks
     static constexpr int QBYTES = RT * QPITCH;
-    static constexpr int STATE = kWarps * RT * 8;
+    static constexpr int STATE = W * RT * 8;
     static constexpr int ENTRIES = 8;                       // tiles requested and not used up, at most
-    static constexpr int META = kWarps * ENTRIES * 32;
+    static constexpr int META = W * ENTRIES * 32;
     static constexpr int VIEWS = 2 * RT * 8;
     // alignment slack, buffers above, then barriers, walks, scan words and the warps' V scales
-    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + kWarps * 64 + (kWarps + 2) * 64 + 128 + 16;
+    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 + 16;
     // 32 keys a slot where three slots of them fit (K, V and the next K), else 16
-    static constexpr int SUB = 3 * kWarps * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
+    static constexpr int SUB = 3 * W * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
     static constexpr int KT = kTile * SUB;                  // keys of a warp's tile
     static constexpr int SUBB = kTile * ROWB, SLOT = SUB * SUBB;
-    static constexpr int NS_ = (LIMIT - FIXED) / (kWarps * SLOT);
+    static constexpr int NS_ = (LIMIT - FIXED) / (W * SLOT);
     static constexpr int NS = NS_ > 8 ? 8 : NS_;            // slots of a warp's ring
-    static constexpr int SMEM = FIXED + NS * kWarps * SLOT;
-    static_assert(NS >= 3, "ring");
+    static constexpr int SMEM = FIXED + NS * W * SLOT;
+    static_assert(NS >= 3 && SMEM <= 232448, "ring");
     // rows of a warp's O^T that one slot holds in fp32: the epilogue's chunk
     static constexpr int CNT = SLOT / (HD * 32) < NT ? SLOT / (HD * 32) : NT;
     static_assert(CNT >= 1 && NT % CNT == 0, "epilogue chunk");
@@ -120,7 +120,7 @@ struct Seg {
     int tile0, n_tiles, n_units;
 };
 
-template <int RT, int KT>
+template <int RT, int KT, int W>
 __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
     int hi = s.n_kv, lo = 0;
     if (a.causal) {
@@ -135,7 +135,7 @@ __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
     s.n_tiles = hi > lo ? (hi + KT - 1) / KT - s.tile0 : 0;
     // a segment's start and end cost a CTA as much as about two units of its
     // keys: it counts those ahead of them (rows without keys still get their zeros)
-    s.n_units = kSegCost + (s.n_tiles + kWarps - 1) / kWarps;
+    s.n_units = kSegCost + (s.n_tiles + W - 1) / W;
 }
 template <int RT>
 __device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
@@ -148,7 +148,7 @@ __device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
     return q.bad;
 }
 // The next segment in order (row tile fastest, then KV head, then sequence).
-template <int RT, int KT>
+template <int RT, int KT, int W>
 __device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
     if (++s.rt == s.n_rt) {
         s.rt = 0;
@@ -161,17 +161,15 @@ __device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
             } while (s.n_rt == 0);
         }
     }
-    seg_keys<RT, KT>(s, a);
+    seg_keys<RT, KT, W>(s, a);
 }
 // Units of all segments of sequence b for one KV head.
-template <int RT, int KT>
-__device__ __forceinline__ int seq_units(const AttnArgs& a, int b, int& n_rt, bool& bad) {
-    Seg s;
+template <int RT, int KT, int W>
+__device__ __forceinline__ int seq_units(const AttnArgs& a, int b, Seg& s, bool& bad) {
     bad = seg_seq<RT>(s, a, b);
-    n_rt = s.n_rt;
     int u = 0;
     for (s.rt = 0; s.rt < s.n_rt; ++s.rt) {
-        seg_keys<RT, KT>(s, a);
+        seg_keys<RT, KT, W>(s, a);
         u += s.n_units;
     }
     return u;
@@ -189,49 +187,50 @@ struct Walk {
     int pad;
 };
 static_assert(sizeof(Walk) == 64, "walk");
+template <int W>
 __device__ __forceinline__ int2 walk_tiles(const Walk& w, int warp) {
-    return make_int2(max(w.ua - kSegCost, 0) * kWarps + warp, min(max(w.ub - kSegCost, 0) * kWarps, w.s.n_tiles));
+    return make_int2(max(w.ua - kSegCost, 0) * W + warp, min(max(w.ub - kSegCost, 0) * W, w.s.n_tiles));
 }
 // What happens once a piece stays out of line: the loop over tiles is what the
 // instruction cache has to hold.
-template <int RT, int KT>
-__device__ __noinline__ void walk_next(Walk* w, const AttnArgs* a) {
-    Walk v = *w;
+template <int RT, int KT, int W>
+__device__ __noinline__ void walk_next(const Walk* from, Walk* to, const AttnArgs* a) {
+    Walk v = *from;
     v.left -= v.ub - v.ua;
     v.more = v.left > 0;
     if (v.more) {
-        seg_next<RT, KT>(v.s, *a);
+        seg_next<RT, KT, W>(v.s, *a);
         ++v.seg_no;
         v.ua = 0;
         v.ub = min(v.s.n_units, v.left);
     }
-    *w = v;
+    *to = v;
 }
 // The warp's requests go on to its next piece with tiles: {next tile, end}, {0, 0} at the share's end.
-template <int RT, int KT>
+template <int RT, int KT, int W>
 __device__ __noinline__ int2 request_next(Walk* w, const AttnArgs* a, int warp) {
     for (;;) {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) walk_next<RT, KT>(w, a);
+        if ((threadIdx.x & 31) == 0) walk_next<RT, KT, W>(w, w, a);
         __syncwarp();
         if (!w->more) return make_int2(0, 0);
-        const int2 t = walk_tiles(*w, warp);
+        const int2 t = walk_tiles<W>(*w, warp);
         if (t.x < t.y) return t;
     }
 }
 static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, uint64_t ns) { return mbar_wait(bar, phase, ns); }
 
 template <int HD, int TYPE, int NT>
-__global__ void __launch_bounds__(kWarps * 32, ctas_per_sm(HD, NT))
+__global__ void __launch_bounds__(cta_warps(HD, NT) * 32, ctas_per_sm(HD, NT))
 paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = Cfg<HD, TYPE, NT>;
-    constexpr int RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
+    constexpr int W = C::W, RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
     constexpr bool E4 = C::E4;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     unsigned char* ring = base + warp * NS * C::SLOT;
-    unsigned char* after = base + kWarps * NS * C::SLOT;
+    unsigned char* after = base + W * NS * C::SLOT;
     unsigned char* q_sm = after;                                                         // [RT][QPITCH]
     float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);                         // [warp][RT]
     struct Entry { float ks[2], vs[2]; uint32_t bad, pad[3]; };                          // of a tile's 16-key halves
@@ -240,9 +239,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     int2* views = reinterpret_cast<int2*>(misc + C::META);                               // [2][RT]
     misc += C::META + C::VIEWS;
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc) + warp * 8;
-    Walk* cws = reinterpret_cast<Walk*>(misc + kWarps * 64);                             // [2]
+    Walk* cws = reinterpret_cast<Walk*>(misc + W * 64);                             // [2]
     Walk* pw = cws + 2 + warp;
-    int* scan = reinterpret_cast<int*>(cws + 2 + kWarps);                                // [32]
+    int* scan = reinterpret_cast<int*>(cws + 2 + W);                                // [32]
     float* v_refs = reinterpret_cast<float*>(scan + 32);                                 // [warp]
     const uint32_t ring_u = smem_addr(ring), bars_u = smem_addr(bars);
 
@@ -258,23 +257,22 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- this CTA's share of the units ------------------------------------
-    // (the first 128 sequences are scanned as they are counted)
+    // (a thread for each of the first W * 32 sequences keeps what it reads)
+    constexpr int NTH = W * 32;
     const int cta = blockIdx.x;
-    int u_b = 0, s_b = 0, n_rt_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind the first 128
+    Seg seq;
+    int u_b = 0, s_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind
     {
         bool bad_any = false;
-        for (int b = tid; b < a.n_seq; b += kWarps * 32) {
-            int n_rt;
+        if (tid < a.n_seq) {
+            u_b = seq_units<RT, KT, W>(a, tid, seq, bad_any) * a.n_kv_head;
+            s_b = seq.n_rt * a.n_kv_head;
+        }
+        for (int b = tid + NTH; b < a.n_seq; b += NTH) {
+            Seg s;
             bool bad;
-            const int u = seq_units<RT, KT>(a, b, n_rt, bad) * a.n_kv_head;
-            if (b == tid) {
-                u_b = u;
-                n_rt_b = n_rt;
-                s_b = n_rt * a.n_kv_head;
-            } else {
-                more_u += u;
-                more_s += n_rt * a.n_kv_head;
-            }
+            more_u += seq_units<RT, KT, W>(a, b, s, bad) * a.n_kv_head;
+            more_s += s.n_rt * a.n_kv_head;
             bad_any |= bad;
         }
         if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
@@ -291,45 +289,52 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     };
     int inc = u_b, inc_s = s_b;
     scan_warp(inc, inc_s);
-    if (a.n_seq > kWarps * 32) scan_warp(more_u, more_s);
+    if (a.n_seq > NTH) scan_warp(more_u, more_s);
     if (lane == 31) {
         scan[warp] = inc;
-        scan[4 + warp] = inc_s;
-        scan[8 + warp] = more_u;
-        scan[12 + warp] = more_s;
+        scan[W + warp] = inc_s;
+        scan[2 * W + warp] = more_u;
+        scan[3 * W + warp] = more_s;
     }
     if (tid == 0) cws[0].more = 0;
     __syncthreads();
-    int base_u = scan[0] + scan[1] + scan[2] + scan[3], base_s = scan[4] + scan[5] + scan[6] + scan[7];
-    // (the host refuses batches whose units could pass 31 bits)
-    const int total = base_u + scan[8] + scan[9] + scan[10] + scan[11];
+    int base_u = 0, base_s = 0, total = 0, segs = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) {
+            inc += scan[w];
+            inc_s += scan[W + w];
+        }
+        base_u += scan[w];
+        base_s += scan[W + w];
+        total += scan[2 * W + w];
+        segs += scan[3 * W + w];
+    }
+    total += base_u;             // (the host refuses batches whose units could pass 31 bits)
+    segs += base_s;
     const int n_cta = min((int)gridDim.x, total);
     if (cta == 0 && tid == 0)    // entries of split[] that this call writes
-        *a.n_split = a.split_by_segment ? min(kMaxCtas, base_s + scan[12] + scan[13] + scan[14] + scan[15]) : n_cta;
+        *a.n_split = a.split_by_segment ? min(kMaxCtas, segs) : n_cta;
     if (cta >= n_cta) return;
     // the first `extra` CTAs take one unit more than the others
     const int per_cta = total / n_cta, extra = total - per_cta * n_cta;
     const int u0 = per_cta * cta + min(cta, extra), my_units = per_cta + (cta < extra ? 1 : 0);
     {
-        for (int w = 0; w < warp; ++w) {
-            inc += scan[w];
-            inc_s += scan[4 + w];
-        }
         int b = tid;
         for (;;) {
             if (u_b > 0 && u0 >= inc - u_b && u0 < inc) {      // one thread of the block: the share starts in its sequence
                 Walk w;
                 int rem = u0 - (inc - u_b);
                 const int per_head = u_b / a.n_kv_head;
-                seg_seq<RT>(w.s, a, b);
+                w.s = seq;
                 w.s.h = a.n_kv_head == 1 ? 0 : rem / per_head;
                 rem -= w.s.h * per_head;
                 for (w.s.rt = 0;; ++w.s.rt) {
-                    seg_keys<RT, KT>(w.s, a);
+                    seg_keys<RT, KT, W>(w.s, a);
                     if (rem < w.s.n_units || w.s.rt + 1 >= w.s.n_rt) break;
                     rem -= w.s.n_units;
                 }
-                w.seg_no = inc_s - s_b + w.s.h * n_rt_b + w.s.rt;
+                w.seg_no = inc_s - s_b + w.s.h * w.s.n_rt + w.s.rt;
                 w.ua = rem;
                 w.left = my_units;
                 w.ub = min(w.s.n_units, w.ua + w.left);
@@ -337,36 +342,36 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 cws[0] = w;
             }
             if (u0 < base_u || b - tid >= a.n_seq) break;
-            // behind the first 128 sequences: the next 128
-            b += kWarps * 32;
+            // the next W * 32 sequences
+            b += NTH;
             bool bad;
-            n_rt_b = 0;
-            u_b = b < a.n_seq ? seq_units<RT, KT>(a, b, n_rt_b, bad) * a.n_kv_head : 0;
-            s_b = n_rt_b * a.n_kv_head;
+            seq.n_rt = 0;
+            u_b = b < a.n_seq ? seq_units<RT, KT, W>(a, b, seq, bad) * a.n_kv_head : 0;
+            s_b = seq.n_rt * a.n_kv_head;
             inc = u_b;
             inc_s = s_b;
             scan_warp(inc, inc_s);
             __syncthreads();
             if (lane == 31) {
                 scan[warp] = inc;
-                scan[4 + warp] = inc_s;
+                scan[W + warp] = inc_s;
             }
             __syncthreads();
             inc += base_u;
             inc_s += base_s;
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 if (w < warp) {
                     inc += scan[w];
-                    inc_s += scan[4 + w];
+                    inc_s += scan[W + w];
                 }
                 base_u += scan[w];
-                base_s += scan[4 + w];
+                base_s += scan[W + w];
             }
         }
     }
     // For a piece's rows: the keys each sees, [y, x), and copies of its Q rows to
     // shared memory (a 16-dim group in the order the MMA takes its dims).
-    constexpr int QN = (RT * HD / 8 + kWarps * 32 - 1) / (kWarps * 32);      // 16-byte chunks of a thread
+    constexpr int QN = (RT * HD / 8 + W * 32 - 1) / (W * 32);      // 16-byte chunks of a thread
     uint4 qx[QN];                // (e4m3: on their way)
     auto open_piece = [&](int which) {
         const Walk& w = cws[which];
@@ -384,7 +389,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         const uint32_t q_u = smem_addr(q_sm);
 #pragma unroll
         for (int k = 0; k < QN; ++k) {
-            const int r = (k * kWarps * 32 + tid) / (HD / 8), c = tid % (HD / 8);
+            const int r = (k * W * 32 + tid) / (HD / 8), c = tid % (HD / 8);
             if (r >= RT) break;
             const int i = (row0 + min(r, rows - 1)) / a.group, hh = row0 + min(r, rows - 1) - i * a.group;
             const __half* src = a.q16 + (int64_t)(w.s.tok0 + i) * a.q_stride + (int64_t)(w.s.h * a.group + hh) * HD + c * 8;
@@ -403,7 +408,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         } else if (cws[which].more) {
 #pragma unroll
             for (int k = 0; k < QN; ++k) {
-                const int r = (k * kWarps * 32 + tid) / (HD / 8), c = tid % (HD / 8);
+                const int r = (k * W * 32 + tid) / (HD / 8), c = tid % (HD / 8);
                 if (r >= RT) break;
                 unsigned char* dst = q_sm + r * C::QPITCH + (c >> 1) * 32 + (c & 1) * 8;
                 *reinterpret_cast<uint2*>(dst) = make_uint2(qx[k].x, qx[k].z);
@@ -418,8 +423,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     __syncwarp();
 
     // ---- the warp's ring: slots q = 0, 1, ... hold K, V, K, V, ... of its tiles ----
-    int2 pt = walk_tiles(*pw, warp);   // the next tile to request of the piece, and its end
-    if (pt.x >= pt.y) pt = request_next<RT, KT>(pw, &a, warp);
+    int2 pt = walk_tiles<W>(*pw, warp);   // the next tile to request of the piece, and its end
+    if (pt.x >= pt.y) pt = request_next<RT, KT, W>(pw, &a, warp);
     constexpr int BLK = 32 / SUB;  // tiles of a page block: a lane for each 16 keys
     int blk = 0;                 // tiles of the page block used up
     int b_page = -1, p_page[SUB] = {};
@@ -430,7 +435,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     // for one request ahead of their use.
     auto load_pages = [&]() {
         blk = 0;
-        const int tl = pt.x + lane / SUB * kWarps, key = (pw->s.tile0 + tl) * KT + lane % SUB * kTile;
+        const int tl = pt.x + lane / SUB * W, key = (pw->s.tile0 + tl) * KT + lane % SUB * kTile;
         b_has = tl < pt.y && key < pw->s.n_kv;
         b_page = -1;
         if (b_has) b_page = __ldcg(a.table + pw->s.b * a.table_stride + (key >> a.page_shift));
@@ -491,8 +496,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             }
             i_tile = (i_tile + 1) % C::ENTRIES;
             ++blk;
-            if ((pt.x += kWarps) >= pt.y) {
-                pt = request_next<RT, KT>(pw, &a, warp);
+            if ((pt.x += W) >= pt.y) {
+                pt = request_next<RT, KT, W>(pw, &a, warp);
                 blk = BLK;
             }
             if (blk == BLK) load_pages();
@@ -539,7 +544,23 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         // ---- a piece: its rows and their Q fragments --------------------------
         const Walk& cw = cws[which];
         const int2* view = views + which * RT;
-        const int rows = min(RT, cw.s.n_q * a.group - cw.s.rt * RT);
+        const bool whole = cw.ua == 0 && cw.ub == cw.s.n_units;
+        // state slot: 2*cta + 1 for a segment that goes on in the next CTA from its start here, else 2*cta
+        const int part = 2 * cta + (cw.ua == 0 && !whole ? 1 : 0);
+        const int row0 = cw.s.rt * RT, tok0 = cw.s.tok0, head0 = cw.s.h * a.group;
+        const int rows = min(RT, cw.s.n_q * a.group - row0);
+        if (tid == (W - 1) * 32) {         // (the last warp has no more tiles than the others)
+            // the merge kernel's entry: who holds states of this segment
+            const bool starts = cw.ua == 0, last_piece = cw.left <= cw.ub - cw.ua;
+            Split sp{cta, -1, tok0, row0, rows, cw.s.h, {0, 0}};
+            if (starts && !whole) {
+                const int x = u0 + my_units - cw.left + cw.s.n_units - 1, wide = extra * (per_cta + 1);   // its last unit
+                sp.last = min(n_cta - 1, x < wide ? x / (per_cta + 1) : extra + (x - wide) / per_cta);
+            }
+            const int at = a.split_by_segment ? cw.seg_no : cta;
+            if ((a.split_by_segment ? starts : last_piece) && at < kMaxCtas) a.split[at] = sp;
+            walk_next<RT, KT, W>(&cw, &cws[which ^ 1], &a);
+        }
         const int min_lim = view[0].x, max_low = view[RT - 1].y;       // (rows behind the last see what it sees)
         const uint32_t q_lane = smem_addr(q_sm) + ((lane & 7) + (NT > 1 ? lane >> 4 : 0) * 8) * C::QPITCH +
                                 (NT > 1 ? (lane >> 3) & 1 : lane >> 3) * 16;
@@ -584,9 +605,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             for (int m = 0; m < MT; ++m) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
         }
 
-        const int2 tiles = walk_tiles(cw, warp);
+        const int2 tiles = walk_tiles<W>(cw, warp);
         const int tile0 = cw.s.tile0;
-        for (int t = tiles.x; t < tiles.y; t += kWarps) {
+        for (int t = tiles.x; t < tiles.y; t += W) {
             // ---- S^T = K Q^T ------------------------------------------------
             wait_slot();
             const Entry& en = meta[c_tile];
@@ -846,7 +867,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         for (int n = 0; n < NT; ++n) mma(o[m][n], r, pl[u][n][0], pl[u][n][1]);
                     }
                 }
-            pass_slot(t + kWarps >= tiles.y);        // the piece's last slot takes O first
+            pass_slot(t + W >= tiles.y);        // the piece's last slot takes O first
             c_tile = (c_tile + 1) % C::ENTRIES;
         }
 
@@ -865,23 +886,6 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 if (g == 0) state[warp * RT + n * 8 + 2 * t4 + e] = make_float2(mref[n][e], l[n][e]);
             }
         if (E4 && lane == 0) v_refs[warp] = vref;
-        const bool whole = cw.ua == 0 && cw.ub == cw.s.n_units;
-        // state slot: 2*cta + 1 for a segment that goes on in the next CTA from its start here, else 2*cta
-        const int part = 2 * cta + (cw.ua == 0 && !whole ? 1 : 0);
-        const int row0 = cw.s.rt * RT, tok0 = cw.s.tok0, head0 = cw.s.h * a.group;
-        if (tid == 0) {
-            // the merge kernel's entry: who holds states of this segment
-            const bool starts = cw.ua == 0, last_piece = cw.left <= cw.ub - cw.ua;
-            Split sp{cta, -1, tok0, row0, rows, cw.s.h, {0, 0}};
-            if (starts && !whole) {
-                const int x = u0 + my_units - cw.left + cw.s.n_units - 1, wide = extra * (per_cta + 1);   // its last unit
-                sp.last = min(n_cta - 1, x < wide ? x / (per_cta + 1) : extra + (x - wide) / per_cta);
-            }
-            const int at = a.split_by_segment ? cw.seg_no : cta;
-            if ((a.split_by_segment ? starts : last_piece) && at < kMaxCtas) a.split[at] = sp;
-            cws[which ^ 1] = cw;
-            walk_next<RT, KT>(&cws[which ^ 1], &a);
-        }
         // O^T as fp32 rows in the slot that the warp held back, in chunks of CNT
         // row blocks; dims of a row are moved by its number against bank conflicts
         auto o_at = [](int r, int d) { return r * HD + (d ^ ((r >> 1 & 3) << 3)); };
@@ -903,14 +907,14 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             __syncthreads();
             if (n0 == 0) open_piece(which ^ 1);      // the next piece's Q rows come while this one is written
             const int chunk_rows = min(C::CNT * 8, rows - n0 * 8);
-            for (int w = tid; w < chunk_rows * (HD / 4); w += kWarps * 32) {
+            for (int w = tid; w < chunk_rows * (HD / 4); w += W * 32) {
                 const int rr = w / (HD / 4), r = n0 * 8 + rr, d = (w - rr * (HD / 4)) * 4;
                 float m = -INFINITY, lsum = 0.f;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v) m = fmaxf(m, state[v * RT + r].x);
+                for (int v = 0; v < W; ++v) m = fmaxf(m, state[v * RT + r].x);
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v) {
+                for (int v = 0; v < W; ++v) {
                     const float2 st = state[v * RT + r];
                     if (st.x == -INFINITY) continue;             // no key seen, or no tile
                     float f = ex2(st.x - m);
@@ -964,7 +968,7 @@ static fr_status launch_one(const KvDesc& kv, const AttnArgs& a, int ctas, cudaS
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(C::W * 32);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
