@@ -316,9 +316,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     if (cta == 0 && tid == 0)    // entries of split[] that this call writes
         *a.n_split = a.split_by_segment ? min(kMaxCtas, segs) : n_cta;
     if (cta >= n_cta) return;
-    // the first `extra` CTAs take one unit more than the others
+    // shares [floor(total i / n_cta), floor(total (i + 1) / n_cta)): segments of one
+    // length are cut alike, at their ends where the numbers allow
     const int per_cta = total / n_cta, extra = total - per_cta * n_cta;
-    const int u0 = per_cta * cta + min(cta, extra), my_units = per_cta + (cta < extra ? 1 : 0);
+    auto share = [&](int i) { return per_cta * i + extra * i / n_cta; };
+    const int u0 = share(cta), my_units = share(cta + 1) - u0;
     {
         int b = tid;
         for (;;) {
@@ -554,8 +556,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             const bool starts = cw.ua == 0, last_piece = cw.left <= cw.ub - cw.ua;
             Split sp{cta, -1, tok0, row0, rows, cw.s.h, {0, 0}};
             if (starts && !whole) {
-                const int x = u0 + my_units - cw.left + cw.s.n_units - 1, wide = extra * (per_cta + 1);   // its last unit
-                sp.last = min(n_cta - 1, x < wide ? x / (per_cta + 1) : extra + (x - wide) / per_cta);
+                // the CTA whose share holds its last unit x: the largest c with share(c) <= x
+                const int x = u0 + my_units - cw.left + cw.s.n_units - 1;
+                sp.last = min(n_cta - 1, (int)((((int64_t)x + 1) * n_cta - 1) / total));
             }
             const int at = a.split_by_segment ? cw.seg_no : cta;
             if ((a.split_by_segment ? starts : last_piece) && at < kMaxCtas) a.split[at] = sp;

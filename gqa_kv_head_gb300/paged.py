@@ -19,9 +19,12 @@ _KV = {torch.float16: FR_KV_F16, torch.float8_e4m3fn: FR_KV_E4M3}
 
 def _stream_of(stream, index):
     """Handle of the stream to launch on: the given one, else the current one of GPU `index`."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch.cuda.current_stream(index).cuda_stream
+    return _current(index) if stream is None else stream.cuda_stream
+
+
+# the handle alone, where torch offers it: a Stream object costs a decode call microseconds
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class PagedKV:
@@ -54,14 +57,16 @@ class PagedKV:
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.n_pages, self.n_kv_head, self.page_size, self.hd = n_pages, n_kv_head, page_size, hd
         self.device = k_pages.device
+        self._index = self.device.index
         for t in (v_pages, k_scale, v_scale):
             if t is not None and t.device != self.device:
                 raise ValueError("tensors of a cache must be on one GPU")
+        self._lib = _abi.load()
         self._desc = _abi.FrPagedKV()
         self._p = ctypes.c_void_p(ctypes.addressof(self._desc))
         st = [(ctypes.c_int64 * 3)(*t.stride()[:3]) for t in (k_pages, v_pages)]
         with torch.cuda.device(self.device):
-            _abi.check(_abi.load().fr_paged_kv_init(
+            _abi.check(self._lib.fr_paged_kv_init(
                 self._p, _KV[k_pages.dtype], k_pages.data_ptr(), st[0], v_pages.data_ptr(), st[1],
                 k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None, n_pages, page_size,
                 n_kv_head, hd), "fr_paged_kv_init")
@@ -108,20 +113,20 @@ class PagedBatch:
                     stride, n_seq, n_tok, max_pages), "fr_paged_batch_init")
             if len(self._by_rows) >= 64:
                 self._by_rows.clear()
-            self._by_rows[n_tok] = d
-        return ctypes.addressof(d)
+            d = self._by_rows[n_tok] = (ctypes.addressof(d), d)
+        return d[0]
 
 
 def _rows(t, name, cache):
-    """k_new / v_new: [n_tok, n_kv_head, hd] with contiguous heads, or [n_tok, n_kv_head * hd]; returns the token stride."""
-    if t.dim() == 3:
-        ok = tuple(t.shape[1:]) == (cache.n_kv_head, cache.hd) and t.stride(2) == 1 and (
-            cache.n_kv_head == 1 or t.stride(1) == cache.hd)
+    """k_new / v_new: [n_tok, n_kv_head, hd] with contiguous heads, or [n_tok, n_kv_head * hd]; returns (n_tok, token stride)."""
+    shape, stride, heads, hd = t.shape, t.stride(), cache.n_kv_head, cache.hd
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == hd and stride[2] == 1 and (heads == 1 or stride[1] == hd)
     else:
-        ok = t.dim() == 2 and t.shape[1] == cache.n_kv_head * cache.hd and t.stride(1) == 1
+        ok = len(shape) == 2 and shape[1] == heads * hd and stride[1] == 1
     if not ok:
         raise ValueError(f"{name} must be [n_tok, n_kv_head, hd] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else cache.n_kv_head * cache.hd
+    return shape[0], stride[0] if shape[0] > 1 else heads * hd
 
 
 def kv_append_paged(cache, batch, k_new, v_new, pos, rope, workspace=None, stream=None):
@@ -131,20 +136,24 @@ def kv_append_paged(cache, batch, k_new, v_new, pos, rope, workspace=None, strea
     stride may be larger, e.g. columns of a fused QKV buffer); pos: int32
     [n_tok]. workspace: optional, its status word reports bad pages and lengths
     (workspace_check)."""
-    _check_dev(k_new, v_new, pos, workspace)
-    if k_new.dtype not in _ROWS or v_new.dtype != k_new.dtype:
+    if not (k_new.is_cuda and v_new.is_cuda and pos.is_cuda and (workspace is None or workspace.is_cuda)):
+        raise ValueError("tensors must be CUDA tensors")
+    dtype = k_new.dtype
+    if dtype not in _ROWS or v_new.dtype != dtype:
         raise TypeError("k_new and v_new must both be float32 or both float16")
     if pos.dtype != torch.int32:
         raise TypeError("pos must be int32")
-    k_stride, v_stride = _rows(k_new, "k_new", cache), _rows(v_new, "v_new", cache)
-    n_tok = k_new.shape[0]
-    if v_new.shape[0] != n_tok or pos.dim() != 1 or pos.shape[0] != n_tok or not pos.is_contiguous():
+    n_tok, k_stride = _rows(k_new, "k_new", cache)
+    n_v, v_stride = _rows(v_new, "v_new", cache)
+    if n_v != n_tok or pos.shape != (n_tok,) or not pos.is_contiguous():
         raise ValueError("k_new, v_new and pos must have one row a token")
-    st = _abi.load().fr_kv_append_paged(
-        cache._p, batch._desc(n_tok), _ROWS[k_new.dtype], k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
-        pos.data_ptr(), ctypes.addressof(_as_rope(rope)), None if workspace is None else workspace.data_ptr(),
-        _stream_of(stream, cache.device))
-    _abi.check(st, "fr_kv_append_paged")
+    rope = _as_rope(rope)
+    st = cache._lib.fr_kv_append_paged(
+        cache._p, batch._desc(n_tok), _ROWS[dtype], k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+        pos.data_ptr(), ctypes.addressof(rope), None if workspace is None else workspace.data_ptr(),
+        _stream_of(stream, cache._index))
+    if st:
+        _abi.check(st, "fr_kv_append_paged")
 
 
 def paged_attn_workspace_size(n_head, n_kv_head, hd):
@@ -158,7 +167,7 @@ def make_paged_workspace(n_head, n_kv_head, hd, device="cuda", stream=None):
         raise FrError(2, "fr_paged_attn_workspace_size")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _abi.check(_abi.load().fr_workspace_init(ws.data_ptr(), n, _stream_of(stream, ws.device)), "fr_workspace_init")
+        _abi.check(_abi.load().fr_workspace_init(ws.data_ptr(), n, _stream_of(stream, ws.device.index)), "fr_workspace_init")
     return ws
 
 
@@ -169,27 +178,29 @@ def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0
     sequence sees the keys up to its own; window > 0: only the last `window` of
     them. Returns out [n_tok, n_head, hd] f32; rows behind the last sequence are
     left as they were."""
-    _check_dev(q16, out, workspace)
-    hd = cache.hd
+    if not (q16.is_cuda and (out is None or out.is_cuda) and (workspace is None or workspace.is_cuda)):
+        raise ValueError("tensors must be CUDA tensors")
+    hd, shape, strides = cache.hd, q16.shape, q16.stride()
     if q16.dtype != torch.float16:
         raise TypeError("q16 must be float16")
-    if q16.dim() == 2 and q16.shape[1] == hd and q16.shape[0] % n_head == 0 and q16.is_contiguous():
-        n_tok, stride = q16.shape[0] // n_head, n_head * hd
-    elif q16.dim() == 3 and tuple(q16.shape[1:]) == (n_head, hd) and q16.stride(2) == 1 and (
-            n_head == 1 or q16.stride(1) == hd):
-        n_tok = q16.shape[0]
-        stride = q16.stride(0) if n_tok > 1 else n_head * hd
+    if len(shape) == 3 and shape[1] == n_head and shape[2] == hd and strides[2] == 1 and (
+            n_head == 1 or strides[1] == hd):
+        n_tok = shape[0]
+        stride = strides[0] if n_tok > 1 else n_head * hd
+    elif len(shape) == 2 and shape[1] == hd and n_head > 0 and shape[0] % n_head == 0 and q16.is_contiguous():
+        n_tok, stride = shape[0] // n_head, n_head * hd
     else:
         raise ValueError("q16 must be [n_tok, n_head, hd] with contiguous heads, or [n_tok * n_head, hd] contiguous")
     if out is None:
         with torch.cuda.stream(stream):
             out = torch.empty((n_tok, n_head, hd), dtype=torch.float32, device=q16.device)
-    elif out.dtype != torch.float32 or tuple(out.shape) != (n_tok, n_head, hd) or not out.is_contiguous():
+    elif out.dtype != torch.float32 or out.shape != (n_tok, n_head, hd) or not out.is_contiguous():
         raise ValueError("out must be contiguous float32 [n_tok, n_head, hd]")
     if workspace is None:
         workspace = make_paged_workspace(n_head, cache.n_kv_head, hd, cache.device, stream)
-    st = _abi.load().fr_paged_attn(
+    st = cache._lib.fr_paged_attn(
         cache._p, batch._desc(n_tok), q16.data_ptr(), stride, n_head, 1 if causal else 0, window, kq_scale,
-        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache.device))
-    _abi.check(st, "fr_paged_attn")
+        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache._index))
+    if st:
+        _abi.check(st, "fr_paged_attn")
     return out
