@@ -84,8 +84,9 @@ struct SeqInfo {
 __device__ __forceinline__ SeqInfo seq_info(const int32_t* tok_start, const int32_t* kv_len, int b, int n_tok,
                                             int max_pages, int page_shift) {
     SeqInfo s;
-    // (past L1: the kernel before may have written them while this one was starting)
-    const int t0 = __ldcg(tok_start + b), t1 = __ldcg(tok_start + b + 1), n = __ldcg(kv_len + b);
+    // (plain loads: the kernel before may have written these while this one was
+    // starting, which the read-only path does not cover)
+    const int t0 = tok_start[b], t1 = tok_start[b + 1], n = kv_len[b];
     const int64_t most = (int64_t)max_pages << page_shift;
     s.bad = t0 < 0 || t1 < t0 || t1 > n_tok || n < 0 || n > most;
     s.tok0 = t0;

@@ -3,12 +3,19 @@
 // as e4m3 codes with one power-of-two scale for each page and head.
 //
 // Bound by the bytes of the rows read and written; a decode step (one row for
-// each sequence) is bound by latency. One block takes one piece (a sequence's
-// new rows inside one page) of kHeads heads, K or V: an e4m3 page has its
-// scale from every row in it, so one block must see all of a page's new rows.
-// A work item is 8 elements of a row: four rotated pairs (or 8 contiguous
-// elements), loaded as two vectors and kept in registers between the maximum
-// and the rounding, so the rows are read once.
+// each sequence) is bound by latency. A block takes one piece (a sequence's new
+// rows inside one page, or for f16 pages inside a part of one), K or V:
+//   * one head, small blocks (kv_append_paged_kernel): decode steps, and the
+//     shapes that the other kernel leaves out;
+//   * several heads one after the other (kv_append_prompt_kernel): prompts. The
+//     angles of a row are the same for every head, and at about 100 instructions
+//     an angle, computed for each head again, they took longer than the bytes.
+//     So a thread keeps the cosines and sines of its few row places in
+//     registers and takes head after head through them. (Shared over a cluster
+//     through its distributed memory instead, they took as long as before.)
+// An e4m3 page has its scale from every row in it, so one block sees all of a
+// page's new rows of a head; rows are read once and stay in registers between
+// the maximum and the rounding.
 //
 // e4m3: s = the smallest power of two with amax <= 448 s over the page. New
 // rows may make it grow; the page's earlier codes are then stored again at the
@@ -34,7 +41,6 @@ struct AppendArgs {
     int n_seq, n_tok, max_pages, n_pages, page_shift, n_kv_head;
 };
 
-constexpr int kKeep = 8;                  // items of a thread held in registers
 constexpr int kMinScaleExp = -100;        // smallest scale 2^-100: its reciprocal stays normal
 
 // Smallest power of two s with amax <= 448 s, amax finite and >= 0.
@@ -58,333 +64,449 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
+// One copy of the angle's code: inlined for every element, the slow reduction of
+// sincosf alone would outgrow the instruction cache.
+__device__ __noinline__ float2 rope_cs_call(int pos, int i, const RopeTable* tb) {
+    float2 r;
+    rope_cs_tab(pos, i, *tb, r.x, r.y);
+    return r;
 }
-template <>
-__device__ __forceinline__ float4 load4<__half>(const __half* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x)),
-                 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-template <typename T>
-__device__ __forceinline__ float load1(const T* p);
-template <>
-__device__ __forceinline__ float load1<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load1<__half>(const __half* p) { return __half2float(__ldg(p)); }
 
-// The 8 elements of item c (slots 4c .. 4c + 3 of a K row, or elements 8c ..
-// 8c + 7 of a V row): vectors at d0 and d1, or (single) one dim for each.
-struct Item {
-    int d[8];
-    bool vec;
+// Four elements of a row as they come, and as floats.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    using V = float4;
+    __device__ static __forceinline__ float4 floats(const V& v) { return v; }
+    __device__ static __forceinline__ float one(const float* p) { return *p; }
+};
+template <> struct Raw<__half> {
+    using V = uint2;
+    __device__ static __forceinline__ float4 floats(const V& v) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)),
+                     b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    __device__ static __forceinline__ float one(const __half* p) { return __half2float(*p); }
 };
 
-// T: type of the new rows; E4: e4m3 pages; HEADS: heads of one block.
-template <typename T, int HD, bool E4, int HEADS>
+// The nth piece: the sequences' pieces (of 2^shift rows at most, aligned) in
+// order, counted from their lengths. Every warp finds it alone, with no barrier
+// ahead of the loads, 128 sequences at a time so that their numbers arrive together.
+struct Piece {
+    int b, first, last, tok, row0, row1;      // sequence; its new cache rows; token of row0; the piece's cache rows
+    bool found;
+};
+__device__ __forceinline__ Piece find_piece(const AppendArgs& a, int shift, int nth) {
+    const int lane = threadIdx.x & 31;
+    Piece p;
+    p.found = false;
+    for (int b0 = 0; b0 < a.n_seq && !p.found; b0 += 128) {
+        int f[4], t[4], q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = t[i] = q[i] = 0;
+            if (b0 + i * 32 + lane < a.n_seq) {
+                const SeqInfo s = seq_info(a.tok_start, a.kv_len, b0 + i * 32 + lane, a.n_tok, a.max_pages, a.page_shift);
+                if (!s.bad && s.n_q <= s.n_kv) {
+                    f[i] = s.n_kv - s.n_q;
+                    t[i] = s.tok0;
+                    q[i] = s.n_q;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (p.found) continue;
+            const int n = q[i] > 0 ? ((f[i] + q[i] - 1) >> shift) - (f[i] >> shift) + 1 : 0;
+            int inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const unsigned hit = __ballot_sync(~0u, nth < inc);        // the first of these lanes has it
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                p.found = true;
+                p.b = b0 + i * 32 + at;
+                p.first = __shfl_sync(~0u, f[i], at);
+                p.last = p.first + __shfl_sync(~0u, q[i], at);
+                const int unit = (p.first >> shift) + nth - __shfl_sync(~0u, inc - n, at);
+                p.row0 = max(p.first, unit << shift);
+                p.row1 = min(p.last, (unit + 1) << shift);
+                p.tok = __shfl_sync(~0u, t[i], at) + p.row0 - p.first;
+            } else {
+                nth -= __shfl_sync(~0u, inc, 31);
+            }
+        }
+    }
+    return p;
+}
+// One warp of the grid looks at every sequence's numbers.
+__device__ __forceinline__ void report_bad(const AppendArgs& a) {
+    if (!a.status || blockIdx.x || blockIdx.y || threadIdx.x >= 32) return;
+    bool bad = false;
+    for (int i = threadIdx.x; i < a.n_seq; i += 32) {
+        const SeqInfo s = seq_info(a.tok_start, a.kv_len, i, a.n_tok, a.max_pages, a.page_shift);
+        bad |= s.bad || s.n_q > s.n_kv;
+    }
+    if (bad) atomicOr(a.status, kStatusInput);
+}
+// An e4m3 page's rows 0 .. rows - 1, hd of them a row, at a scale grown by 1 / ratio.
+__device__ __forceinline__ void restore_rows(unsigned char* page, int rows, int items, int64_t row_stride, float ratio) {
+    for (int w = threadIdx.x; w < rows * items; w += blockDim.x) {
+        uint2* p = reinterpret_cast<uint2*>(page + w / items * row_stride + w % items * 8);
+        uint2 y = *p;
+        const float2 a0 = from_e4m3x2(y.x & 0xffffu), a1 = from_e4m3x2(y.x >> 16), a2 = from_e4m3x2(y.y & 0xffffu),
+                     a3 = from_e4m3x2(y.y >> 16);
+        y.x = to_e4m3x4(a0.x * ratio, a0.y * ratio, a1.x * ratio, a1.y * ratio);
+        y.y = to_e4m3x4(a2.x * ratio, a2.y * ratio, a3.x * ratio, a3.y * ratio);
+        *p = y;
+    }
+}
+// The larger of m and the finite magnitudes of y (infinities and NaN set no scale).
+__device__ __forceinline__ float widen(float m0, const float* y) {
+    float m = m0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(y[u]));                // (NaN leaves it)
+    if (m > 3.402823466e38f) {
+        m = m0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (fabsf(y[u]) <= 3.402823466e38f) m = fmaxf(m, fabsf(y[u]));
+    }
+    return m;
+}
+// rope_lo and rope_hi at scale 1.
+__device__ __forceinline__ void rotate(float& lo, float& hi, const float2& cs) {
+    const float x = lo, y = hi;
+    lo = __fmaf_rn(x, cs.x, -__fmul_rn(y, cs.y));
+    hi = __fmaf_rn(x, cs.y, __fmul_rn(y, cs.x));
+}
+
+// T: type of the new rows; E4: e4m3 pages; KEEP: items of a thread held in registers.
+template <typename T, int HD, bool E4, int KEEP>
 __global__ void __launch_bounds__(256)
-kv_append_paged_kernel(const AppendArgs a, const __grid_constant__ RopeTable tb) {
+kv_append_paged_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RopeTable tb) {
     constexpr int ITEMS = HD / 8;                 // items of a row
-    constexpr int KEEP = kKeep / HEADS;
-    __shared__ int sc[16];
-    __shared__ float red[8][HEADS];
+    using V = typename Raw<T>::V;
+    __shared__ float red[8];
+    const bool is_v = blockIdx.x & 1;             // neighbours, so that K's arithmetic overlaps V's loads
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, warps = nthr >> 5;
-    const bool is_v = blockIdx.z != 0;
-    const int ps = 1 << a.page_shift;
-
-    // ---- which piece: the sequences' pieces in order, counted from kv_len -----
-    const int64_t want = blockIdx.x;
-    int64_t base = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < a.n_seq && !found; b0 += nthr) {
-        const int b = b0 + tid;
-        int n = 0, first = 0, tok0 = 0, n_q = 0;
-        bool bad = false;
-        if (b < a.n_seq) {
-            const SeqInfo s = seq_info(a.tok_start, a.kv_len, b, a.n_tok, a.max_pages, a.page_shift);
-            bad = s.bad || s.n_q > s.n_kv;
-            if (!bad && s.n_q > 0) {
-                tok0 = s.tok0;
-                n_q = s.n_q;
-                first = s.n_kv - s.n_q;
-                n = ((s.n_kv - 1) >> a.page_shift) - (first >> a.page_shift) + 1;
-            }
-        }
-        if (bad && a.status && want == 0 && blockIdx.y == 0 && !is_v) atomicOr(a.status, kStatusInput);
-        int inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += x;
-        }
-        if (lane == 31) sc[warp] = inc;
-        if (tid == 0) sc[8] = -1;
-        __syncthreads();
-        int64_t off = base;
-        for (int w = 0; w < warp; ++w) off += sc[w];
-        const int64_t end = off + inc;
-        if (n > 0 && want >= end - n && want < end) {
-            sc[8] = b;
-            sc[9] = (int)(want - (end - n));
-            sc[10] = first;
-            sc[11] = tok0;
-            sc[12] = n_q;
-        }
-        int64_t all = 0;
-        for (int w = 0; w < warps; ++w) all += sc[w];
-        base += all;
-        __syncthreads();
-        found = sc[8] >= 0;
-        if (!found) __syncthreads();
-    }
-    if (!found) return;
-    const int b = sc[8], first = sc[10], last = first + sc[12];          // cache rows [first, last) are new
-    const int pi = (first >> a.page_shift) + sc[9];                      // page of the sequence
-    const int page = __ldcg(a.table + b * a.table_stride + pi);
-    if (page < 0 || page >= a.n_pages) {
-        if (tid == 0 && a.status) atomicOr(a.status, kStatusInput);
-        return;
-    }
-    const int r0 = max(first - (pi << a.page_shift), 0), r1 = min(last - (pi << a.page_shift), ps);
-    const int tok = sc[11] + (pi << a.page_shift) + r0 - first;          // token of row r0
-    const int h0 = blockIdx.y * HEADS, nh = min(HEADS, a.n_kv_head - h0);
-    const T* src = reinterpret_cast<const T*>(is_v ? a.v_new : a.k_new);
+    const Piece pc = find_piece(a, a.page_shift, (int)(blockIdx.x >> 1));
+    report_bad(a);
+    if (!pc.found) return;                                               // fewer pieces than blocks
+    const int pi = pc.row0 >> a.page_shift;                              // page of the sequence
+    const int page = a.table[pc.b * a.table_stride + pi];
+    const int r0 = pc.row0 - (pi << a.page_shift), tok = pc.tok;
+    const int h = blockIdx.y;
+    const T* src = reinterpret_cast<const T*>(is_v ? a.v_new : a.k_new) + (int64_t)tok * (is_v ? a.v_stride : a.k_stride) + h * HD;
     const int64_t s_tok = is_v ? a.v_stride : a.k_stride;
-    const int64_t p_page = is_v ? a.v_page : a.k_page, p_head = is_v ? a.v_head : a.k_head, p_row = is_v ? a.v_row : a.k_row;
-    const int n_items = (r1 - r0) * ITEMS;
-    const bool vec = is_v || (tb.n_dims & 7) == 0;
+    const int64_t p_row = is_v ? a.v_row : a.k_row;
+    const int64_t p_base = page * (is_v ? a.v_page : a.k_page) + h * (is_v ? a.v_head : a.k_head);
 
-    auto item_dims = [&](int c) {
-        Item it;
-        it.vec = vec;
-        if (is_v) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) it.d[u] = c * 8 + u;
+    // This thread's items: rows r, r + rstep, ... of the piece, all at place c of
+    // their row (a block's threads are a multiple of a row's items). x[u] and
+    // x[4 + u] are the two dims of slot 4c + u: where rotated dims come as
+    // vectors, at d0 .. d0 + 3 and d1 .. d1 + 3; other vectors are 8 contiguous
+    // elements, which no rotation touches.
+    const int c = tid % ITEMS, r = tid / ITEMS, rstep = nthr / ITEMS, n_rows = pc.row1 - pc.row0;
+    const bool vec = is_v || (tb.n_dims & 7) == 0, rot = !is_v && c * 4 < tb.half;
+    const int d0 = rot ? c * 4 : c * 8, d1 = rot ? c * 4 + tb.half : c * 8 + 4;
+    V raw[KEEP][2];
+    float x[E4 ? KEEP : 1][8];
+    auto load = [&](int i, V* v) {
+        if (i < n_rows && vec) {
+            const T* row = src + i * s_tok;
+            v[0] = *reinterpret_cast<const V*>(row + d0);
+            v[1] = *reinterpret_cast<const V*>(row + d1);
+        }
+    };
+    // item (row i, place c) as rotated floats, from its vectors or (n_dims no multiple of 8) element by element
+    auto values = [&](int i, const V* v, float* y) {
+        if (vec) {
+            const float4 p = Raw<T>::floats(v[0]), q = Raw<T>::floats(v[1]);
+            y[0] = p.x; y[1] = p.y; y[2] = p.z; y[3] = p.w;
+            y[4] = q.x; y[5] = q.y; y[6] = q.z; y[7] = q.w;
         } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                int x, y;
-                rope_slot_dims(c * 4 + u, tb, x, y);
-                it.d[2 * u] = x;
-                it.d[2 * u + 1] = y;
+                int p, q;
+                rope_slot_dims(c * 4 + u, tb, p, q);
+                y[u] = Raw<T>::one(src + i * s_tok + p);
+                y[4 + u] = Raw<T>::one(src + i * s_tok + q);
             }
         }
-        return it;
-    };
-    // Elements in slot order: x[2u], x[2u + 1] are slot u's two dims. A rotated
-    // vector item has its first dims at d[0] .. d[0] + 3 and its second ones at
-    // d[1] .. d[1] + 3; the others are 8 contiguous elements from d[0].
-    auto rotated = [&](int c) { return !is_v && c * 4 < tb.half; };
-    auto load = [&](const Item& it, int c, const T* row, float* x) {
-        if (it.vec) {
-            const bool rot = rotated(c);
-            const float4 p = load4<T>(row + it.d[0]), q = load4<T>(row + (rot ? it.d[1] : it.d[0] + 4));
-            if (rot) {
-                x[0] = p.x; x[2] = p.y; x[4] = p.z; x[6] = p.w;
-                x[1] = q.x; x[3] = q.y; x[5] = q.z; x[7] = q.w;
-            } else {
-                x[0] = p.x; x[1] = p.y; x[2] = p.z; x[3] = p.w;
-                x[4] = q.x; x[5] = q.y; x[6] = q.z; x[7] = q.w;
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = load1<T>(row + it.d[u]);
-        }
-    };
-    auto angles = [&](int c, int t, float* cs, float* sn) {
-        if (is_v) return;
-        const int p = __ldg(a.pos + t);
+        if (!rot) return;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (c * 4 + u < tb.half) rope_cs_tab(p, c * 4 + u, tb, cs[u], sn[u]);
+            if (c * 4 + u < tb.half) rotate(y[u], y[4 + u], rope_cs_call(a.pos[tok + i], c * 4 + u, &tb));
     };
-    auto rotate = [&](int c, const float* cs, const float* sn, float* x) {
-        if (is_v) return;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (c * 4 + u < tb.half) {
-                const float x0 = x[2 * u], x1 = x[2 * u + 1];
-                x[2 * u] = rope_lo(x0, x1, cs[u], sn[u], 1.f);
-                x[2 * u + 1] = rope_hi(x0, x1, cs[u], sn[u], 1.f);
-            }
-    };
-    auto store = [&](const Item& it, int c, int64_t at, const float* x, float inv) {
-        const bool rot = rotated(c);
+    auto store = [&](int i, const float* y, float inv) {
+        const int64_t at = p_base + (r0 + i) * p_row;
         if (E4) {
             unsigned char* dst = reinterpret_cast<unsigned char*>(is_v ? a.v : a.k) + at;
-            if (it.vec) {
-                const uint32_t p = rot ? to_e4m3x4(x[0] * inv, x[2] * inv, x[4] * inv, x[6] * inv)
-                                       : to_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-                const uint32_t q = rot ? to_e4m3x4(x[1] * inv, x[3] * inv, x[5] * inv, x[7] * inv)
-                                       : to_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-                if (rot) {
-                    *reinterpret_cast<uint32_t*>(dst + it.d[0]) = p;
-                    *reinterpret_cast<uint32_t*>(dst + it.d[1]) = q;
-                } else {
-                    *reinterpret_cast<uint2*>(dst + it.d[0]) = make_uint2(p, q);
-                }
+            if (vec) {
+                *reinterpret_cast<uint32_t*>(dst + d0) = to_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+                *reinterpret_cast<uint32_t*>(dst + d1) = to_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
             } else {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) dst[it.d[u]] = (unsigned char)to_e4m3x4(x[u] * inv, 0.f, 0.f, 0.f);
+                for (int u = 0; u < 4; ++u) {
+                    int p, q;
+                    rope_slot_dims(c * 4 + u, tb, p, q);
+                    dst[p] = (unsigned char)to_e4m3x4(y[u] * inv, 0.f, 0.f, 0.f);
+                    dst[q] = (unsigned char)to_e4m3x4(y[4 + u] * inv, 0.f, 0.f, 0.f);
+                }
             }
         } else {
             __half* dst = reinterpret_cast<__half*>(is_v ? a.v : a.k) + at;
-            if (it.vec) {
-                const uint2 p = rot ? make_uint2(pack_half2(x[0], x[2]), pack_half2(x[4], x[6]))
-                                    : make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
-                const uint2 q = rot ? make_uint2(pack_half2(x[1], x[3]), pack_half2(x[5], x[7]))
-                                    : make_uint2(pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
-                if (rot) {
-                    *reinterpret_cast<uint2*>(dst + it.d[0]) = p;
-                    *reinterpret_cast<uint2*>(dst + it.d[1]) = q;
-                } else {
-                    *reinterpret_cast<uint4*>(dst + it.d[0]) = make_uint4(p.x, p.y, q.x, q.y);
-                }
+            if (vec) {
+                *reinterpret_cast<uint2*>(dst + d0) = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
+                *reinterpret_cast<uint2*>(dst + d1) = make_uint2(pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
             } else {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) dst[it.d[u]] = __float2half_rn(x[u]);
+                for (int u = 0; u < 4; ++u) {
+                    int p, q;
+                    rope_slot_dims(c * 4 + u, tb, p, q);
+                    dst[p] = __float2half_rn(y[u]);
+                    dst[q] = __float2half_rn(y[4 + u]);
+                }
             }
         }
     };
-    auto at_row = [&](int r, int h) { return page * p_page + (int64_t)h * p_head + (int64_t)r * p_row; };
-
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) load(r + k * rstep, raw[k]);
+    const bool bad_page = page < 0 || page >= a.n_pages;
+    if (bad_page && tid == 0 && a.status) atomicOr(a.status, kStatusInput);
+    if (bad_page) return;
+    const int behind = r + KEEP * rstep;          // rows that registers do not hold
     if (!E4) {
-        for (int w = tid; w < n_items; w += nthr) {
-            const int i = w / ITEMS, c = w - i * ITEMS;
-            const T* row = src + (int64_t)(tok + i) * s_tok + (int64_t)h0 * HD;
-            const Item it = item_dims(c);
-            float x[HEADS][8], cs[4], sn[4];
 #pragma unroll
-            for (int h = 0; h < HEADS; ++h)
-                if (h < nh) load(it, c, row + h * HD, x[h]);
-            angles(c, tok + i, cs, sn);
-#pragma unroll
-            for (int h = 0; h < HEADS; ++h)
-                if (h < nh) {
-                    rotate(c, cs, sn, x[h]);
-                    store(it, c, at_row(r0 + i, h0 + h), x[h], 1.f);
-                }
+        for (int k = 0; k < KEEP; ++k) {
+            const int i = r + k * rstep;
+            if (i >= n_rows) break;
+            values(i, raw[k], x[0]);
+            store(i, x[0], 1.f);
+        }
+        for (int i = behind; i < n_rows; i += rstep) {
+            V v[2];
+            load(i, v);
+            values(i, v, x[0]);
+            store(i, x[0], 1.f);
         }
         return;
     }
-
-    // ---- e4m3: the largest finite value first ------------------------------
-    float* scale = (is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.n_kv_head + h0;
-    float kept[KEEP][HEADS][8], amax[HEADS], old[HEADS];
+    // ---- e4m3: the page's scale from the largest finite value ----------------
+    float* scale = (is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.n_kv_head + h;
+    const float old = r0 > 0 ? *scale : 0.f;                              // a page's first rows start it anew
+    float amax = 0.f;
 #pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-        amax[h] = 0.f;
-        old[h] = r0 > 0 && h < nh ? scale[h] : 0.f;           // a page's first rows start it anew
+    for (int k = 0; k < KEEP; ++k) {
+        const int i = r + k * rstep;
+        if (i >= n_rows) break;
+        values(i, raw[k], x[k]);
+        amax = widen(amax, x[k]);
     }
-    auto fetch = [&](int w, float (*x)[8]) {
-        const int i = w / ITEMS, c = w - i * ITEMS;
-        const T* row = src + (int64_t)(tok + i) * s_tok + (int64_t)h0 * HD;
-        const Item it = item_dims(c);
-        float cs[4], sn[4];
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h)
-            if (h < nh) load(it, c, row + h * HD, x[h]);
-        angles(c, tok + i, cs, sn);
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h)
-            if (h < nh) rotate(c, cs, sn, x[h]);
-    };
-    auto widen = [&](float (*x)[8]) {
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h)
-            if (h < nh)
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float v = fabsf(x[h][u]);
-                    if (v <= 3.402823466e38f) amax[h] = fmaxf(amax[h], v);    // inf and NaN set no scale
-                }
-    };
-#pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        if (tid + k * nthr < n_items) {
-            fetch(tid + k * nthr, kept[k]);
-            widen(kept[k]);
-        }
-    for (int w = tid + KEEP * nthr; w < n_items; w += nthr) {
-        float x[HEADS][8];
-        fetch(w, x);
-        widen(x);
+    for (int i = behind; i < n_rows; i += rstep) {
+        V v[2];
+        float y[8];
+        load(i, v);
+        values(i, v, y);
+        amax = widen(amax, y);
     }
 #pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) amax[h] = fmaxf(amax[h], __shfl_xor_sync(~0u, amax[h], o));
-        if (lane == 0) red[warp][h] = amax[h];
-    }
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if (lane == 0) red[warp] = amax;
     __syncthreads();
-    float inv[HEADS];
+    float m = red[0];
+    for (int w = 1; w < warps; ++w) m = fmaxf(m, red[w]);
+    const float s = fmaxf(pow2_scale(m), old), inv = 1.f / s;
+    if (tid == 0) *scale = s;
+    if (r0 > 0 && s > old)                                    // the page's earlier rows at the grown scale
+        restore_rows(reinterpret_cast<unsigned char*>(is_v ? a.v : a.k) + p_base, r0, ITEMS, p_row, old / s);
 #pragma unroll
-    for (int h = 0; h < HEADS; ++h) {
-        float m = red[0][h];
-        for (int w = 1; w < warps; ++w) m = fmaxf(m, red[w][h]);
-        const float s = fmaxf(pow2_scale(m), old[h]);
-        inv[h] = 1.f / s;
-        if (h < nh) {
-            if (tid == 0) scale[h] = s;
-            if (r0 > 0 && s > old[h]) {                       // the page's earlier rows at the grown scale
-                const float ratio = old[h] / s;
-                for (int w = tid; w < r0 * (HD / 8); w += nthr) {
-                    const int r = w / (HD / 8), c = w - r * (HD / 8);
-                    uint2* p = reinterpret_cast<uint2*>(reinterpret_cast<unsigned char*>(is_v ? a.v : a.k) +
-                                                        at_row(r, h0 + h) + c * 8);
-                    uint2 x = *p;
-                    const float2 a0 = from_e4m3x2(x.x & 0xffffu), a1 = from_e4m3x2(x.x >> 16),
-                                 a2 = from_e4m3x2(x.y & 0xffffu), a3 = from_e4m3x2(x.y >> 16);
-                    x.x = to_e4m3x4(a0.x * ratio, a0.y * ratio, a1.x * ratio, a1.y * ratio);
-                    x.y = to_e4m3x4(a2.x * ratio, a2.y * ratio, a3.x * ratio, a3.y * ratio);
-                    *p = x;
-                }
-            }
-        }
+    for (int k = 0; k < KEEP; ++k) {
+        const int i = r + k * rstep;
+        if (i >= n_rows) break;
+        store(i, x[k], inv);
     }
-    auto put = [&](int w, float (*x)[8]) {
-        const int i = w / ITEMS, c = w - i * ITEMS;
-        const Item it = item_dims(c);
-#pragma unroll
-        for (int h = 0; h < HEADS; ++h)
-            if (h < nh) store(it, c, at_row(r0 + i, h0 + h), x[h], inv[h]);
-    };
-#pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        if (tid + k * nthr < n_items) put(tid + k * nthr, kept[k]);
-    for (int w = tid + KEEP * nthr; w < n_items; w += nthr) {
-        float x[HEADS][8];
-        fetch(w, x);
-        put(w, x);
+    for (int i = behind; i < n_rows; i += rstep) {
+        V v[2];
+        float y[8];
+        load(i, v);
+        values(i, v, y);
+        store(i, y, inv);
     }
 }
 
+// Prompts, n_dims a multiple of 8. A thread has place c of KR rows and takes the
+// block's heads through them, HC heads' loads at a time; the angles are computed
+// while the first of these are on their way. e4m3: 512 threads hold KR = 2 rows
+// each, so a page has at most 1024 items (64 rows at hd 128).
+template <typename T, bool E4>
+struct Prompt {
+    static constexpr int THREADS = E4 ? 512 : 256, KR = E4 ? 2 : 1;
+    static constexpr int HC = (E4 ? 4 : 8) / (sizeof(T) == 4 ? 2 : 1);
+};
 template <typename T, int HD, bool E4>
-static cudaError_t launch_append(const AppendArgs& a, const RopeTable& tb, cudaStream_t st) {
-    // at most one piece a token, and for each sequence its whole pages and two partly new ones
-    const int64_t by_page = 2 * (int64_t)a.n_seq + (a.n_tok >> a.page_shift);
-    const int64_t pieces = a.n_tok < by_page ? a.n_tok : by_page;
-    // two heads share a block's angles once there are blocks enough without
-    const bool two = a.n_kv_head > 1 && pieces * a.n_kv_head >= 608;
+__global__ void __launch_bounds__((Prompt<T, E4>::THREADS), (E4 ? 2 : 4))
+kv_append_prompt_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RopeTable tb, int shift, int heads) {
+    constexpr int ITEMS = HD / 8, NTH = Prompt<T, E4>::THREADS, KR = Prompt<T, E4>::KR, HC = Prompt<T, E4>::HC;
+    using V = typename Raw<T>::V;
+    __shared__ float red[2][HC][NTH / 32];
+    const bool is_v = blockIdx.x & 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Piece pc = find_piece(a, shift, (int)(blockIdx.x >> 1));
+    report_bad(a);
+    if (!pc.found) return;                                               // fewer pieces than blocks
+    const int pi = pc.row0 >> a.page_shift;                              // page of the sequence
+    const int page = a.table[pc.b * a.table_stride + pi];
+    const int r0 = pc.row0 - (pi << a.page_shift), n_rows = pc.row1 - pc.row0;
+    const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.n_kv_head);
+    const int64_t s_tok = is_v ? a.v_stride : a.k_stride, p_row = is_v ? a.v_row : a.k_row, p_head = is_v ? a.v_head : a.k_head;
+    const T* src = reinterpret_cast<const T*>(is_v ? a.v_new : a.k_new) + pc.tok * s_tok;
+    // (places as in the other kernel)
+    const int c = tid % ITEMS, r = tid / ITEMS;
+    constexpr int RSTEP = NTH / ITEMS;
+    const bool rot = !is_v && c * 4 < tb.half;
+    const int d0 = rot ? c * 4 : c * 8, d1 = rot ? c * 4 + tb.half : c * 8 + 4;
+    int pos[KR];
+#pragma unroll
+    for (int k = 0; k < KR; ++k) pos[k] = rot && r + k * RSTEP < n_rows ? a.pos[pc.tok + r + k * RSTEP] : 0;
+    V raw[HC][KR][2];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < HC; ++j)
+#pragma unroll
+            for (int k = 0; k < KR; ++k)
+                if (h + j < h1 && r + k * RSTEP < n_rows) {
+                    const T* row = src + (r + k * RSTEP) * s_tok + (h + j) * HD;
+                    raw[j][k][0] = *reinterpret_cast<const V*>(row + d0);
+                    raw[j][k][1] = *reinterpret_cast<const V*>(row + d1);
+                }
+    };
+    load(h0);
+    const bool bad_page = page < 0 || page >= a.n_pages;
+    if (bad_page && tid == 0 && a.status) atomicOr(a.status, kStatusInput);
+    if (bad_page) return;
+    float2 cs[KR][4];
+    if (rot)
+#pragma unroll
+        for (int k = 0; k < KR; ++k)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) cs[k][u] = rope_cs_call(pos[k], c * 4 + u, &tb);
+    auto values = [&](int j, int k, float* y) {
+        const float4 p = Raw<T>::floats(raw[j][k][0]), q = Raw<T>::floats(raw[j][k][1]);
+        y[0] = p.x; y[1] = p.y; y[2] = p.z; y[3] = p.w;
+        y[4] = q.x; y[5] = q.y; y[6] = q.z; y[7] = q.w;
+        if (rot)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) rotate(y[u], y[4 + u], cs[k][u]);
+    };
+    const int64_t p_base = page * (is_v ? a.v_page : a.k_page);
+    for (int h = h0; h < h1; h += HC) {
+        if (h > h0) load(h);
+        if (!E4) {
+            __half* dst = reinterpret_cast<__half*>(is_v ? a.v : a.k) + p_base + (r0 + r) * p_row;
+#pragma unroll
+            for (int j = 0; j < HC; ++j)
+                if (h + j < h1 && r < n_rows) {
+                    float y[8];
+                    values(j, 0, y);
+                    __half* at = dst + (h + j) * p_head;
+                    *reinterpret_cast<uint2*>(at + d0) = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
+                    *reinterpret_cast<uint2*>(at + d1) = make_uint2(pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+                }
+            continue;
+        }
+        const int par = (h - h0) / HC & 1;                               // two sets of maxima: one barrier for each HC heads
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < KR; ++k)
+                if (h + j < h1 && r + k * RSTEP < n_rows) {
+                    float y[8];
+                    values(j, k, y);
+                    m = widen(m, y);
+                }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            if (lane == 0) red[par][j][warp] = m;
+        }
+        float old[HC];
+        float* scale = (is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.n_kv_head + h;
+#pragma unroll
+        for (int j = 0; j < HC; ++j) old[j] = r0 > 0 && h + j < h1 ? scale[j] : 0.f;   // a page's first rows start it anew
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            if (h + j >= h1) break;
+            float m = red[par][j][lane & (NTH / 32 - 1)];
+#pragma unroll
+            for (int o = NTH / 64; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            const float s = fmaxf(pow2_scale(m), old[j]), inv = 1.f / s;
+            unsigned char* dst = reinterpret_cast<unsigned char*>(is_v ? a.v : a.k) + p_base + (h + j) * p_head;
+            if (tid == 0) scale[j] = s;
+            if (r0 > 0 && s > old[j]) restore_rows(dst, r0, ITEMS, p_row, old[j] / s);   // the page's earlier rows
+#pragma unroll
+            for (int k = 0; k < KR; ++k)
+                if (r + k * RSTEP < n_rows) {
+                    float y[8];
+                    values(j, k, y);
+                    unsigned char* at = dst + (r0 + r + k * RSTEP) * p_row;
+                    *reinterpret_cast<uint32_t*>(at + d0) = to_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+                    *reinterpret_cast<uint32_t*>(at + d1) = to_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+                }
+        }
+    }
+}
+
+// Programmatic launch: set-up overlaps the kernel before it on the stream.
+template <typename K, typename... A>
+static cudaError_t launch(K kernel, int64_t x, int y, int threads, cudaStream_t st, const A&... args) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)pieces, (unsigned)(two ? (a.n_kv_head + 1) / 2 : a.n_kv_head), 2);
-    cfg.blockDim = dim3(a.n_tok <= 2 * a.n_seq ? 64 : 256);
+    cfg.gridDim = dim3((unsigned)x, (unsigned)y);
+    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return two ? cudaLaunchKernelEx(&cfg, kv_append_paged_kernel<T, HD, E4, 2>, a, tb)
-               : cudaLaunchKernelEx(&cfg, kv_append_paged_kernel<T, HD, E4, 1>, a, tb);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// At most this many pieces of 2^shift rows: one a token, and for each sequence
+// its whole ones and two that its rows fill in part.
+static int64_t most_pieces(const AppendArgs& a, int shift) {
+    const int64_t n = 2 * (int64_t)a.n_seq + (a.n_tok >> shift);
+    return a.n_tok < n ? a.n_tok : n;
+}
+template <typename T, int HD, bool E4>
+static cudaError_t launch_append(const AppendArgs& a, const RopeTable& tb, cudaStream_t st) {
+    // decode: few rows a piece, small blocks
+    if (a.n_tok <= 2 * a.n_seq)
+        return launch(kv_append_paged_kernel<T, HD, E4, 1>, 2 * most_pieces(a, a.page_shift), a.n_kv_head, 64, st, a, tb);
+    using P = Prompt<T, E4>;
+    constexpr int kRows = P::THREADS * P::KR / (HD / 8);                 // rows of a prompt block
+    int shift = a.page_shift;
+    if (!E4)
+        while ((1 << shift) > kRows) --shift;                            // an f16 piece may be a part of a page
+    if ((1 << shift) > kRows || (tb.n_dims & 7))
+        return launch(kv_append_paged_kernel<T, HD, E4, 4>, 2 * most_pieces(a, a.page_shift), a.n_kv_head, 256, st, a, tb);
+    // all heads to a block, or as few as leave kBlocks blocks
+    constexpr int64_t kBlocks = E4 ? 304 : 608;
+    const int64_t n = 2 * most_pieces(a, shift);
+    int64_t heads = n * a.n_kv_head / kBlocks;
+    heads = heads < P::HC ? P::HC : heads;
+    const int groups = (int)((a.n_kv_head + heads - 1) / heads);
+    heads = (a.n_kv_head + groups - 1) / groups;
+    return launch(kv_append_prompt_kernel<T, HD, E4>, n, groups, P::THREADS, st, a, tb, shift, (int)heads);
 }
 template <typename T, int HD>
 static cudaError_t launch_append(const AppendArgs& a, const RopeTable& tb, bool e4, cudaStream_t st) {
