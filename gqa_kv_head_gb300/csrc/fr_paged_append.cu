@@ -64,13 +64,31 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// One copy of the angle's code: inlined for every element, the slow reduction of
-// sincosf alone would outgrow the instruction cache.
-__device__ __noinline__ float2 rope_cs_call(int pos, int i, const RopeTable* tb) {
+// Scaled cosines and sines of a thread's four slots. One copy of the code: inlined
+// for every element, the slow reduction of sincosf alone would outgrow the
+// instruction cache.
+__device__ __noinline__ float2 rope_cs_fixed(int pos, uint64_t turns, float mscale) {
+    float2 r;
+    rope_cs(pos, turns, mscale, r.x, r.y);
+    return r;
+}
+__device__ __noinline__ float2 rope_cs_f32(int pos, int i, const RopeTable* tb) {
     float2 r;
     rope_cs_tab(pos, i, *tb, r.x, r.y);
     return r;
 }
+struct Angles {
+    uint64_t turns[4];                            // of slots 4c .. 4c + 3 (exact mode)
+    // The constants are asked for at once, ahead of everything: read where they
+    // are used they cost a fresh block two trips to memory in a row.
+    __device__ __forceinline__ void get(const RopeTable& tb, int c) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) turns[u] = tb.turns[min(c * 4 + u, kMaxPairs - 1)];
+    }
+    __device__ __forceinline__ float2 at(int pos, int c, int u, const RopeTable& tb) const {
+        return tb.mode == FR_ROPE_GGML_F32 ? rope_cs_f32(pos, c * 4 + u, &tb) : rope_cs_fixed(pos, turns[u], tb.mscale);
+    }
+};
 
 // Four elements of a row as they come, and as floats.
 template <typename T> struct Raw;
@@ -192,6 +210,8 @@ kv_append_paged_kernel(const __grid_constant__ AppendArgs a, const __grid_consta
     using V = typename Raw<T>::V;
     __shared__ float red[8];
     const bool is_v = blockIdx.x & 1;             // neighbours, so that K's arithmetic overlaps V's loads
+    Angles angles;
+    if (!is_v) angles.get(tb, threadIdx.x % ITEMS);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, warps = nthr >> 5;
@@ -242,7 +262,7 @@ kv_append_paged_kernel(const __grid_constant__ AppendArgs a, const __grid_consta
         if (!rot) return;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (c * 4 + u < tb.half) rotate(y[u], y[4 + u], rope_cs_call(a.pos[tok + i], c * 4 + u, &tb));
+            if (c * 4 + u < tb.half) rotate(y[u], y[4 + u], angles.at(a.pos[tok + i], c, u, tb));
     };
     auto store = [&](int i, const float* y, float inv) {
         const int64_t at = p_base + (r0 + i) * p_row;
@@ -351,12 +371,14 @@ struct Prompt {
     static constexpr int HC = (E4 ? 4 : 8) / (sizeof(T) == 4 ? 2 : 1);
 };
 template <typename T, int HD, bool E4>
-__global__ void __launch_bounds__((Prompt<T, E4>::THREADS), (E4 ? 2 : 4))
+__global__ void __launch_bounds__((Prompt<T, E4>::THREADS), (E4 ? 2 : 3))
 kv_append_prompt_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RopeTable tb, int shift, int heads) {
     constexpr int ITEMS = HD / 8, NTH = Prompt<T, E4>::THREADS, KR = Prompt<T, E4>::KR, HC = Prompt<T, E4>::HC;
     using V = typename Raw<T>::V;
     __shared__ float red[2][HC][NTH / 32];
     const bool is_v = blockIdx.x & 1;
+    Angles angles;
+    if (!is_v) angles.get(tb, threadIdx.x % ITEMS);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -398,7 +420,7 @@ kv_append_prompt_kernel(const __grid_constant__ AppendArgs a, const __grid_const
 #pragma unroll
         for (int k = 0; k < KR; ++k)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) cs[k][u] = rope_cs_call(pos[k], c * 4 + u, &tb);
+            for (int u = 0; u < 4; ++u) cs[k][u] = angles.at(pos[k], c, u, tb);
     auto values = [&](int j, int k, float* y) {
         const float4 p = Raw<T>::floats(raw[j][k][0]), q = Raw<T>::floats(raw[j][k][1]);
         y[0] = p.x; y[1] = p.y; y[2] = p.z; y[3] = p.w;
