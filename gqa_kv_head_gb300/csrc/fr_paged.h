@@ -15,13 +15,13 @@ namespace paged {
 constexpr int kTile = 16;            // keys of an MMA step (its M)
 constexpr int kUnit = 64;            // keys of one unit of work at least: a tile for each warp of a CTA
 // Warps of an attention CTA, CTAs per SM and shared memory of each, for nt blocks
-// of 8 query rows. Up to 8 rows at hd <= 128 the accumulators leave room for
+// of 8 query rows. Up to 16 rows at hd <= 128 the accumulators leave room for
 // many warps of small CTAs, which share out many short sequences well; else
 // eight warps are all that the registers hold, and one CTA of them writes half
 // the split states of two. The shares of an SM's shared memory leave room for a
 // few small blocks of the kernel before: where they lie in the way of a CTA, it
 // starts only when another one ends.
-__host__ __device__ constexpr bool many_warps(int hd, int nt) { return nt == 1 && hd <= 128; }
+__host__ __device__ constexpr bool many_warps(int hd, int nt) { return nt <= 2 && hd <= 128; }
 __host__ __device__ constexpr int cta_warps(int hd, int nt) { return many_warps(hd, nt) ? 4 : 8; }
 __host__ __device__ constexpr int ctas_per_sm(int hd, int nt) { return many_warps(hd, nt) ? 3 : 1; }
 __host__ __device__ constexpr int cta_smem(int hd, int nt) { return many_warps(hd, nt) ? 65536 : 212992; }

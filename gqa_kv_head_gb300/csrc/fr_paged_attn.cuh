@@ -90,8 +90,10 @@ struct Cfg {
     static constexpr int W = cta_warps(HD, NT);
     static constexpr int LIMIT = cta_smem(HD, NT);          // shared memory of one CTA
     // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
-    // Q rows lie in shared memory; up to 64 registers of fragments are kept from them for a piece
-    static constexpr bool QREG = HD * NT <= 256;
+    // Q rows lie in shared memory; the fragments stay in registers for a piece
+    // where these allow (hd 128 with 16 rows reads them again for each tile: 63 ->
+    // 59 us at 131072 keys of e4m3, the registers went to a third CTA)
+    static constexpr bool QREG = many_warps(HD, NT) ? HD * NT <= 128 : HD * NT <= 256;
     static constexpr int QPITCH = HD * 2 + 16;              // bytes: rows on different banks
     static constexpr int QBYTES = RT * QPITCH;
     static constexpr int STATE = W * RT * 8;
