@@ -420,6 +420,137 @@ def test_agrees_with_the_contiguous_operators():
     check(a, b.double().cpu(), 2 * tol)
 
 
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("hd,H,G,n", [(256, 1, 8, 300), (128, 2, 4, 200), (64, 1, 16, 130)])
+def test_many_query_rows(kind, hd, H, G, n):
+    """A prompt's rows: many row tiles, each over its own keys."""
+    run_case(kind, hd, H, G, 64, [n, 1, n // 3], [n + 50, 20, n // 3], seed=hd, window=0)
+    run_case(kind, hd, H, G, 16, [n], [n + 7], seed=hd + 1, window=33)
+
+
+def test_more_sequences_than_threads_of_large_blocks():
+    rng = np.random.default_rng(19)
+    kv = [int(x) for x in rng.integers(0, 40, 700)]
+    new = [int(min(a, b)) for a, b in zip(rng.integers(0, 4, 700), kv)]
+    run_case("f16", 256, 1, 8, 16, new, kv, seed=19)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_nothing_else_is_written(kind):
+    """Margins around the output and the workspace, and the cache itself, stay as they were."""
+    hd, H, G, ps = 128, 2, 4, 16
+    kv, new = [300, 7, 1000], [2, 1, 1]
+    n_pages = 90
+    _, cache = make_cache(kind, n_pages, H, ps, hd, 73)
+    before = [t.clone() for t in (cache.k_pages.view(torch.uint8), cache.v_pages.view(torch.uint8))]
+    n = 4 * H * G * hd
+    out = torch.full((n + 4096,), 5.0, device="cuda")
+    size = fr.paged_attn_workspace_size(H * G, H, hd)
+    ws = torch.full((size + 8192,), 171, dtype=torch.uint8, device="cuda")
+    ws[4096:4096 + size] = 0
+    fr.paged_attn(cache, make_batch(new, kv, make_tables(kv, ps, n_pages, 73)), rand_q(4, H * G, hd, 74).cuda(), H * G,
+                  out=out[2048:2048 + n].view(4, H * G, hd), workspace=ws[4096:4096 + size])
+    torch.cuda.synchronize()
+    assert (out[:2048] == 5.0).all() and (out[2048 + n:] == 5.0).all()
+    assert (ws[:4096] == 171).all() and (ws[4096 + size:] == 171).all()
+    assert torch.equal(cache.k_pages.view(torch.uint8), before[0]) and torch.equal(cache.v_pages.view(torch.uint8), before[1])
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured with one workspace and replayed in turn on one stream."""
+    hd, H, G, ps, n_pages = 128, 2, 8, 64, 60
+    (k, _, v, _), cache = make_cache("f16", n_pages, H, ps, hd, 79)
+    ws = fr.make_paged_workspace(H * G, H, hd)
+    cases = []
+    for i, (new, kv) in enumerate((([1], [3500]), ([2, 1, 1], [100, 900, 40]))):
+        table = make_tables(kv, ps, n_pages, 80 + i)
+        q = rand_q(sum(new), H * G, hd, 82 + i)
+        want, tol = ref.attention(q, k.double(), v.double(), starts(new), kv, table, H * G)
+        qd, batch = q.cuda(), make_batch(new, kv, table)
+        out = fr.paged_attn(cache, batch, qd, H * G, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fr.paged_attn(cache, batch, qd, H * G, out=out, workspace=ws)
+        cases.append((graph, out, want, tol, qd, batch))
+    for _ in range(3):
+        for graph, out, *_ in cases:
+            out.fill_(float("nan"))
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, want, tol, *_ in cases:
+        check(out, want, tol)
+
+
+def test_refusals():
+    """What the calls refuse, before anything is launched."""
+    hd, H, G, ps = 128, 2, 4, 16
+    _, cache = make_cache("f16", 4, H, ps, hd)
+    _, cache8 = make_cache("e4m3", 4, H, ps, hd)
+    table = make_tables([20, 20], ps, 4)
+    batch = make_batch([1, 1], [20, 20], table)
+    q = rand_q(2, H * G, hd).cuda()
+    ws = fr.make_paged_workspace(H * G, H, hd)
+
+    def status(f, want):
+        with pytest.raises(fr.FrError) as e:
+            f()
+        assert e.value.status == want
+    for bad in (dict(window=-1), dict(window=4, causal=False), dict(kq_scale=float("nan")), dict(kq_scale=float("inf"))):
+        status(lambda: fr.paged_attn(cache, batch, q, H * G, workspace=ws, **bad), 1)
+    status(lambda: fr.paged_attn(cache, batch, q, H * G, workspace=ws[:1024]), 3)
+    status(lambda: fr.paged_attn(cache, batch, q[:, :7].contiguous(), 7, workspace=ws), 1)       # 7 heads on 2
+    for bad in (q.float(), q.bfloat16()):
+        with pytest.raises(TypeError):
+            fr.paged_attn(cache, batch, bad, H * G)
+    for bad in (q[..., :64], q.transpose(0, 1), q.view(2, -1)[:, :-8]):
+        with pytest.raises(ValueError):
+            fr.paged_attn(cache, batch, bad, H * G)
+    with pytest.raises(ValueError):
+        fr.paged_attn(cache, batch, q, H * G, out=torch.empty((2, H * G, hd + 1), device="cuda"))
+    with pytest.raises(ValueError):
+        fr.paged_attn(cache, batch, q, H * G, out=torch.empty((2, H * G, hd), dtype=torch.float16, device="cuda"))
+    wide = torch.zeros(2, H * G * hd + 4, dtype=torch.float16, device="cuda")[:, :H * G * hd].unflatten(1, (H * G, hd))
+    status(lambda: fr.paged_attn(cache, batch, wide, H * G, workspace=ws), 1)                    # token stride of 8 bytes more
+
+    rows = torch.zeros((2, H, hd), device="cuda")
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    rope = fr.rope_params(hd)
+    fr.kv_append_paged(cache8, batch, rows, rows, pos, rope)
+    for bad in (fr.rope_params(127), fr.rope_params(256), fr.rope_params(128, freq_base=-1.0)):
+        status(lambda: fr.kv_append_paged(cache, batch, rows, rows, pos, bad), 1)
+    for a, b in ((rows.half(), rows), (rows.double(), rows.double()), (rows.bfloat16(), rows.bfloat16())):
+        with pytest.raises(TypeError):
+            fr.kv_append_paged(cache, batch, a, b, pos, rope)
+    with pytest.raises(TypeError):
+        fr.kv_append_paged(cache, batch, rows, rows, pos.long(), rope)
+    for a, p in ((rows[:, :1], pos), (rows[..., :64], pos), (rows, pos[:1]), (rows.transpose(0, 1), pos)):
+        with pytest.raises(ValueError):
+            fr.kv_append_paged(cache, batch, a, a, p, rope)
+    k = cache.k_pages
+    with pytest.raises(TypeError):
+        fr.PagedKV(k.float(), k.float())
+    with pytest.raises(TypeError):
+        fr.PagedKV(k, cache8.k_pages)
+    with pytest.raises(ValueError):
+        fr.PagedKV(k, k[:2])
+    with pytest.raises(ValueError):
+        fr.PagedKV(k, k, cache8.k_scale, cache8.v_scale)
+    with pytest.raises(ValueError):
+        fr.PagedKV(cache8.k_pages, cache8.v_pages)
+    with pytest.raises(ValueError):
+        fr.PagedKV(cache8.k_pages, cache8.v_pages, cache8.k_scale[:2], cache8.v_scale)
+    status(lambda: fr.PagedKV(k[:, :, :12], k[:, :, :12]), 2)
+    status(lambda: fr.PagedKV(k[:1].expand(4, -1, -1, -1), k), 1)                                # one page four times
+    with pytest.raises(TypeError):
+        fr.PagedBatch(batch.tok_start.long(), batch.kv_len, batch.page_table)
+    with pytest.raises(ValueError):
+        fr.PagedBatch(batch.tok_start[:2], batch.kv_len, batch.page_table)
+    with pytest.raises(ValueError):
+        fr.PagedBatch(batch.tok_start, batch.kv_len, batch.page_table.t().contiguous().t())
+    torch.cuda.synchronize()
+
+
 # ---- append -----------------------------------------------------------------
 
 def rotated_rows(k_new, pos, rope):
