@@ -165,16 +165,56 @@ __device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
     }
     seg_keys<RT, KT, W>(s, a);
 }
-// Units of all segments of sequence b for one KV head.
+// Units of all segments of one KV head of each lane's sequence (0 without rows).
+// Called by whole warps: a sequence of many row tiles is counted by all lanes.
+constexpr int kSerialTiles = 4;
 template <int RT, int KT, int W>
-__device__ __forceinline__ int seq_units(const AttnArgs& a, int b, Seg& s, bool& bad) {
-    bad = seg_seq<RT>(s, a, b);
+__device__ __forceinline__ int seq_units(const AttnArgs& a, const Seg& s) {
     int u = 0;
-    for (s.rt = 0; s.rt < s.n_rt; ++s.rt) {
-        seg_keys<RT, KT, W>(s, a);
-        u += s.n_units;
+    Seg x = s;
+    if (s.n_rt <= kSerialTiles)
+        for (x.rt = 0; x.rt < s.n_rt; ++x.rt) {
+            seg_keys<RT, KT, W>(x, a);
+            u += x.n_units;
+        }
+    for (unsigned big = __ballot_sync(~0u, s.n_rt > kSerialTiles); big; big &= big - 1) {
+        const int from = __ffs(big) - 1, lane = threadIdx.x & 31;
+        x.n_q = __shfl_sync(~0u, s.n_q, from);
+        x.n_kv = __shfl_sync(~0u, s.n_kv, from);
+        x.n_rt = __shfl_sync(~0u, s.n_rt, from);
+        int sum = 0;
+        for (x.rt = lane; x.rt < x.n_rt; x.rt += 32) {
+            seg_keys<RT, KT, W>(x, a);
+            sum += x.n_units;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == from) u = sum;
     }
     return u;
+}
+// Called by a whole warp with one sequence's numbers: the row tile that holds unit
+// rem of its list, and rem within it.
+template <int RT, int KT, int W>
+__device__ __noinline__ int2 find_row_tile(Seg x, int rem, const AttnArgs* a) {
+    const int lane = threadIdx.x & 31;
+    for (int rt0 = 0;; rt0 += 32) {
+        x.rt = rt0 + lane;
+        if (x.rt < x.n_rt) seg_keys<RT, KT, W>(x, *a);
+        const int own = x.rt < x.n_rt ? x.n_units : 0;
+        int inc = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(~0u, rem < inc);
+        if (hit || rt0 + 32 >= x.n_rt) {
+            const int at = hit ? __ffs(hit) - 1 : 0;
+            return make_int2(rt0 + at, rem - __shfl_sync(~0u, inc - own, at));
+        }
+        rem -= __shfl_sync(~0u, inc, 31);
+    }
 }
 
 // A walk over a CTA's share of the units: the piece of a segment it is at. In
@@ -266,16 +306,16 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     int u_b = 0, s_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind
     {
         bool bad_any = false;
-        if (tid < a.n_seq) {
-            u_b = seq_units<RT, KT, W>(a, tid, seq, bad_any) * a.n_kv_head;
-            s_b = seq.n_rt * a.n_kv_head;
-        }
-        for (int b = tid + NTH; b < a.n_seq; b += NTH) {
+        seq.n_rt = 0;
+        if (tid < a.n_seq) bad_any = seg_seq<RT>(seq, a, tid);
+        u_b = seq_units<RT, KT, W>(a, seq) * a.n_kv_head;
+        s_b = seq.n_rt * a.n_kv_head;
+        for (int b0 = NTH; b0 < a.n_seq; b0 += NTH) {
             Seg s;
-            bool bad;
-            more_u += seq_units<RT, KT, W>(a, b, s, bad) * a.n_kv_head;
+            s.n_rt = 0;
+            if (b0 + tid < a.n_seq) bad_any |= seg_seq<RT>(s, a, b0 + tid);
+            more_u += seq_units<RT, KT, W>(a, s) * a.n_kv_head;
             more_s += s.n_rt * a.n_kv_head;
-            bad_any |= bad;
         }
         if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
     }
@@ -326,14 +366,30 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     {
         int b = tid;
         for (;;) {
-            if (u_b > 0 && u0 >= inc - u_b && u0 < inc) {      // one thread of the block: the share starts in its sequence
-                Walk w;
-                int rem = u0 - (inc - u_b);
+            const bool hit = u_b > 0 && u0 >= inc - u_b && u0 < inc;   // one thread of the block: the share starts in its sequence
+            int rem = u0 - (inc - u_b), head = 0, tile = 0;
+            if (hit) {
                 const int per_head = u_b / a.n_kv_head;
+                head = a.n_kv_head == 1 ? 0 : rem / per_head;
+                rem -= head * per_head;
+            }
+            if (const unsigned many = __ballot_sync(~0u, hit && seq.n_rt > kSerialTiles)) {
+                const int from = __ffs(many) - 1;
+                Seg x;
+                x.n_q = __shfl_sync(~0u, seq.n_q, from);
+                x.n_kv = __shfl_sync(~0u, seq.n_kv, from);
+                x.n_rt = __shfl_sync(~0u, seq.n_rt, from);
+                const int2 at = find_row_tile<RT, KT, W>(x, __shfl_sync(~0u, rem, from), &a);
+                if (lane == from) {
+                    tile = at.x;
+                    rem = at.y;
+                }
+            }
+            if (hit) {
+                Walk w;
                 w.s = seq;
-                w.s.h = a.n_kv_head == 1 ? 0 : rem / per_head;
-                rem -= w.s.h * per_head;
-                for (w.s.rt = 0;; ++w.s.rt) {
+                w.s.h = head;
+                for (w.s.rt = tile;; ++w.s.rt) {
                     seg_keys<RT, KT, W>(w.s, a);
                     if (rem < w.s.n_units || w.s.rt + 1 >= w.s.n_rt) break;
                     rem -= w.s.n_units;
@@ -348,9 +404,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             if (u0 < base_u || b - tid >= a.n_seq) break;
             // the next W * 32 sequences
             b += NTH;
-            bool bad;
             seq.n_rt = 0;
-            u_b = b < a.n_seq ? seq_units<RT, KT, W>(a, b, seq, bad) * a.n_kv_head : 0;
+            if (b < a.n_seq) seg_seq<RT>(seq, a, b);
+            u_b = seq_units<RT, KT, W>(a, seq) * a.n_kv_head;
             s_b = seq.n_rt * a.n_kv_head;
             inc = u_b;
             inc_s = s_b;
