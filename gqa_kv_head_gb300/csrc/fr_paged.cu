@@ -17,17 +17,17 @@ using sm100::ex2;
 // The states (m, l, O) of one split segment's row become its output row:
 //   out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p,  M = max_p m_p,
 // in the order of the pieces, whatever order they were computed in. One block
-// per (segment, row, 64 dims): thread = (4 dims, group of states). Bound by
+// per (segment, row, 4 * cols dims): thread = (4 dims, group of states). Bound by
 // latency, and by how slowly one SM reads lines that others have just written,
 // so a row is spread over blocks and the first kAhead states of each group are
 // asked for before the weights are known. Blocks of unsplit segments leave at
 // once.
-constexpr int kAhead = 4, kMergeCols = 16, kMergeThreads = 512;
+constexpr int kAhead = 4, kMergeThreads = 512;
 
 __global__ void __launch_bounds__(kMergeThreads)
 paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_split, const float* __restrict__ part_o,
                    const float2* __restrict__ part_ml, float* __restrict__ out, int row_tile, int hd, int group,
-                   int n_kv_head) {
+                   int n_kv_head, int cols) {
     __shared__ float red_l[kMergeThreads / 32], red_m[kMergeThreads / 32];
     extern __shared__ float4 red[];                 // [threads], then the states' weights
     float* wt = reinterpret_cast<float*>(red + blockDim.x);
@@ -38,7 +38,7 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
     const int2 s1 = __ldcg(reinterpret_cast<const int2*>(split + blockIdx.x) + 2);
     const int first = s0.x, n = s0.y - first + 1, tok0 = s0.z, row0 = s0.w, rows = s1.x, head = s1.y;
     if ((int)blockIdx.x >= n_entries || n < 1) return;
-    const int groups = blockDim.x / kMergeCols, c = blockIdx.z * kMergeCols + tid % kMergeCols, gi = tid / kMergeCols;
+    const int groups = blockDim.x / cols, c = blockIdx.z * cols + tid % cols, gi = tid / cols;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
         auto slot = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * row_tile + row; };
         float4 ahead[kAhead];
@@ -88,7 +88,7 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
             l = 0.f;
             for (int w = 0; w < warps; ++w) l += red_l[w];
             for (int i = 1; i < groups; ++i) {
-                const float4 y = red[i * kMergeCols + tid];
+                const float4 y = red[i * cols + tid];
                 x.x += y.x;
                 x.y += y.y;
                 x.z += y.z;
@@ -329,6 +329,8 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     a.page_shift = kv->page_shift;
     a.n_kv_head = kv->n_kv_head;
     a.group = G;
+    // r * ceil(2^32 / G) / 2^32 = r / G + r e / (2^32 G) with e < G: exact below r e < 2^32
+    if (G > 1 && (int64_t)bt->n_tok * G * G < (int64_t{1} << 32)) a.group_magic = (unsigned)(((uint64_t{1} << 32) + G - 1) / G);
     a.causal = causal ? 1 : 0;
     a.window = window;
     a.split_by_segment = segs <= ctas ? 1 : 0;
@@ -341,11 +343,14 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
                                             : (avg < rt ? avg : rt);      // (a block goes on to the rows behind)
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)(a.split_by_segment ? segs : ctas), (unsigned)rows, (unsigned)(kv->hd / (4 * kMergeCols)));
     // threads for the states that a segment has when all are as long: kAhead for each group
     const int64_t usual = bt->n_tok < bt->n_seq ? bt->n_tok : bt->n_seq * ((avg + rt - 1) / rt);
     const int64_t groups = (ctas / (usual * kv->n_kv_head) + 2 + kAhead - 1) / kAhead;
-    int64_t threads = (groups * kMergeCols + 31) / 32 * 32;
+    const int64_t entries = a.split_by_segment ? segs : ctas;
+    // few rows in all: 64 dims to a block, so that more SMs read the fresh states; many: fewer blocks
+    const int cols = kv->hd > 64 && entries * rows > 608 ? 32 : 16;
+    int64_t threads = (groups * cols + 31) / 32 * 32;
+    cfg.gridDim = dim3((unsigned)entries, (unsigned)rows, (unsigned)(kv->hd / (4 * cols)));
     cfg.blockDim = dim3((unsigned)(threads > kMergeThreads ? kMergeThreads : threads));
     cfg.dynamicSmemBytes = cfg.blockDim.x * sizeof(float4) + kMaxCtas * sizeof(float);
     cfg.stream = stream;
@@ -356,6 +361,6 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_merge_kernel, (const Split*)a.split, (const int*)a.n_split,
                                              (const float*)a.part_o, (const float2*)a.part_ml, out, rt, kv->hd, G,
-                                             kv->n_kv_head);
+                                             kv->n_kv_head, cols);
     return e == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }

@@ -115,6 +115,11 @@ struct Cfg {
     static_assert(CNT >= 1 && NT % CNT == 0, "epilogue chunk");
 };
 
+// Row r's token: r / group, by a multiplication where the host found it exact.
+__device__ __forceinline__ int token_of(int r, const AttnArgs& a) {
+    return a.group_magic ? (int)__umulhi((unsigned)r, a.group_magic) : r / a.group;
+}
+
 // One (sequence, KV head, row tile): its rows, and its keys as 16-key tiles.
 struct Seg {
     int b, h, rt, n_rt;
@@ -127,8 +132,8 @@ __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
     int hi = s.n_kv, lo = 0;
     if (a.causal) {
         // the tile's first and last token; one row tile holds all of most sequences
-        const int i0 = s.rt == 0 ? 0 : s.rt * RT / a.group;
-        const int i1 = s.rt == s.n_rt - 1 ? s.n_q - 1 : (s.rt * RT + RT - 1) / a.group;
+        const int i0 = s.rt == 0 ? 0 : token_of(s.rt * RT, a);
+        const int i1 = s.rt == s.n_rt - 1 ? s.n_q - 1 : token_of(s.rt * RT + RT - 1, a);
         const int first = s.n_kv - s.n_q;
         hi = min(hi, first + i1 + 1);
         if (a.window > 0) lo = max(0, first + i0 - a.window + 1);
@@ -303,12 +308,13 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     constexpr int NTH = W * 32;
     const int cta = blockIdx.x;
     Seg seq;
-    int u_b = 0, s_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind
+    int per_head = 0, u_b = 0, s_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind
     {
         bool bad_any = false;
         seq.n_rt = 0;
         if (tid < a.n_seq) bad_any = seg_seq<RT>(seq, a, tid);
-        u_b = seq_units<RT, KT, W>(a, seq) * a.n_kv_head;
+        per_head = seq_units<RT, KT, W>(a, seq);
+        u_b = per_head * a.n_kv_head;
         s_b = seq.n_rt * a.n_kv_head;
         for (int b0 = NTH; b0 < a.n_seq; b0 += NTH) {
             Seg s;
@@ -369,7 +375,6 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             const bool hit = u_b > 0 && u0 >= inc - u_b && u0 < inc;   // one thread of the block: the share starts in its sequence
             int rem = u0 - (inc - u_b), head = 0, tile = 0;
             if (hit) {
-                const int per_head = u_b / a.n_kv_head;
                 head = a.n_kv_head == 1 ? 0 : rem / per_head;
                 rem -= head * per_head;
             }
@@ -406,7 +411,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             b += NTH;
             seq.n_rt = 0;
             if (b < a.n_seq) seg_seq<RT>(seq, a, b);
-            u_b = seq_units<RT, KT, W>(a, seq) * a.n_kv_head;
+            per_head = seq_units<RT, KT, W>(a, seq);
+            u_b = per_head * a.n_kv_head;
             s_b = seq.n_rt * a.n_kv_head;
             inc = u_b;
             inc_s = s_b;
@@ -440,7 +446,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         if (tid < RT) {
             int hi = w.s.n_kv, lo = 0;
             if (a.causal) {
-                const int p = w.s.n_kv - w.s.n_q + (row0 + min(tid, rows - 1)) / a.group;
+                const int p = w.s.n_kv - w.s.n_q + token_of(row0 + min(tid, rows - 1), a);
                 hi = min(hi, p + 1);
                 if (a.window > 0) lo = max(0, p + 1 - a.window);
             }
@@ -451,7 +457,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         for (int k = 0; k < QN; ++k) {
             const int r = (k * W * 32 + tid) / (HD / 8), c = tid % (HD / 8);
             if (r >= RT) break;
-            const int i = (row0 + min(r, rows - 1)) / a.group, hh = row0 + min(r, rows - 1) - i * a.group;
+            const int i = token_of(row0 + min(r, rows - 1), a), hh = row0 + min(r, rows - 1) - i * a.group;
             const __half* src = a.q16 + (int64_t)(w.s.tok0 + i) * a.q_stride + (int64_t)(w.s.h * a.group + hh) * HD + c * 8;
             // rows behind the last are zeros
             if (E4)
@@ -994,7 +1000,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                     x.y *= inv;
                     x.z *= inv;
                     x.w *= inv;
-                    const int i = (row0 + r) / a.group, hh = (row0 + r) - i * a.group;
+                    const int i = token_of(row0 + r, a), hh = (row0 + r) - i * a.group;
                     float* dst = a.out + ((int64_t)(tok0 + i) * a.n_kv_head * a.group + head0 + hh) * HD;
                     *reinterpret_cast<float4*>(dst + d) = x;
                 } else {
