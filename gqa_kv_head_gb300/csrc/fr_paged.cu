@@ -142,6 +142,7 @@ static bool strides_ok(const int64_t* st, int n_pages, int n_head, int page_size
     for (int i = 0; i < 3; ++i) {
         if (d[i].n == 1) continue;
         if (d[i].stride < extent) return false;
+        if (d[i].stride > (int64_t{1} << 62) / d[i].n - extent / d[i].n - 1) return false;   // (no memory is that large)
         extent += d[i].stride * (d[i].n - 1);
     }
     return true;
@@ -206,7 +207,7 @@ extern "C" fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const 
     if (n_kv_head > 65535) return FR_ERR_UNSUPPORTED;
     const bool e4 = type == FR_KV_E4M3;
     if (e4 ? !k_scale || !v_scale : k_scale || v_scale) return FR_ERR_INVALID_ARG;
-    if (!aligned16(k) || !aligned16(v)) return FR_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3)) return FR_ERR_INVALID_ARG;
     const int elem = e4 ? 1 : 2;
     if (!strides_ok(k_strides, n_pages, n_kv_head, page_size, hd, elem) ||
         !strides_ok(v_strides, n_pages, n_kv_head, page_size, hd, elem))
@@ -280,7 +281,8 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     if (n_head < 1 || n_head % kv->n_kv_head) return FR_ERR_INVALID_ARG;
     if (n_head > (1 << 16)) return FR_ERR_UNSUPPORTED;
     if (q_tok_stride < (int64_t)n_head * kv->hd || (q_tok_stride & 7)) return FR_ERR_INVALID_ARG;
-    if (window < 0 || (window > 0 && !causal) || !isfinite(kq_scale)) return FR_ERR_INVALID_ARG;
+    const float scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
+    if (window < 0 || (window > 0 && !causal) || !isfinite(scale_log2)) return FR_ERR_INVALID_ARG;
     if (!aligned16(q16) || !aligned16(out) || !aligned16(workspace)) return FR_ERR_INVALID_ARG;
     if (((int64_t)bt->max_pages << kv->page_shift) > 0x7fff0000) return FR_ERR_UNSUPPORTED;
     if (workspace_bytes < ws_bytes(kv->hd)) return FR_ERR_WORKSPACE;
@@ -332,9 +334,10 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     // r * ceil(2^32 / G) / 2^32 = r / G + r e / (2^32 G) with e < G: exact below r e < 2^32
     if (G > 1 && (int64_t)bt->n_tok * G * G < (int64_t{1} << 32)) a.group_magic = (unsigned)(((uint64_t{1} << 32) + G - 1) / G);
     a.causal = causal ? 1 : 0;
-    a.window = window;
+    // a window that no sequence outgrows is none (and positions less it stay in 32 bits)
+    a.window = window >= ((int64_t)bt->max_pages << kv->page_shift) ? 0 : window;
     a.split_by_segment = segs <= ctas ? 1 : 0;
-    a.scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     const fr_status st = kv->type == FR_KV_E4M3 ? launch_attn_e4m3(*kv, a, nt, (int)ctas, stream)
                                                 : launch_attn_f16(*kv, a, nt, (int)ctas, stream);
     if (st != FR_OK) return st;

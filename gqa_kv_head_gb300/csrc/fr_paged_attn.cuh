@@ -125,6 +125,7 @@ struct Seg {
     int b, h, rt, n_rt;
     int tok0, n_q, n_kv;
     int tile0, n_tiles, n_units;
+    int lo;             // first key in some row's view
 };
 
 template <int RT, int KT, int W>
@@ -138,6 +139,7 @@ __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
         hi = min(hi, first + i1 + 1);
         if (a.window > 0) lo = max(0, first + i0 - a.window + 1);
     }
+    s.lo = lo;
     s.tile0 = lo / KT;
     s.n_tiles = hi > lo ? (hi + KT - 1) / KT - s.tile0 : 0;
     // a segment's start and end cost a CTA as much as about two units of its
@@ -231,7 +233,6 @@ struct Walk {
     int ua, ub;         // this piece's units within the segment
     int more;           // 0: the share has ended
     int seg_no;         // the segment's number in the whole list
-    int pad;
 };
 static_assert(sizeof(Walk) == 64, "walk");
 template <int W>
@@ -502,7 +503,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     auto load_pages = [&]() {
         blk = 0;
         const int tl = pt.x + lane / SUB * W, key = (pw->s.tile0 + tl) * KT + lane % SUB * kTile;
-        b_has = tl < pt.y && key < pw->s.n_kv;
+        // (16 keys that no row sees: their page may be gone)
+        b_has = tl < pt.y && key < pw->s.n_kv && key + kTile > pw->s.lo;
         b_page = -1;
         if (b_has) b_page = __ldcg(a.table + pw->s.b * a.table_stride + (key >> a.page_shift));
         fresh = true;

@@ -384,7 +384,8 @@ fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const int64_t* k_
  *   kv_len      int32 [n_seq]: keys of sequence b, its new tokens included.
  *   page_table  int32 [n_seq][max_pages], row stride page_table_stride: page
  *               of the sequence's rows i*page_size .. Entries behind the
- *               sequence's last page are not read.
+ *               sequence's last page are not read, nor used where a window
+ *               leaves a page out of every row's view.
  * Sequences may share pages that no call writes. The arrays are read on the
  * device by every call. A sequence whose numbers do not fit (tokens outside
  * 0..n_tok, kv_len outside 0..max_pages*page_size, or fewer keys than new

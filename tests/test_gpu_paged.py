@@ -104,7 +104,7 @@ def test_attention_page_sizes_and_layouts(kind, ps, nhd):
 
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("kw", [dict(causal=False), dict(window=1), dict(window=5), dict(window=16), dict(window=100),
-                                dict(window=100000), dict(kq_scale=0.37), dict(causal=False, kq_scale=-2.0)],
+                                dict(window=100000), dict(window=2 ** 31 - 1), dict(kq_scale=0.37), dict(causal=False, kq_scale=-2.0)],
                          ids=lambda k: "_".join(f"{a}{b}" for a, b in k.items()))
 @pytest.mark.parametrize("n", [1, 4])
 def test_attention_masks(kind, kw, n):
@@ -117,6 +117,8 @@ def test_uneven_tokens_and_empty_sequences(kind):
     (their first rows see nothing and are 0), and one token beside forty."""
     new = [0, 3, 1, 0, 40, 2, 1, 5]
     kv = [0, 3, 0, 50, 75, 1, 200, 2]
+    run_case(kind, 128, 2, 4, 16, new, kv, seed=6, window=2 ** 31 - 1)
+    run_case(kind, 128, 2, 4, 16, new, kv, seed=7, window=3)
     out = run_case(kind, 128, 2, 4, 16, new, kv, seed=5)
     s = starts(new)
     assert not out[s[2]].any()                       # no keys
@@ -251,6 +253,28 @@ def test_e4m3_scales_of_any_size():
     check(out, want, tol)
     zero = fr.PagedKV(k.cuda(), v.cuda(), ks.cuda(), torch.zeros_like(vs).cuda())
     assert not fr.paged_attn(zero, make_batch([1, 1], kv, table), q.cuda(), H * G).any()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("ps,n,window", [(16, 1, 40), (16, 3, 16), (32, 2, 50), (64, 1, 1)])
+def test_pages_behind_the_window_may_be_gone(kind, ps, n, window):
+    """Table entries of pages that no row sees are not used: nothing is
+    reported, and what other sequences keep in such pages does not matter."""
+    hd, H, G = 128, 2, 4
+    kv = [1000, 77, 16, 300 + n]
+    n_pages = sum(-(-x // ps) for x in kv) + 2
+    (k, ks, v, vs), cache = make_cache(kind, n_pages, H, ps, hd, 83)
+    table = make_tables(kv, ps, n_pages, 83)
+    q = rand_q(n * len(kv), H * G, hd, 84)
+    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts([n] * len(kv)), kv, table, H * G, window=window)
+    gone = table.clone()
+    for b, x in enumerate(kv):
+        first = max(0, x - n + 1 - window)
+        gone[b, :first // ps] = torch.tensor([-1, n_pages, 2 ** 31 - 1], dtype=torch.int32)[torch.arange(first // ps) % 3]
+    ws = fr.make_paged_workspace(H * G, H, hd)
+    out = fr.paged_attn(cache, make_batch([n] * len(kv), kv, gone), q.cuda(), H * G, window=window, workspace=ws)
+    check(out, want, tol)
+    fr.workspace_check(ws)
 
 
 @pytest.mark.parametrize("kind", TYPES)
@@ -496,7 +520,8 @@ def test_refusals():
         with pytest.raises(fr.FrError) as e:
             f()
         assert e.value.status == want
-    for bad in (dict(window=-1), dict(window=4, causal=False), dict(kq_scale=float("nan")), dict(kq_scale=float("inf"))):
+    for bad in (dict(window=-1), dict(window=4, causal=False), dict(kq_scale=float("nan")), dict(kq_scale=float("inf")),
+                dict(kq_scale=3e38)):
         status(lambda: fr.paged_attn(cache, batch, q, H * G, workspace=ws, **bad), 1)
     status(lambda: fr.paged_attn(cache, batch, q, H * G, workspace=ws[:1024]), 3)
     status(lambda: fr.paged_attn(cache, batch, q[:, :7].contiguous(), 7, workspace=ws), 1)       # 7 heads on 2

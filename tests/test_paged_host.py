@@ -48,6 +48,7 @@ def test_cache_descriptor_refusals(lib):
     assert _kv(lib, ks=FAKE) == 1 and _kv(lib, vs=FAKE) == 1
     assert _kv(lib, type=1) == 1 and _kv(lib, type=1, ks=FAKE) == 1
     assert _kv(lib, type=1, ks=FAKE, vs=FAKE) in OK_BUT_NO_GPU
+    assert _kv(lib, type=1, ks=FAKE + 2, vs=FAKE) == 1 and _kv(lib, type=1, ks=FAKE, vs=FAKE + 1) == 1
 
 
 def test_cache_strides(lib):
@@ -62,6 +63,8 @@ def test_cache_strides(lib):
     assert _kv(lib, k_st=(0, 64 * 128, 128)) == 1
     assert _kv(lib, k_st=(2 * 64 * 128, 0, 128)) == 1
     assert _kv(lib, k_st=(-2 * 64 * 128, 64 * 128, 128)) == 1
+    # more than any memory
+    assert _kv(lib, n_pages=2 ** 31 - 1, k_st=(1 << 38, 64 * 128, 128)) == 1
     # not multiples of 16 bytes
     assert _kv(lib, k_st=(2 * 64 * 132, 64 * 132, 132)) == 1
     assert _kv(lib, type=1, ks=FAKE, vs=FAKE, k_st=(2 * 64 * 136, 64 * 136, 136)) == 1
