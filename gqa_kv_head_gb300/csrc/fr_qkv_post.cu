@@ -93,7 +93,7 @@ bool build_rope_table(const fr_rope_params* rp, float q_scale, int hd, RopeTable
         }
         double f = w / two_pi;
         f -= floor(f);                                           // turns per step, mod 1
-        const double scaled = ldexp(f, 64);
+        const double scaled = f * 18446744073709551616.0;       // 2^64: exact
         t->turns[i] = scaled >= 18446744073709551616.0 ? 0ull : (uint64_t)scaled;
         w_base *= step;
     }

@@ -144,7 +144,10 @@ def kv_append_paged(cache, batch, k_new, v_new, pos, rope, workspace=None, strea
     if pos.dtype != torch.int32:
         raise TypeError("pos must be int32")
     n_tok, k_stride = _rows(k_new, "k_new", cache)
-    n_v, v_stride = _rows(v_new, "v_new", cache)
+    if v_new.shape == k_new.shape and v_new.stride() == k_new.stride():
+        n_v, v_stride = n_tok, k_stride
+    else:
+        n_v, v_stride = _rows(v_new, "v_new", cache)
     if n_v != n_tok or pos.shape != (n_tok,) or not pos.is_contiguous():
         raise ValueError("k_new, v_new and pos must have one row a token")
     rope = _as_rope(rope)

@@ -441,6 +441,8 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  *               (fr_workspace_init); one for each concurrently running call
  * Made for few query rows a sequence (decode, speculative tokens): each 32 rows
  * (16 at hd 256) of a sequence's KV head read its keys once.
+ * A weight enters the PV product within 2^-22 of itself, or 2^-32 of its row's
+ * largest (e4m3: each times its V scale, against the largest V scale in view).
  * The result does not depend on timing: same inputs, same bits.
  */
 fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
