@@ -34,8 +34,7 @@
 #include <cuda_fp16.h>
 #include <string.h>
 
-#include "fr_paged.h"
-#include "fr_sm100.cuh"
+#include "fr_paged_work.cuh"
 
 namespace fr {
 namespace paged {
@@ -115,157 +114,6 @@ struct Cfg {
     static_assert(CNT >= 1 && NT % CNT == 0, "epilogue chunk");
 };
 
-// Row r's token: r / group, by a multiplication where the host found it exact.
-__device__ __forceinline__ int token_of(int r, const AttnArgs& a) {
-    return a.group_magic ? (int)__umulhi((unsigned)r, a.group_magic) : r / a.group;
-}
-
-// One (sequence, KV head, row tile): its rows, and its keys as 16-key tiles.
-struct Seg {
-    int b, h, rt, n_rt;
-    int tok0, n_q, n_kv;
-    int tile0, n_tiles, n_units;
-    int lo;             // first key in some row's view
-};
-
-template <int RT, int KT, int W>
-__device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
-    int hi = s.n_kv, lo = 0;
-    if (a.causal) {
-        // the tile's first and last token; one row tile holds all of most sequences
-        const int i0 = s.rt == 0 ? 0 : token_of(s.rt * RT, a);
-        const int i1 = s.rt == s.n_rt - 1 ? s.n_q - 1 : token_of(s.rt * RT + RT - 1, a);
-        const int first = s.n_kv - s.n_q;
-        hi = min(hi, first + i1 + 1);
-        if (a.window > 0) lo = max(0, first + i0 - a.window + 1);
-    }
-    s.lo = lo;
-    s.tile0 = lo / KT;
-    s.n_tiles = hi > lo ? (hi + KT - 1) / KT - s.tile0 : 0;
-    // a segment's start and end cost a CTA as much as about two units of its
-    // keys: it counts those ahead of them (rows without keys still get their zeros)
-    s.n_units = kSegCost + (s.n_tiles + W - 1) / W;
-}
-template <int RT>
-__device__ __forceinline__ bool seg_seq(Seg& s, const AttnArgs& a, int b) {
-    const SeqInfo q = seq_info(a.tok_start, a.kv_len, b, a.n_tok, a.max_pages, a.page_shift);
-    s.b = b;
-    s.tok0 = q.tok0;
-    s.n_q = q.n_q;
-    s.n_kv = q.n_kv;
-    s.n_rt = (q.n_q * a.group + RT - 1) / RT;
-    return q.bad;
-}
-// The next segment in order (row tile fastest, then KV head, then sequence).
-template <int RT, int KT, int W>
-__device__ __forceinline__ void seg_next(Seg& s, const AttnArgs& a) {
-    if (++s.rt == s.n_rt) {
-        s.rt = 0;
-        if (++s.h == a.n_kv_head) {
-            s.h = 0;
-            int b = s.b;
-            do {
-                if (++b >= a.n_seq) return;
-                seg_seq<RT>(s, a, b);
-            } while (s.n_rt == 0);
-        }
-    }
-    seg_keys<RT, KT, W>(s, a);
-}
-// Units of all segments of one KV head of each lane's sequence (0 without rows).
-// Called by whole warps: a sequence of many row tiles is counted by all lanes.
-constexpr int kSerialTiles = 4;
-template <int RT, int KT, int W>
-__device__ __forceinline__ int seq_units(const AttnArgs& a, const Seg& s) {
-    int u = 0;
-    Seg x = s;
-    if (s.n_rt <= kSerialTiles)
-        for (x.rt = 0; x.rt < s.n_rt; ++x.rt) {
-            seg_keys<RT, KT, W>(x, a);
-            u += x.n_units;
-        }
-    for (unsigned big = __ballot_sync(~0u, s.n_rt > kSerialTiles); big; big &= big - 1) {
-        const int from = __ffs(big) - 1, lane = threadIdx.x & 31;
-        x.n_q = __shfl_sync(~0u, s.n_q, from);
-        x.n_kv = __shfl_sync(~0u, s.n_kv, from);
-        x.n_rt = __shfl_sync(~0u, s.n_rt, from);
-        int sum = 0;
-        for (x.rt = lane; x.rt < x.n_rt; x.rt += 32) {
-            seg_keys<RT, KT, W>(x, a);
-            sum += x.n_units;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if (lane == from) u = sum;
-    }
-    return u;
-}
-// Called by a whole warp with one sequence's numbers: the row tile that holds unit
-// rem of its list, and rem within it.
-template <int RT, int KT, int W>
-__device__ __noinline__ int2 find_row_tile(Seg x, int rem, const AttnArgs* a) {
-    const int lane = threadIdx.x & 31;
-    for (int rt0 = 0;; rt0 += 32) {
-        x.rt = rt0 + lane;
-        if (x.rt < x.n_rt) seg_keys<RT, KT, W>(x, *a);
-        const int own = x.rt < x.n_rt ? x.n_units : 0;
-        int inc = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(~0u, inc, o);
-            if (lane >= o) inc += y;
-        }
-        const unsigned hit = __ballot_sync(~0u, rem < inc);
-        if (hit || rt0 + 32 >= x.n_rt) {
-            const int at = hit ? __ffs(hit) - 1 : 0;
-            return make_int2(rt0 + at, rem - __shfl_sync(~0u, inc - own, at));
-        }
-        rem -= __shfl_sync(~0u, inc, 31);
-    }
-}
-
-// A walk over a CTA's share of the units: the piece of a segment it is at. In
-// shared memory: one for the CTA, two pieces deep, and one for each warp's
-// requests, which run ahead.
-struct Walk {
-    Seg s;
-    int left;           // units of the share from this piece on
-    int ua, ub;         // this piece's units within the segment
-    int more;           // 0: the share has ended
-    int seg_no;         // the segment's number in the whole list
-};
-static_assert(sizeof(Walk) == 64, "walk");
-template <int W>
-__device__ __forceinline__ int2 walk_tiles(const Walk& w, int warp) {
-    return make_int2(max(w.ua - kSegCost, 0) * W + warp, min(max(w.ub - kSegCost, 0) * W, w.s.n_tiles));
-}
-// What happens once a piece stays out of line: the loop over tiles is what the
-// instruction cache has to hold.
-template <int RT, int KT, int W>
-__device__ __noinline__ void walk_next(const Walk* from, Walk* to, const AttnArgs* a) {
-    Walk v = *from;
-    v.left -= v.ub - v.ua;
-    v.more = v.left > 0;
-    if (v.more) {
-        seg_next<RT, KT, W>(v.s, *a);
-        ++v.seg_no;
-        v.ua = 0;
-        v.ub = min(v.s.n_units, v.left);
-    }
-    *to = v;
-}
-// The warp's requests go on to its next piece with tiles: {next tile, end}, {0, 0} at the share's end.
-template <int RT, int KT, int W>
-__device__ __noinline__ int2 request_next(Walk* w, const AttnArgs* a, int warp) {
-    for (;;) {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) walk_next<RT, KT, W>(w, w, a);
-        __syncwarp();
-        if (!w->more) return make_int2(0, 0);
-        const int2 t = walk_tiles<W>(*w, warp);
-        if (t.x < t.y) return t;
-    }
-}
 static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, uint64_t ns) { return mbar_wait(bar, phase, ns); }
 
 template <int HD, int TYPE, int NT>
@@ -274,6 +122,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     using C = Cfg<HD, TYPE, NT>;
     constexpr int W = C::W, RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
     constexpr bool E4 = C::E4;
+    using P = Units<RT, KT, W, kSegCost>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -305,137 +154,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- this CTA's share of the units ------------------------------------
-    // (a thread for each of the first W * 32 sequences keeps what it reads)
-    constexpr int NTH = W * 32;
     const int cta = blockIdx.x;
-    Seg seq;
-    int per_head = 0, u_b = 0, s_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind
-    {
-        bool bad_any = false;
-        seq.n_rt = 0;
-        if (tid < a.n_seq) bad_any = seg_seq<RT>(seq, a, tid);
-        per_head = seq_units<RT, KT, W>(a, seq);
-        u_b = per_head * a.n_kv_head;
-        s_b = seq.n_rt * a.n_kv_head;
-        for (int b0 = NTH; b0 < a.n_seq; b0 += NTH) {
-            Seg s;
-            s.n_rt = 0;
-            if (b0 + tid < a.n_seq) bad_any |= seg_seq<RT>(s, a, b0 + tid);
-            more_u += seq_units<RT, KT, W>(a, s) * a.n_kv_head;
-            more_s += s.n_rt * a.n_kv_head;
-        }
-        if (bad_any && cta == 0) atomicOr(a.status, kStatusInput);
-    }
-    auto scan_warp = [&](int& u, int& n) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, u, o), y = __shfl_up_sync(~0u, n, o);
-            if (lane >= o) {
-                u += x;
-                n += y;
-            }
-        }
-    };
-    int inc = u_b, inc_s = s_b;
-    scan_warp(inc, inc_s);
-    if (a.n_seq > NTH) scan_warp(more_u, more_s);
-    if (lane == 31) {
-        scan[warp] = inc;
-        scan[W + warp] = inc_s;
-        scan[2 * W + warp] = more_u;
-        scan[3 * W + warp] = more_s;
-    }
-    if (tid == 0) cws[0].more = 0;
-    __syncthreads();
-    int base_u = 0, base_s = 0, total = 0, segs = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) {
-            inc += scan[w];
-            inc_s += scan[W + w];
-        }
-        base_u += scan[w];
-        base_s += scan[W + w];
-        total += scan[2 * W + w];
-        segs += scan[3 * W + w];
-    }
-    total += base_u;             // (the host refuses batches whose units could pass 31 bits)
-    segs += base_s;
-    const int n_cta = min((int)gridDim.x, total);
-    if (cta == 0 && tid == 0)    // entries of split[] that this call writes
-        *a.n_split = a.split_by_segment ? min(kMaxCtas, segs) : n_cta;
-    if (cta >= n_cta) return;
-    // shares [floor(total i / n_cta), floor(total (i + 1) / n_cta)): segments of one
-    // length are cut alike, at their ends where the numbers allow
-    const int per_cta = total / n_cta, extra = total - per_cta * n_cta;
-    auto share = [&](int i) { return per_cta * i + extra * i / n_cta; };
-    const int u0 = share(cta), my_units = share(cta + 1) - u0;
-    {
-        int b = tid;
-        for (;;) {
-            const bool hit = u_b > 0 && u0 >= inc - u_b && u0 < inc;   // one thread of the block: the share starts in its sequence
-            int rem = u0 - (inc - u_b), head = 0, tile = 0;
-            if (hit) {
-                head = a.n_kv_head == 1 ? 0 : rem / per_head;
-                rem -= head * per_head;
-            }
-            if (const unsigned many = __ballot_sync(~0u, hit && seq.n_rt > kSerialTiles)) {
-                const int from = __ffs(many) - 1;
-                Seg x;
-                x.n_q = __shfl_sync(~0u, seq.n_q, from);
-                x.n_kv = __shfl_sync(~0u, seq.n_kv, from);
-                x.n_rt = __shfl_sync(~0u, seq.n_rt, from);
-                const int2 at = find_row_tile<RT, KT, W>(x, __shfl_sync(~0u, rem, from), &a);
-                if (lane == from) {
-                    tile = at.x;
-                    rem = at.y;
-                }
-            }
-            if (hit) {
-                Walk w;
-                w.s = seq;
-                w.s.h = head;
-                for (w.s.rt = tile;; ++w.s.rt) {
-                    seg_keys<RT, KT, W>(w.s, a);
-                    if (rem < w.s.n_units || w.s.rt + 1 >= w.s.n_rt) break;
-                    rem -= w.s.n_units;
-                }
-                w.seg_no = inc_s - s_b + w.s.h * w.s.n_rt + w.s.rt;
-                w.ua = rem;
-                w.left = my_units;
-                w.ub = min(w.s.n_units, w.ua + w.left);
-                w.more = w.s.n_rt > 0;
-                cws[0] = w;
-            }
-            if (u0 < base_u || b - tid >= a.n_seq) break;
-            // the next W * 32 sequences
-            b += NTH;
-            seq.n_rt = 0;
-            if (b < a.n_seq) seg_seq<RT>(seq, a, b);
-            per_head = seq_units<RT, KT, W>(a, seq);
-            u_b = per_head * a.n_kv_head;
-            s_b = seq.n_rt * a.n_kv_head;
-            inc = u_b;
-            inc_s = s_b;
-            scan_warp(inc, inc_s);
-            __syncthreads();
-            if (lane == 31) {
-                scan[warp] = inc;
-                scan[W + warp] = inc_s;
-            }
-            __syncthreads();
-            inc += base_u;
-            inc_s += base_s;
-            for (int w = 0; w < W; ++w) {
-                if (w < warp) {
-                    inc += scan[w];
-                    inc_s += scan[W + w];
-                }
-                base_u += scan[w];
-                base_s += scan[W + w];
-            }
-        }
-    }
+    const Share share = first_walk<P, W * 32>(a, cta, scan, cws);
+    if (share.units == 0) return;
     // For a piece's rows: the keys each sees, [y, x), and copies of its Q rows to
     // shared memory (a 16-dim group in the order the MMA takes its dims).
     constexpr int QN = (RT * HD / 8 + W * 32 - 1) / (W * 32);      // 16-byte chunks of a thread
@@ -490,8 +211,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     __syncwarp();
 
     // ---- the warp's ring: slots q = 0, 1, ... hold K, V, K, V, ... of its tiles ----
-    int2 pt = walk_tiles<W>(*pw, warp);   // the next tile to request of the piece, and its end
-    if (pt.x >= pt.y) pt = request_next<RT, KT, W>(pw, &a, warp);
+    int2 pt = walk_tiles<P>(*pw, warp);   // the next tile to request of the piece, and its end
+    if (pt.x >= pt.y) pt = request_next<P>(pw, &a, warp);
     constexpr int BLK = 32 / SUB;  // tiles of a page block: a lane for each 16 keys
     int blk = 0;                 // tiles of the page block used up
     int b_page = -1, p_page[SUB] = {};
@@ -565,7 +286,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             i_tile = (i_tile + 1) % C::ENTRIES;
             ++blk;
             if ((pt.x += W) >= pt.y) {
-                pt = request_next<RT, KT, W>(pw, &a, warp);
+                pt = request_next<P>(pw, &a, warp);
                 blk = BLK;
             }
             if (blk == BLK) load_pages();
@@ -618,17 +339,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         const int row0 = cw.s.rt * RT, tok0 = cw.s.tok0, head0 = cw.s.h * a.group;
         const int rows = min(RT, cw.s.n_q * a.group - row0);
         if (tid == (W - 1) * 32) {         // (the last warp has no more tiles than the others)
-            // the merge kernel's entry: who holds states of this segment
-            const bool starts = cw.ua == 0, last_piece = cw.left <= cw.ub - cw.ua;
-            Split sp{cta, -1, tok0, row0, rows, cw.s.h, {0, 0}};
-            if (starts && !whole) {
-                // the CTA whose share holds its last unit x: the largest c with share(c) <= x
-                const int x = u0 + my_units - cw.left + cw.s.n_units - 1;
-                sp.last = min(n_cta - 1, (int)((((int64_t)x + 1) * n_cta - 1) / total));
-            }
-            const int at = a.split_by_segment ? cw.seg_no : cta;
-            if ((a.split_by_segment ? starts : last_piece) && at < kMaxCtas) a.split[at] = sp;
-            walk_next<RT, KT, W>(&cw, &cws[which ^ 1], &a);
+            put_split(a, share, cta, cw, row0, rows);
+            walk_next<P>(&cw, &cws[which ^ 1], &a);
         }
         const int min_lim = view[0].x, max_low = view[RT - 1].y;       // (rows behind the last see what it sees)
         const uint32_t q_lane = smem_addr(q_sm) + ((lane & 7) + (NT > 1 ? lane >> 4 : 0) * 8) * C::QPITCH +
@@ -674,7 +386,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             for (int m = 0; m < MT; ++m) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
         }
 
-        const int2 tiles = walk_tiles<W>(cw, warp);
+        const int2 tiles = walk_tiles<P>(cw, warp);
         const int tile0 = cw.s.tile0;
         for (int t = tiles.x; t < tiles.y; t += W) {
             // ---- S^T = K Q^T ------------------------------------------------
