@@ -49,7 +49,7 @@ class FrAttnPlan(ctypes.Structure):
 
 
 class FrPagedKV(ctypes.Structure):
-    _fields_ = [("opaque", ctypes.c_uint64 * 64)]
+    _fields_ = [("opaque", ctypes.c_uint64 * 96)]
 
 
 class FrPagedBatch(ctypes.Structure):

@@ -148,7 +148,8 @@ static bool strides_ok(const int64_t* st, int n_pages, int n_head, int page_size
     return true;
 }
 
-static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, int64_t page, int64_t head, int64_t row) {
+static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, int64_t page, int64_t head, int64_t row,
+                         int box_rows, bool all_boxes) {
     auto enc = get_encoder();
     if (!enc) return false;
     const bool e4 = d.type == FR_KV_E4M3;
@@ -159,7 +160,7 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
     // the stride of a size-1 dimension is never used, but has to be valid
     cuuint64_t strides[4] = {(cuuint64_t)row * elem, (cuuint64_t)box_bytes, (cuuint64_t)(d.n_kv_head > 1 ? head * elem : 16),
                              (cuuint64_t)(d.n_pages > 1 ? page * elem : 16)};
-    cuuint32_t box[5] = {in_box, 16, (cuuint32_t)(row_bytes / box_bytes), 1, 1};
+    cuuint32_t box[5] = {in_box, (cuuint32_t)box_rows, all_boxes ? (cuuint32_t)(row_bytes / box_bytes) : 1u, 1, 1};
     cuuint32_t es[5] = {1, 1, 1, 1, 1};
     CUtensorMap m;
     if (enc(&m, e4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), dims,
@@ -171,6 +172,10 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
     return true;
 }
 
+// Average query rows of a sequence and KV head from which the 128-row kernel takes
+// f16 pages. One sequence of 65536 keys, 8 KV heads, hd 128: 32 rows 63 us in tiles
+// of 32; 64 rows 79 us in one tile of 128 and 106 us in two of 32; 128 rows 82 and 178 us.
+constexpr int kManyRows = 33;
 static int max_nt(int hd) { return hd == 256 ? 2 : 4; }
 // Attention CTAs for row tiles of 8*nt rows on a GPU of sms SMs (the workspace is sized for the most)
 static int ctas_for(int hd, int nt, int sms) {
@@ -183,7 +188,7 @@ static size_t ws_rows(int hd) {        // rows of split states, two states for e
         const size_t r = (size_t)2 * ctas_for(hd, nt, kMaxCtas) * 8 * nt;
         if (r > n) n = r;
     }
-    return n;
+    return n < (size_t)2 * kTcCtas * kTcRows ? (size_t)2 * kTcCtas * kTcRows : n;
 }
 static size_t ws_bytes(int hd) {
     return kWsHeader + sizeof(Split) * kMaxCtas + ws_rows(hd) * (sizeof(float2) + 4 * (size_t)hd);
@@ -235,7 +240,12 @@ extern "C" fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const 
     d.hd = hd;
     d.type = type;
     d.magic = kKvMagic;
-    if (!encode_pages(d.k_map, d, k, d.k_page, d.k_head, d.k_row) || !encode_pages(d.v_map, d, v, d.v_page, d.v_head, d.v_row))
+    if (!encode_pages(d.k_map, d, k, d.k_page, d.k_head, d.k_row, kTile, true) ||
+        !encode_pages(d.v_map, d, v, d.v_page, d.v_head, d.v_row, kTile, true))
+        return FR_ERR_CUDA;
+    const int rows = page_size < 64 ? page_size : 64;
+    if (!e4 && (!encode_pages(d.k_map_tc, d, k, d.k_page, d.k_head, d.k_row, rows, false) ||
+                !encode_pages(d.v_map_tc, d, v, d.v_page, d.v_head, d.v_row, rows, false)))
         return FR_ERR_CUDA;
     memcpy(kv, &d, sizeof(d));
     return FR_OK;
@@ -297,13 +307,15 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     // sequence of the batch fills (a longer one takes several row tiles)
     const int64_t avg = (int64_t)G * ((bt->n_tok + bt->n_seq - 1) / bt->n_seq);
     const int nt = avg <= 8 ? 1 : avg <= 16 ? 2 : max_nt(kv->hd);
-    const int rt = 8 * nt;
+    const bool many = kv->type == FR_KV_F16 && avg >= kManyRows && G <= kTcRows;
+    const int rt = many ? kTcRows / G * G : 8 * nt;
+    const int part_rows = many ? kTcRows : rt;        // rows of a state in the workspace
     // at most this many segments, and units of work, whatever the lengths say
     const int64_t per_tok = (int64_t)bt->n_tok * ((G + rt - 1) / rt), per_seq = bt->n_seq + (int64_t)bt->n_tok * G / rt;
     const int64_t segs = (per_tok < per_seq ? per_tok : per_seq) * kv->n_kv_head;
     const int64_t cap_units = (((int64_t)bt->max_pages << kv->page_shift) + kUnit - 1) / kUnit;
-    int64_t ctas = ctas_for(kv->hd, nt, sms);
-    const int64_t cap = segs * (cap_units + kSegCost);
+    int64_t ctas = !many ? ctas_for(kv->hd, nt, sms) : sms < kTcCtas ? sms : kTcCtas;
+    const int64_t cap = segs * (cap_units + (many ? kTcSegCost : kSegCost));
     if (cap > 0x7fffffff) return FR_ERR_UNSUPPORTED;
     if (cap < ctas) ctas = cap;
 
@@ -333,12 +345,14 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     a.group = G;
     // r * ceil(2^32 / G) / 2^32 = r / G + r e / (2^32 G) with e < G: exact below r e < 2^32
     if (G > 1 && (int64_t)bt->n_tok * G * G < (int64_t{1} << 32)) a.group_magic = (unsigned)(((uint64_t{1} << 32) + G - 1) / G);
+    a.row_tile = rt;
     a.causal = causal ? 1 : 0;
     // a window that no sequence outgrows is none (and positions less it stay in 32 bits)
     a.window = window >= ((int64_t)bt->max_pages << kv->page_shift) ? 0 : window;
     a.split_by_segment = segs <= ctas ? 1 : 0;
     a.scale_log2 = scale_log2;
-    const fr_status st = kv->type == FR_KV_E4M3 ? launch_attn_e4m3(*kv, a, nt, (int)ctas, stream)
+    const fr_status st = many                     ? launch_attn_tc(*kv, a, (int)ctas, stream)
+                         : kv->type == FR_KV_E4M3 ? launch_attn_e4m3(*kv, a, nt, (int)ctas, stream)
                                                 : launch_attn_f16(*kv, a, nt, (int)ctas, stream);
     if (st != FR_OK) return st;
 
@@ -363,7 +377,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_merge_kernel, (const Split*)a.split, (const int*)a.n_split,
-                                             (const float*)a.part_o, (const float2*)a.part_ml, out, rt, kv->hd, G,
+                                             (const float*)a.part_o, (const float2*)a.part_ml, out, part_rows, kv->hd, G,
                                              kv->n_kv_head, cols);
     return e == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }

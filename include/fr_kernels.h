@@ -359,7 +359,7 @@ fr_status fr_decode_attn_noalloc_check(cudaStream_t stream);
 #define FR_KV_F16 0    /* f16 pages */
 #define FR_KV_E4M3 1   /* e4m3 codes, one f32 scale for each page and KV head: value = scale * code */
 
-typedef struct fr_paged_kv { uint64_t opaque[64]; } fr_paged_kv;
+typedef struct fr_paged_kv { uint64_t opaque[96]; } fr_paged_kv;
 typedef struct fr_paged_batch { uint64_t opaque[16]; } fr_paged_batch;
 
 /*
@@ -439,10 +439,13 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  *   out         f32 [n_tok][n_head][hd] contiguous
  *   workspace   >= fr_paged_attn_workspace_size bytes, zeroed once
  *               (fr_workspace_init); one for each concurrently running call
- * Made for few query rows a sequence (decode, speculative tokens): each 32 rows
- * (16 at hd 256) of a sequence's KV head read its keys once.
+ * Few query rows a sequence (decode, speculative tokens) and e4m3 pages take row
+ * tiles of 8 to 32 rows, each of which reads the keys; many rows over f16 pages
+ * (prompts) take tiles of 128.
  * A weight enters the PV product within 2^-22 of itself, or 2^-32 of its row's
  * largest (e4m3: each times its V scale, against the largest V scale in view).
+ * It does so as two terms: infinite values of V in a row's view make the element
+ * infinite or NaN.
  * The result does not depend on timing: same inputs, same bits.
  */
 fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,

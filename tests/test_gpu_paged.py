@@ -780,3 +780,176 @@ def test_a_serving_run(kind):
         want, tol = ref.attention(q16.cpu().view(n_tok, n_head, hd), ref.values(k, ks), ref.values(v, vs), starts(new), kv, table, n_head)
         check(out, want, tol, f"step {i}")
     fr.workspace_check(ws)
+
+
+# ---- many query rows (prompts, wide windows): the 128-row tiles --------------------
+
+PROMPTS = ([70, 1, 129, 0, 300, 64, 33, 5], [70, 65, 129, 40, 300, 1000, 33, 3])     # (the last: more tokens than keys)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("H,G", [(2, 1), (2, 3), (1, 8), (1, 16), (1, 100)])
+def test_prompt_head_layouts(hd, H, G):
+    new, kv = PROMPTS if G < 16 else ([x // 4 for x in PROMPTS[0]], PROMPTS[1])
+    run_case("f16", hd, H, G, 32, new, kv, seed=hd + G)
+
+
+@pytest.mark.parametrize("ps", [16, 64, 128, 256])
+@pytest.mark.parametrize("nhd", [False, True])
+def test_prompt_page_sizes_and_layouts(ps, nhd):
+    run_case("f16", 128, 2, 4, ps, *PROMPTS, seed=ps, nhd=nhd)
+
+
+@pytest.mark.parametrize("ps", [16, 32, 256])
+@pytest.mark.parametrize("kw", [dict(causal=False), dict(window=1), dict(window=50), dict(window=130),
+                                dict(window=2 ** 31 - 1), dict(kq_scale=-1.5)],
+                         ids=lambda k: "_".join(f"{a}{b}" for a, b in k.items()))
+def test_prompt_masks(ps, kw):
+    run_case("f16", 128, 1, 5, ps, *PROMPTS, seed=3, **kw)
+
+
+@pytest.mark.parametrize("hd,G,n,kv", [(128, 8, 16, 20000), (256, 4, 40, 9000), (64, 16, 9, 30011)])
+def test_prompt_behind_a_long_cache(hd, G, n, kv):
+    """Few row tiles, split over every CTA."""
+    run_case("f16", hd, 1, G, 64, [n], [kv], seed=7)
+
+
+def test_prompts_of_many_sequences():
+    """More sequences than threads of a block; many segments to a CTA."""
+    rng = np.random.default_rng(12)
+    kv = [int(x) for x in rng.integers(1, 130, 400)]
+    new = [int(min(a, b)) for a, b in zip(rng.integers(0, 30, 400), kv)]
+    run_case("f16", 64, 2, 4, 16, new, kv, seed=12)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_prompt_places_out_of_view(hd):
+    """Junk behind the sequences' ends, in V rows that only later tokens see (one
+    row NaN, one infinite, in two places of a tile), and in pages of nobody: each
+    row of the result has what its own view holds."""
+    H, G, ps = 2, 4, 32
+    new, kv = [100, 40], [150, 40]
+    n_pages = 9
+    (k, _, v, _), _ = make_cache("f16", n_pages, H, ps, hd, 17)
+    table = make_tables(kv, ps, n_pages, 17)
+    want, tol = ref.attention(rand_q(sum(new), H * G, hd, 18), k.double(), v.double(), starts(new), kv, table, H * G)
+    used = torch.zeros((n_pages, ps), dtype=torch.bool)
+    for b, n in enumerate(kv):
+        for j in range(n):
+            used[table[b, j // ps], j % ps] = True
+    for d in (k, v):
+        d.transpose(1, 2)[~used] = float("nan")
+    at = lambda b, j: (int(table[b, j // ps]), j % ps)
+    p, r = at(0, 149)
+    v[p, :, r] = float("nan")                           # seen by the last token only
+    p, r = at(0, 130)
+    v[p, 1, r, 5] = float("inf")                        # tokens from 80 on, head 1, one dim
+    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda()), make_batch(new, kv, table), rand_q(sum(new), H * G, hd, 18).cuda(),
+                        H * G)
+    assert torch.isnan(out[99]).all()
+    # (a weight is the sum of two f16 terms, the second of either sign or 0: infinity
+    # times them is infinity or NaN)
+    assert not torch.isfinite(out[80:99, G:, 5]).any()
+    keep = torch.ones(out.shape, dtype=torch.bool)
+    keep[99] = False
+    keep[80:99, G:, 5] = False
+    got = torch.where(keep, out.cpu().double(), want)
+    check(got.float().where(keep, torch.zeros(())), want.where(keep, torch.zeros((), dtype=torch.float64)), tol)
+
+
+def test_prompt_visible_nan_keys():
+    """A NaN key makes NaN of the rows that see it, and of no others."""
+    hd, G, ps, n, kv = 128, 4, 16, 100, 120
+    (k, _, v, _), _ = make_cache("f16", 8, 1, ps, hd, 3)
+    table = make_tables([kv], ps, 8, 3)
+    q = rand_q(n, G, hd)
+    want, tol = ref.attention(q, k.double(), v.double(), [0, n], [kv], table, G)
+    k[int(table[0, 90 // ps]), 0, 90 % ps, 7] = float("nan")
+    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda()), make_batch([n], [kv], table), q.cuda(), G)
+    assert torch.isnan(out[70:]).all()
+    check(out[:70], want[:70], tol[:70])
+
+
+@pytest.mark.parametrize("ps", [16, 32, 128])
+def test_prompt_pages_behind_the_window_and_bad_pages(ps):
+    hd, H, G, window = 128, 1, 4, 70
+    new, kv = [40, 30], [500, 300]
+    n_pages = sum(-(-x // ps) for x in kv) + 2
+    (k, _, v, _), cache = make_cache("f16", n_pages, H, ps, hd, 83)
+    table = make_tables(kv, ps, n_pages, 83)
+    q = rand_q(sum(new), H * G, hd, 84)
+    want, tol = ref.attention(q, k.double(), v.double(), starts(new), kv, table, H * G, window=window)
+    gone = table.clone()
+    for b in range(2):
+        gone[b, :max(0, kv[b] - new[b] + 1 - window) // ps] = -1
+    ws = fr.make_paged_workspace(H * G, H, hd)
+    out = fr.paged_attn(cache, make_batch(new, kv, gone), q.cuda(), H * G, window=window, workspace=ws)
+    check(out, want, tol)
+    fr.workspace_check(ws)
+    # a page that is in view and outside the pool: its keys are masked, and the status word tells
+    first = kv[1] - 10                                   # (within the last page, or its tile)
+    bad = table.clone()
+    bad[1, first // ps] = n_pages
+    out = fr.paged_attn(cache, make_batch(new, kv, bad), q.cuda(), H * G, workspace=ws)
+    with pytest.raises(fr.FrError):
+        fr.workspace_check(ws)
+    want, tol = ref.attention(q, k.double(), v.double(), starts(new), kv, table, H * G)
+    check(out[:40], want[:40], tol[:40])
+    cut = first // ps * ps                               # tokens that see nothing of that page
+    before = max(0, cut - (kv[1] - new[1]))
+    check(out[40:40 + before], want[40:40 + before], tol[40:40 + before])
+    assert torch.isfinite(out).all()
+
+
+def test_prompt_strided_q_rows_behind_and_repeats():
+    """q16 as columns of a wider buffer; rows behind the last sequence keep what
+    the output held; the same call twice gives the same bits; a captured graph
+    follows the lengths."""
+    hd, H, G, ps, new, kv = 128, 2, 4, 16, [50, 21], [400, 33]
+    n_pages, n_tok = 30, 80
+    (k, _, v, _), cache = make_cache("f16", n_pages, H, ps, hd)
+    table = make_tables(kv, ps, n_pages)
+    q = rand_q(n_tok, H * G, hd)
+    qw = torch.full((n_tok, H * G * hd + 64), float("nan"), dtype=torch.float16)
+    qw[:, :H * G * hd] = q.reshape(n_tok, -1)
+    qd = qw.cuda()[:, :H * G * hd].unflatten(1, (H * G, hd))
+    out = torch.full((n_tok, H * G, hd), -3.0, device="cuda")
+    batch = make_batch(new, kv, table)
+    ws = fr.make_paged_workspace(H * G, H, hd)
+    keep = torch.full(out.shape, -3.0)
+    fr.paged_attn(cache, batch, qd, H * G, out=out, workspace=ws)
+    want, tol = ref.attention(q, k.double(), v.double(), starts(new), kv, table, H * G, out=keep)
+    check(out, want, tol)
+    assert (out[sum(new):] == -3.0).all()
+    again = torch.full_like(out, -3.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        fr.paged_attn(cache, batch, qd, H * G, out=again, workspace=ws, stream=side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+    kv2, new2 = [300, 100], [10, 60]
+    t2 = make_tables(kv2, ps, n_pages, 9)
+    batch.kv_len.copy_(torch.tensor(kv2, dtype=torch.int32))
+    batch.tok_start.copy_(torch.tensor(starts(new2), dtype=torch.int32))
+    batch.page_table[:, :t2.shape[1]].copy_(t2)
+    again.fill_(-3.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    want, tol = ref.attention(q, k.double(), v.double(), starts(new2), kv2, t2, H * G, out=keep)
+    check(again, want, tol)
+    fr.workspace_check(ws)
+
+
+def test_prompt_as_its_tokens_one_by_one():
+    """A prompt's rows are those that each token gives by itself over the keys before it."""
+    hd, H, G, ps, n = 128, 2, 4, 16, 64
+    (k, _, v, _), cache = make_cache("f16", 8, H, ps, hd, 5)
+    table = make_tables([n], ps, 8, 5)
+    q = rand_q(n, H * G, hd, 6)
+    out = fr.paged_attn(cache, make_batch([n], [n], table), q.cuda(), H * G)
+    one = torch.cat([fr.paged_attn(cache, make_batch([1], [i + 1], table), q[i:i + 1].cuda(), H * G) for i in range(n)])
+    _, tol = ref.attention(q, k.double(), v.double(), [0, n], [n], table, H * G)
+    check(out, one.double().cpu(), 2 * tol)
