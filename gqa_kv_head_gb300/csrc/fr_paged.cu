@@ -149,7 +149,7 @@ static bool strides_ok(const int64_t* st, int n_pages, int n_head, int page_size
 }
 
 static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, int64_t page, int64_t head, int64_t row,
-                         int box_rows, bool all_boxes) {
+                         int box_rows, bool tc) {
     auto enc = get_encoder();
     if (!enc) return false;
     const bool e4 = d.type == FR_KV_E4M3;
@@ -160,21 +160,23 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
     // the stride of a size-1 dimension is never used, but has to be valid
     cuuint64_t strides[4] = {(cuuint64_t)row * elem, (cuuint64_t)box_bytes, (cuuint64_t)(d.n_kv_head > 1 ? head * elem : 16),
                              (cuuint64_t)(d.n_pages > 1 ? page * elem : 16)};
-    cuuint32_t box[5] = {in_box, (cuuint32_t)box_rows, all_boxes ? (cuuint32_t)(row_bytes / box_bytes) : 1u, 1, 1};
+    cuuint32_t box[5] = {in_box, (cuuint32_t)box_rows, tc ? 1u : (cuuint32_t)(row_bytes / box_bytes), 1, 1};
     cuuint32_t es[5] = {1, 1, 1, 1, 1};
     CUtensorMap m;
     if (enc(&m, e4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), dims,
             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            tc && e4 ? CU_TENSOR_MAP_SWIZZLE_NONE : box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return false;
     memcpy(dst, &m, sizeof(m));
     return true;
 }
 
-// Average query rows of a sequence and KV head from which the 128-row kernel takes
-// f16 pages. One sequence of 65536 keys, 8 KV heads, hd 128: 32 rows 63 us in tiles
-// of 32; 64 rows 79 us in one tile of 128 and 106 us in two of 32; 128 rows 82 and 178 us.
+// Average query rows of a sequence and KV head from which the 128-row kernel is
+// taken. One sequence of 65536 keys, 8 KV heads, hd 128, in tiles of 32 rows and in one
+// of 128: f16, 32 rows 63 and 82 us, 64 rows 106 and 82, 128 rows 178 and 85;
+// e4m3, 32 rows 68 and 99 us, 64 rows 110 and 99, 128 rows 188 and 106.
 constexpr int kManyRows = 33;
 static int max_nt(int hd) { return hd == 256 ? 2 : 4; }
 // Attention CTAs for row tiles of 8*nt rows on a GPU of sms SMs (the workspace is sized for the most)
@@ -240,12 +242,12 @@ extern "C" fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const 
     d.hd = hd;
     d.type = type;
     d.magic = kKvMagic;
-    if (!encode_pages(d.k_map, d, k, d.k_page, d.k_head, d.k_row, kTile, true) ||
-        !encode_pages(d.v_map, d, v, d.v_page, d.v_head, d.v_row, kTile, true))
+    if (!encode_pages(d.k_map, d, k, d.k_page, d.k_head, d.k_row, kTile, false) ||
+        !encode_pages(d.v_map, d, v, d.v_page, d.v_head, d.v_row, kTile, false))
         return FR_ERR_CUDA;
-    const int rows = page_size < 64 ? page_size : 64;
-    if (!e4 && (!encode_pages(d.k_map_tc, d, k, d.k_page, d.k_head, d.k_row, rows, false) ||
-                !encode_pages(d.v_map_tc, d, v, d.v_page, d.v_head, d.v_row, rows, false)))
+    const int rows = tc_box_rows(page_size, hd, e4);
+    if (!encode_pages(d.k_map_tc, d, k, d.k_page, d.k_head, d.k_row, rows, true) ||
+        !encode_pages(d.v_map_tc, d, v, d.v_page, d.v_head, d.v_row, rows, true))
         return FR_ERR_CUDA;
     memcpy(kv, &d, sizeof(d));
     return FR_OK;
@@ -307,7 +309,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     // sequence of the batch fills (a longer one takes several row tiles)
     const int64_t avg = (int64_t)G * ((bt->n_tok + bt->n_seq - 1) / bt->n_seq);
     const int nt = avg <= 8 ? 1 : avg <= 16 ? 2 : max_nt(kv->hd);
-    const bool many = kv->type == FR_KV_F16 && avg >= kManyRows && G <= kTcRows;
+    const bool many = avg >= kManyRows && G <= kTcRows;
     const int rt = many ? kTcRows / G * G : 8 * nt;
     const int part_rows = many ? kTcRows : rt;        // rows of a state in the workspace
     // at most this many segments, and units of work, whatever the lengths say

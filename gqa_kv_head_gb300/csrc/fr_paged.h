@@ -31,6 +31,12 @@ constexpr int kSegCost = 2;          // units that a segment's start and end cou
 constexpr int kTcSegCost = 4;        // the same for the 128-row kernel, whose units are shorter
 constexpr int kTcRows = 128;         // its row tile at most
 constexpr int kTcCtas = 160;         // its CTAs at most, one per SM
+// its loads: rows of a slot of e4m3 codes (what fits beside the f16 tiles), and of a TMA box
+__host__ __device__ constexpr int raw_rows(int hd) { return hd == 256 ? 32 : 64; }
+inline int tc_box_rows(int page_size, int hd, bool e4) {
+    const int most = e4 ? raw_rows(hd) : 64;
+    return page_size < most ? page_size : most;
+}
 constexpr size_t kWsHeader = 1024;   // [0, 4): status word, as in the other workspaces
 
 // What fr_paged_kv holds, in the library's own terms.
@@ -38,7 +44,7 @@ struct KvDesc {
     // 5-D CUtensorMap bytes (dim in box, row, box, head, page) of the attention's
     // tile loads; copied to an aligned place at the launch
     unsigned char k_map[sizeof(CUtensorMap)], v_map[sizeof(CUtensorMap)];
-    unsigned char k_map_tc[sizeof(CUtensorMap)], v_map_tc[sizeof(CUtensorMap)];   // f16: one 64-dim box of up to 64 rows
+    unsigned char k_map_tc[sizeof(CUtensorMap)], v_map_tc[sizeof(CUtensorMap)];   // of the 128-row kernel's: boxes of up to 64 rows
     void *k, *v;
     float *k_scale, *v_scale;        // e4m3: [n_pages][n_kv_head]
     int64_t k_page, k_head, k_row;   // strides in elements
@@ -105,7 +111,7 @@ __device__ __forceinline__ SeqInfo seq_info(const int32_t* tok_start, const int3
 constexpr unsigned kStatusTimeout = 1u, kStatusInput = 0x100u;
 
 fr_status launch_attn_f16(const KvDesc& kv, const AttnArgs& a, int row_tiles8, int ctas, cudaStream_t st);
-// f16 pages, row tiles of up to 128 rows (a.row_tile: whole tokens)
+// either type, row tiles of up to 128 rows (a.row_tile: whole tokens)
 fr_status launch_attn_tc(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st);
 fr_status launch_attn_e4m3(const KvDesc& kv, const AttnArgs& a, int row_tiles8, int ctas, cudaStream_t st);
 // Pointer checks shared by the entry points.

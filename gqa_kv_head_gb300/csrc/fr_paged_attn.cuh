@@ -60,18 +60,6 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Two e4m3 codes (the low or the high half of x) as f16x2, exact.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
-    uint32_t y;
-    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, a; }" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
-    uint32_t y;
-    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, b; }" : "=r"(y) : "r"(x));
-    return y;
-}
-
 // D (16x8 f32) += A (16x16 f16, row) * B (16x8 f16, col); free to be scheduled
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"

@@ -1,13 +1,13 @@
-// fr_paged_tc.cu -- attention over f16 pages for many query rows of a sequence
-// and KV head (prompts, wide speculative windows): row tiles of up to 128 rows
+// fr_paged_tc.cu -- attention over pages for many query rows of a sequence and KV
+// head (prompts, wide speculative windows): row tiles of up to 128 rows
 // on tcgen05.
 //
 // Beyond a few tens of rows the bound is no longer the bytes of K and V but the
 // matrix work: an mma.sync kernel of small row tiles reads the keys again for
 // each tile and ends at about 190 TFLOP/s. Here a row tile holds whole tokens
 // (128 / G tokens of G heads, so one TMA box is the tile) as the M of
-// S = Q K^T and O += P V; S, P and O live in TMEM. One CTA an SM works through its share of the
-// list of units (fr_paged_work.cuh) piece by piece:
+// S = Q K^T and O += P V; S, P and O live in TMEM. One CTA an SM works through
+// its share of the list of units (fr_paged_work.cuh) piece by piece:
 //   warps 0-7  softmax: a thread owns a row's half of the tile's 64 columns;
 //              masks from the row's view, running reference and sum, P as two
 //              f16 terms (P_hi + P_lo, 22 bits) back into TMEM. Where a tile
@@ -17,9 +17,21 @@
 //   warp 8     producer: page numbers and TMA, K and V in rings of their own; it
 //              runs on into the next piece.
 //   warp 9     MMA issuer: S of the next tile ahead of PV of this one.
+//   10-13      e4m3 only: codes to f16, from the slots that the TMA fills into the
+//              MMA's. K's scale joins the score's factor, V's the weights,
+//              relative to the largest in the row's view so far (another running
+//              reference beside the maximum).
 // The roles follow the list each with its own walk and meet only at mbarriers.
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
+//
+// Measured: 2048 new tokens behind 30720 keys, 32 heads on 8, hd 128, f16: 2.0 ms,
+// 530 TFLOP/s (counted once; P_lo makes it 790 on the tensor cores). Four prompts
+// of 2048: 370 us in f16 and 625 us in e4m3 (1620 us in tiles of 32 rows). A tile
+// takes 1.1 us in f16, about as long in the softmax warps as in the MMAs; e4m3 is
+// bound by the conversion: two warps took 752 us for the four prompts, one
+// load at a time 875; the same four with the registers split by warpgroup (144 and
+// 112) spilled more and took 657.
 #include <string.h>
 
 #include <cudaTypedefs.h>
@@ -33,25 +45,30 @@ namespace tc {
 using namespace sm100;
 
 constexpr int kBN = 64;                      // keys of a tile
-constexpr int kSmax = 256, kThreads = 320, kProd = 8, kMma = 9;
+constexpr int kSmax = 256, kProd = 8, kMma = 9, kConv = 10, kConvThreads = 128;   // softmax threads; warps
 constexpr float kTau = 8.0f;
 constexpr uint64_t kLimit = 2000000000ull;
 
-template <int HD>
+template <int HD, bool E4>
 struct Cfg {
-    static constexpr int NB = HD / 64;                        // 128-byte column boxes
+    static constexpr int THREADS = E4 ? 448 : 320;
+    static constexpr int NB = HD / 64;                        // 128-byte column boxes of f16
     static constexpr int KS = HD == 64 ? 6 : HD == 128 ? 4 : 2;   // K slots, and V slots
+    // e4m3: slots of codes, K and V in turn, of RAWR rows each
+    static constexpr int RAWR = raw_rows(HD), BOXB = HD < 128 ? HD : 128, RAW_BYTES = RAWR * HD, PARTS = kBN / RAWR;
+    static constexpr int RS = !E4 ? 0 : HD == 64 ? 8 : HD == 128 ? 6 : 3;
     static constexpr int Q_BOX = 128 * 128, KV_BOX = kBN * 128, TILE = kBN * HD * 2;
-    static constexpr int Q = 0, K = 128 * HD * 2, V = K + KS * TILE, AUX = V + KS * TILE;
-    // auxiliary area: half-row maxima and sums, walks, scan, bad-page masks, odd rows of V, barriers
-    static constexpr int A_MAX = 0, A_L = 2048, A_WALK = 3072, A_SCAN = A_WALK + 64 * 11, A_BAD = A_SCAN + 256,
-                         A_ODD = A_BAD + 64, A_BAR = A_ODD + 528, AUX_BYTES = A_BAR + 512;
+    static constexpr int Q = 0, K = 128 * HD * 2, V = K + KS * TILE, RAW = V + KS * TILE,
+                         AUX = RAW + RS * RAW_BYTES;
+    // auxiliary area: half-row maxima and sums, walks, scan, tiles' pages, odd rows of V, barriers
+    static constexpr int A_MAX = 0, A_L = 2048, A_WALK = 3072, A_SCAN = A_WALK + 64 * 17, A_META = A_SCAN + 256,
+                         A_ODD = A_META + 16 * 64, A_BAR = A_ODD + 528, AUX_BYTES = A_BAR + 512;
     static constexpr int SMEM = AUX + AUX_BYTES + 1024;
     static_assert(SMEM <= 232448, "shared memory");
     // barriers
     static constexpr int B_KF = 0, B_KE = KS, B_VF = 2 * KS, B_VE = 3 * KS, B_SF = 4 * KS, B_PF = B_SF + 2, B_OD = B_SF + 4,
                          B_OF = B_SF + 6, B_QF = B_SF + 7, B_QE = B_SF + 8, B_OE = B_SF + 9, B_END = B_SF + 10,
-                         N_BAR = B_SF + 11;
+                         B_RF = B_SF + 11, B_RE = B_RF + RS, N_BAR = B_RE + RS;
     static_assert(N_BAR <= 60, "barriers");
     // TMEM columns: O, two S tiles, two tiles of P_hi and of P_lo words (two keys a column)
     static constexpr int T_O = 0, T_S = HD, T_P = HD + 2 * kBN, T_PL = T_P + kBN;
@@ -61,8 +78,14 @@ struct Cfg {
 struct TcMaps {
     CUtensorMap q, k, v;
 };
+struct Meta {                                                // a tile's 16-key steps
+    float ks[4], vs[4];                                      // e4m3: scales
+    int page[4];                                             // -1: none
+    uint32_t none;                                           // bit i: step i has none
+    int pad[3];
+};
 struct Pages {                                               // the cache as plain memory (rare rows are read there)
-    const __half *k, *v;
+    const void *k, *v;
     int64_t k_page, k_head, k_row, v_page, v_head, v_row;
     int box_rows;                                            // rows of a K or V box: min(page, 64)
     int tok_tile;                                            // tokens of a row tile
@@ -82,6 +105,13 @@ __device__ __forceinline__ void load_q(uint32_t dst, const CUtensorMap* map, int
 }
 __device__ __forceinline__ bool odd_half2(uint32_t x) { return (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u; }
 
+// Element i of a page row, and whether its pair holds an infinity or NaN.
+template <bool E4>
+__device__ __forceinline__ float page_value(const void* p, int64_t i) {
+    if (!E4) return __half2float(reinterpret_cast<const __half*>(p)[i]);
+    return __half2float(__ushort_as_half((unsigned short)e4m3_lo(reinterpret_cast<const unsigned char*>(p)[i])));
+}
+
 // Keys that a row sees: [lo, hi).
 __device__ __forceinline__ int2 row_view(const Seg& s, int row, const AttnArgs& a) {
     int hi = s.n_kv, lo = 0;
@@ -93,12 +123,12 @@ __device__ __forceinline__ int2 row_view(const Seg& s, int row, const AttnArgs& 
     return make_int2(lo, hi);
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int HD, bool E4>
+__global__ void __launch_bounds__((Cfg<HD, E4>::THREADS), 1)
 paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMaps mp, const __grid_constant__ Pages pg) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, E4>;
     using P = Units<0, kBN, 1, kTcSegCost>;
-    constexpr int KS = C::KS, HB = kBN / 2, OH = HD / 2;
+    constexpr int KS = C::KS, RS = E4 ? C::RS : 1, HB = kBN / 2, OH = HD / 2;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     unsigned char* aux = sm + C::AUX;
@@ -106,7 +136,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     float* s_l = reinterpret_cast<float*>(aux + C::A_L);                 // [2][128]
     Walk* walks = reinterpret_cast<Walk*>(aux + C::A_WALK);              // the share's start, then one for each warp
     int* scan = reinterpret_cast<int*>(aux + C::A_SCAN);
-    volatile uint32_t* s_bad = reinterpret_cast<volatile uint32_t*>(aux + C::A_BAD);   // [16] steps without a page
+    Meta* s_meta = reinterpret_cast<Meta*>(aux + C::A_META);             // [16]
     // Odd rows of V, two deep: one warp may be a tile, or a piece, ahead of another
     volatile int* s_odd = reinterpret_cast<volatile int*>(aux + C::A_ODD);             // [2][64] tile (+ 1) with an odd row here
     volatile int* s_piece = s_odd + 2 * kBN;                             // [2] piece (+ 1) that met odd rows
@@ -122,7 +152,10 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     };
 
     if (tid == 0) {
-        for (int i = 0; i < C::N_BAR; ++i) mbar_init(bar(i), i == C::B_PF || i == C::B_PF + 1 || i == C::B_OE ? kSmax : 1);
+        for (int i = 0; i < C::N_BAR; ++i) {
+            const bool full = (i >= C::B_KF && i < C::B_KF + KS) || (i >= C::B_VF && i < C::B_VF + KS);
+            mbar_init(bar(i), i == C::B_PF || i == C::B_PF + 1 || i == C::B_OE ? kSmax : E4 && full ? kConvThreads : i >= C::B_RE ? kConvThreads / 32 : 1);
+        }
         mbar_fence_init();
         prefetch_tmap(&mp.k);
         prefetch_tmap(&mp.v);
@@ -132,7 +165,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     if (warp == kMma) tmem_alloc(smem_addr(s_tmem), 512);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share share = first_walk<P, kThreads>(a, cta, scan, walks);
+    const Share share = first_walk<P, C::THREADS>(a, cta, scan, walks);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -146,47 +179,78 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     if (!work) {
         // nothing of the list
     } else if (warp == kProd) {
-        int n = 0, piece = 0, blk = 0, nk = 0, nv = 0, nq = 0;     // tiles; pieces; loads (lane 0)
+        int n = 0, piece = 0, blk = 0, nk = 0, nv = 0, nq = 0, item = 0;     // tiles; pieces; loads (lane 0)
         for (;;) {
             const int2 t = walk_tiles<P>(*w, 0);
             const Seg& s = w->s;
             int page = -1;
             bool has = false;
+            float ks = 0.f, vs = 0.f;
             auto look_up = [&](int tile) {       // pages of the next 32 16-key steps, one a lane
                 const int key = (s.tile0 + tile) * kBN + lane * kTile;
                 // (a box is looked up for its first key, also where only its last ones are in view)
                 has = key < s.n_kv && (key | (pg.box_rows - 1)) >= s.lo && tile + lane / 4 < t.y;
                 page = has ? a.table[s.b * a.table_stride + (key >> a.page_shift)] : -1;
+                if (has && (page < 0 || page >= a.n_pages)) {
+                    atomicOr(a.status, kStatusInput);
+                    page = -1;
+                }
+                if (E4) {
+                    ks = page >= 0 ? a.k_scale[(int64_t)page * a.n_kv_head + s.h] : 0.f;
+                    vs = page >= 0 ? a.v_scale[(int64_t)page * a.n_kv_head + s.h] : 0.f;
+                }
                 blk = 0;
             };
             if (t.x < t.y) look_up(t.x);
             for (int tile = t.x; tile < t.y; ++tile, ++n) {
                 if (blk == 8) look_up(tile);
-                if (blk == 0 && has && (page < 0 || page >= a.n_pages)) {
-                    atomicOr(a.status, kStatusInput);
-                    page = -1;
-                }
-                const unsigned none = __ballot_sync(~0u, page < 0) >> (blk * 4) & 15u;
-                int pgs[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) pgs[i] = max(__shfl_sync(~0u, page, blk * 4 + i), 0);   // (page 0 in place of none: masked)
-                ++blk;
                 const int st = n % KS, key = (s.tile0 + tile) * kBN, in_page = (1 << a.page_shift) - 1;
+                // (this wait also keeps the tile within 16 of the softmax's)
                 if (lane == 0) {
-                    auto tile_loads = [&](const CUtensorMap* map, uint32_t dst, uint32_t b) {
-                        mbar_expect_tx(b, C::TILE);
+                    if (!E4 && n >= KS) wait(C::B_KE + st, ((n / KS) - 1) & 1);
+                    if (E4 && item >= C::RS) wait(C::B_RE + item % RS, ((item / RS) - 1) & 1);
+                }
+                __syncwarp();
+                Meta& m = s_meta[n & 15];
+                const unsigned gone = __ballot_sync(~0u, page < 0) >> (blk * 4) & 15u;
+                if (lane == 0) m.none = gone;
+                if (lane >> 2 == blk) {
+                    m.page[lane & 3] = page;
+                    if (E4) {
+                        m.ks[lane & 3] = ks;
+                        m.vs[lane & 3] = vs;
+                    }
+                }
+                ++blk;
+                __syncwarp();
+                if (lane == 0) {
+                    // rows r0 .. r0 + n_rows - 1 of the tile (page 0 in place of none: masked)
+                    auto tile_loads = [&](const CUtensorMap* map, uint32_t dst, uint32_t b, int r0, int n_rows) {
+                        constexpr int PITCH = E4 ? C::BOXB : 128;
+                        mbar_expect_tx(b, n_rows * HD * (E4 ? 1 : 2));
 #pragma unroll 1
-                        for (int r = 0; r < kBN; r += pg.box_rows)
+                        for (int r = 0; r < n_rows; r += pg.box_rows) {
+                            const int page_at = max(m.page[(r0 + r) >> 4], 0);
 #pragma unroll
-                            for (int c = 0; c < C::NB; ++c)
-                                load_box(dst + c * C::KV_BOX + r * 128, map, (key + r) & in_page, c, s.h,
-                                         r == 0 ? pgs[0] : r == 16 ? pgs[1] : r == 32 ? pgs[2] : pgs[3], b);
+                            for (int c = 0; c < HD * (E4 ? 1 : 2) / PITCH; ++c)
+                                load_box(dst + (c * n_rows + r) * PITCH, map, (key + r0 + r) & in_page, c, s.h, page_at, b);
+                        }
+                    };
+                    auto code_loads = [&](const CUtensorMap* map, bool waited) {
+#pragma unroll 1
+                        for (int part = 0; part < C::PARTS; ++part) {
+                            const int rs = item % RS;
+                            if (item >= C::RS && !(waited && part == 0)) wait(C::B_RE + rs, ((item / RS) - 1) & 1);
+                            if (failed) return;
+                            tile_loads(map, smem_addr(sm + C::RAW + rs * C::RAW_BYTES), bar(C::B_RF + rs), part * C::RAWR, C::RAWR);
+                            ++item;
+                        }
                     };
                     // (after a wait that gave up nothing more is loaded)
-                    if (n >= KS) wait(C::B_KE + st, ((n / KS) - 1) & 1);
-                    s_bad[n & 15] = none;
-                    if (!failed) {
-                        tile_loads(&mp.k, smem_addr(sm + C::K + st * C::TILE), bar(C::B_KF + st));
+                    if (E4) {
+                        if (!failed) code_loads(&mp.k, true);
+                    } else if (!failed) {
+                        tile_loads(&mp.k, smem_addr(sm + C::K + st * C::TILE), bar(C::B_KF + st), 0, kBN);
                         ++nk;
                     }
                     if (tile == t.x) {
@@ -199,9 +263,11 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                             ++nq;
                         }
                     }
-                    if (n >= KS) wait(C::B_VE + st, ((n / KS) - 1) & 1);
-                    if (!failed) {
-                        tile_loads(&mp.v, smem_addr(sm + C::V + st * C::TILE), bar(C::B_VF + st));
+                    if (!E4 && n >= KS) wait(C::B_VE + st, ((n / KS) - 1) & 1);
+                    if (E4) {
+                        if (!failed) code_loads(&mp.v, false);
+                    } else if (!failed) {
+                        tile_loads(&mp.v, smem_addr(sm + C::V + st * C::TILE), bar(C::B_VF + st), 0, kBN);
                         ++nv;
                     }
                 }
@@ -209,11 +275,14 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             }
             if (t.x < t.y) ++piece;
             __syncwarp();
-            if (lane == 0) walk_next<P>(w, w, &a);
+            if (lane == 0) walk_on<P>(w, w, &a);
             __syncwarp();
             if (!w->more) break;
         }
         if (lane == 0) {                         // every load has landed before the CTA ends
+            for (int i = max(0, item - C::RS); i < item; ++i)
+                if (!mbar_wait(bar(C::B_RF + i % RS), (i / RS) & 1, kLimit))
+                    atomicOr(a.status, kStatusTimeout);
             for (int i = max(0, nk - KS); i < nk; ++i)
                 if (!mbar_wait(bar(C::B_KF + i % KS), (i / KS) & 1, kLimit)) atomicOr(a.status, kStatusTimeout);
             for (int i = max(0, nv - KS); i < nv; ++i)
@@ -271,11 +340,59 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     n += cnt;
                     ++piece;
                 }
-                walk_next<P>(w, w, &a);
+                walk_on<P>(w, w, &a);
                 if (!w->more) break;
             }
             mma_commit(bar(C::B_END));
             if (!mbar_wait(bar(C::B_END), 0, kLimit)) atomicOr(a.status, kStatusTimeout);
+        }
+    } else if (E4 && warp >= kConv) {
+        // codes to f16, which is exact: 16 of a row at a time, into the 128-byte swizzle of the MMA's operands
+        const int ct = tid - kConv * 32;
+        int n = 0, item = 0;
+        auto convert = [&](unsigned char* ring, int b_full, int b_empty) {
+            const int st = n % KS;
+            if (n >= KS) wait(b_empty + st, ((n / KS) - 1) & 1);
+            unsigned char* dst = ring + st * C::TILE;
+#pragma unroll 1
+            for (int part = 0; part < C::PARTS; ++part, ++item) {
+                constexpr int PER_ROW = C::BOXB / 16;
+                const int rs = item % RS;
+                wait(C::B_RF + rs, (item / RS) & 1);
+                const unsigned char* src = sm + C::RAW + rs * C::RAW_BYTES;
+                constexpr int N = C::RAW_BYTES / 16 / kConvThreads;
+                uint4 zs[N];                          // (all loads ahead of the stores)
+#pragma unroll
+                for (int u = 0; u < N; ++u) zs[u] = *reinterpret_cast<const uint4*>(src + (ct + u * kConvThreads) * 16);
+#pragma unroll
+                for (int u = 0; u < N; ++u) {
+                    const uint4 z = zs[u];
+                    const int i = ct + u * kConvThreads;
+                    const int row = part * C::RAWR + i / PER_ROW % C::RAWR;
+                    const int d = i / (PER_ROW * C::RAWR) * C::BOXB + i % PER_ROW * 16;
+                    const uint4 lo = make_uint4(e4m3_lo(z.x), e4m3_hi(z.x), e4m3_lo(z.y), e4m3_hi(z.y));
+                    const uint4 hi = make_uint4(e4m3_lo(z.z), e4m3_hi(z.z), e4m3_lo(z.w), e4m3_hi(z.w));
+                    unsigned char* to = dst + (d >> 6) * C::KV_BOX + row * 128;
+                    const int c = d >> 3 & 7, odd = d >> 6 & 1;      // (of a row's two boxes one starts with its odd chunks: other banks)
+                    *reinterpret_cast<uint4*>(to + (((c + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+                    *reinterpret_cast<uint4*>(to + (((c + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_RE + rs));
+            }
+            fence_proxy_async_cta();
+            mbar_arrive(bar(b_full + st));
+        };
+        for (;;) {
+            const int2 t = walk_tiles<P>(*w, 0);
+            for (int tile = t.x; tile < t.y; ++tile, ++n) {
+                convert(sm + C::K, C::B_KF, C::B_KE);
+                convert(sm + C::V, C::B_VF, C::B_VE);
+            }
+            __syncwarp();
+            if (lane == 0) walk_on<P>(w, w, &a);
+            __syncwarp();
+            if (!w->more) break;
         }
     } else {
         const int qd = warp & 3, half = warp >> 2, r = qd * 32 + lane, c_base = half * HB;
@@ -289,20 +406,31 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             const int2 view = r < rows ? row_view(s, row0 + r, a) : make_int2(0, 0);
             const bool active = qd * 32 < rows;
             if (tid == 0) put_split(a, share, cta, *w, row0, rows);
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
             for (int tile = t.x; tile < t.y; ++tile, ++n) {
                 wait(C::B_SF + (n & 1), (n >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
                 const int key0 = (s.tile0 + tile) * kBN;
-                const uint32_t none = s_bad[n & 15];
+                const Meta& m = s_meta[n & 15];
+                const uint32_t none = m.none;
                 const bool edge = none || key0 + kBN > first.y || key0 < end.x;
+                float v_max = 0.f, v_step[2] = {1.f, 1.f};        // e4m3: V's scales, of the steps that the row sees
+                if (E4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = key0 + i * kTile;
+                        const float v = edge && (j >= view.y || j + kTile <= view.x || (none >> i & 1u)) ? 0.f : m.vs[i];
+                        v_max = fmaxf(v_max, fabsf(v));
+                        if (i >> 1 == half) v_step[i & 1] = v;
+                    }
+                }
                 float x[HB], pm = -INFINITY;
                 if (active) {
                     tmem_ld_x32(tbase + lanes + C::T_S + (n & 1) * kBN + c_base, reinterpret_cast<uint32_t*>(x));
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < HB; ++c) x[c] *= a.scale_log2;
+                    for (int c = 0; c < HB; ++c) x[c] *= E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2;
                     if (edge || r >= rows) {
 #pragma unroll
                         for (int c = 0; c < HB; ++c) {
@@ -322,8 +450,21 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 if (mx > m_ref + kTau || (m_ref == -INFINITY && mx > -INFINITY)) m_new = fmaxf(mx, m_ref);
                 const bool grown = m_ref != -INFINITY && m_new != m_ref;
                 const float alpha = grown ? ex2(m_ref - m_new) : 1.f;
+                // V's scales join the weights relative to the largest that the row has met
+                float o_scale = alpha;
+                const bool v_up = E4 && v_max > v_ref;
+                if (v_up) {
+                    const float v = fmaxf(v_max, 0x1p-120f);         // its reciprocal stays finite
+                    o_scale *= v_ref / v;
+                    v_ref = v;
+                }
+                if (E4) {
+                    const float v_inv = v_ref > 0.f ? 1.f / v_ref : 0.f;
+                    v_step[0] *= v_inv;
+                    v_step[1] *= v_inv;
+                }
                 if (active) {
-                    if (__any_sync(~0u, grown) && tile > t.x) {
+                    if (__any_sync(~0u, grown || v_up) && tile > t.x) {
                         wait(C::B_OD + ((n - 1) & 1), ((n - 1) >> 1) & 1);           // O holds PV up to the tile before
                         __syncwarp();
                         tc_fence_after();
@@ -333,7 +474,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                             tmem_ld_x32(tbase + lanes + C::T_O + half * OH + c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * o_scale);
                             tmem_st_x32(tbase + lanes + C::T_O + half * OH + c, o);
                         }
                         tmem_wait_st();
@@ -344,8 +485,12 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int c = 0; c < HB; c += 2) {
-                        const float p0 = ex2(x[c] - sub), p1 = ex2(x[c + 1] - sub);
+                        float p0 = ex2(x[c] - sub), p1 = ex2(x[c + 1] - sub);
                         s4[(c >> 1) & 3] += p0 + p1;
+                        if (E4) {
+                            p0 *= v_step[c / 16];
+                            p1 *= v_step[c / 16];
+                        }
                         hi[c / 2] = pack_half2(p0, p1);
                         const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi[c / 2]));
                         lo[c / 2] = pack_half2(p0 - hf.x, p1 - hf.y);
@@ -395,7 +540,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             const bool whole = w->ua == 0 && w->ub == s.n_units;
             const int part = 2 * cta + (w->ua == 0 && !whole ? 1 : 0);
             const float m_out = l == 0.f ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref;
-            const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f, f_v = E4 ? v_ref : 1.f;
             const int tok = token_of(row0 + min(r, rows - 1), a), hh = row0 + min(r, rows - 1) - tok * G;
             float* dst = whole ? a.out + ((int64_t)(s.tok0 + tok) * a.n_kv_head * G + s.h * G + hh) * HD
                                : a.part_o + ((int64_t)part * 128 + r) * HD;
@@ -422,22 +567,25 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                                 const int page = a.table[s.b * a.table_stride + (j >> a.page_shift)];
                                 if (page < 0 || page >= a.n_pages) continue;
                                 const int in = j & ((1 << a.page_shift) - 1);
-                                const __half* k = pg.k + page * pg.k_page + s.h * pg.k_head + in * pg.k_row;
-                                const __half* v = pg.v + page * pg.v_page + s.h * pg.v_head + in * pg.v_row;
+                                const int64_t k = page * pg.k_page + s.h * pg.k_head + in * pg.k_row;
+                                const int64_t v = page * pg.v_page + s.h * pg.v_head + in * pg.v_row;
                                 bool bad = false;
-                                for (int d = 0; d < HD; d += 2) bad |= odd_half2(*reinterpret_cast<const uint32_t*>(v + d));
+                                for (int d = 0; d < HD; ++d) bad |= !isfinite(page_value<E4>(pg.v, v + d));
                                 if (!bad) continue;
                                 float x = 0.f;
-                                for (int d = 0; d < HD; ++d) x = fmaf(__half2float(q[d]), __half2float(k[d]), x);
-                                const float p = ex2(x * a.scale_log2 - (m_out - 7.f));
+                                for (int d = 0; d < HD; ++d) x = fmaf(__half2float(q[d]), page_value<E4>(pg.k, k + d), x);
+                                const int64_t sc = (int64_t)page * a.n_kv_head + s.h;
+                                const float x_log2 = x * (E4 ? a.scale_log2 * a.k_scale[sc] : a.scale_log2);
+                                const float p = ex2(x_log2 - (m_out - 7.f)) *
+                                                (E4 ? (v_ref > 0.f ? a.v_scale[sc] * (1.f / v_ref) : 0.f) : 1.f);
 #pragma unroll
-                                for (int u = 0; u < 32; ++u) o[u] = fmaf(p, __half2float(v[half * OH + c + u]), o[u]);
+                                for (int u = 0; u < 32; ++u) o[u] = fmaf(p, page_value<E4>(pg.v, v + half * OH + c + u), o[u]);
                             }
                         }
 #pragma unroll
                         for (int u = 0; u < 32; u += 4)
                             *reinterpret_cast<float4*>(dst + half * OH + c + u) =
-                                make_float4(o[u] * f, o[u + 1] * f, o[u + 2] * f, o[u + 3] * f);
+                                make_float4(o[u] * f_v * f, o[u + 1] * f_v * f, o[u + 2] * f_v * f, o[u + 3] * f_v * f);
                     }
                     __syncwarp();
                 }
@@ -449,7 +597,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 ++piece;
             }
             __syncwarp();
-            if (lane == 0) walk_next<P>(w, w, &a);
+            if (lane == 0) walk_on<P>(w, w, &a);
             __syncwarp();
             if (!w->more) break;
         }
@@ -472,12 +620,13 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
     return fn;
 }
 
-template <int HD>
+template <int HD, bool E4>
 static fr_status launch(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
-    using C = Cfg<HD>;
+    using C = Cfg<HD, E4>;
     static unsigned long long done = 0ull;           // devices whose shared-memory limit is raised
     if (kv.dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> kv.dev & 1ull)) {
-        if (cudaFuncSetAttribute(paged_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+        if (cudaFuncSetAttribute(paged_tc_kernel<HD, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+            cudaSuccess)
             return FR_ERR_CUDA;
         if (kv.dev < 64) __atomic_fetch_or(&done, 1ull << kv.dev, __ATOMIC_RELEASE);
     }
@@ -497,12 +646,12 @@ static fr_status launch(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStrea
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return FR_ERR_CUDA;
-    const Pages pg{reinterpret_cast<const __half*>(kv.k), reinterpret_cast<const __half*>(kv.v), kv.k_page, kv.k_head,
-                   kv.k_row, kv.v_page, kv.v_head, kv.v_row, kv.page_size < kBN ? kv.page_size : kBN, tok_tile};
+    const Pages pg{kv.k, kv.v, kv.k_page, kv.k_head, kv.k_row, kv.v_page, kv.v_head, kv.v_row,
+                   tc_box_rows(kv.page_size, HD, E4), tok_tile};
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -510,14 +659,19 @@ static fr_status launch(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_tc_kernel<HD>, a, mp, pg) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_tc_kernel<HD, E4>, a, mp, pg) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }
 
 }  // namespace tc
 
 fr_status launch_attn_tc(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
-    return kv.hd == 64 ? tc::launch<64>(kv, a, ctas, st) : kv.hd == 128 ? tc::launch<128>(kv, a, ctas, st)
-                                                                          : tc::launch<256>(kv, a, ctas, st);
+    if (kv.type == FR_KV_E4M3)
+        return kv.hd == 64    ? tc::launch<64, true>(kv, a, ctas, st)
+               : kv.hd == 128 ? tc::launch<128, true>(kv, a, ctas, st)
+                              : tc::launch<256, true>(kv, a, ctas, st);
+    return kv.hd == 64    ? tc::launch<64, false>(kv, a, ctas, st)
+           : kv.hd == 128 ? tc::launch<128, false>(kv, a, ctas, st)
+                          : tc::launch<256, false>(kv, a, ctas, st);
 }
 
 }  // namespace paged

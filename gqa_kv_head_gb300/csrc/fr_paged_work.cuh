@@ -9,6 +9,18 @@
 namespace fr {
 namespace paged {
 
+// Two e4m3 codes (the low or the high half of x) as f16x2, exact.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+    uint32_t y;
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, a; }" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+    uint32_t y;
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, b; }" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // Row r's token: r / group, by a multiplication where the host found it exact.
 __device__ __forceinline__ int token_of(int r, const AttnArgs& a) {
     return a.group_magic ? (int)__umulhi((unsigned)r, a.group_magic) : r / a.group;
@@ -141,10 +153,8 @@ template <class P>
 __device__ __forceinline__ int2 walk_tiles(const Walk& w, int warp) {
     return make_int2(max(w.ua - P::SEG, 0) * P::W + warp, min(max(w.ub - P::SEG, 0) * P::W, w.s.n_tiles));
 }
-// What happens once a piece stays out of line: the loop over tiles is what the
-// instruction cache has to hold.
 template <class P>
-__device__ __noinline__ void walk_next(const Walk* from, Walk* to, const AttnArgs* a) {
+__device__ __forceinline__ void walk_on(const Walk* from, Walk* to, const AttnArgs* a) {
     Walk v = *from;
     v.left -= v.ub - v.ua;
     v.more = v.left > 0;
@@ -155,6 +165,12 @@ __device__ __noinline__ void walk_next(const Walk* from, Walk* to, const AttnArg
         v.ub = min(v.s.n_units, v.left);
     }
     *to = v;
+}
+// What happens once a piece stays out of line: the loop over tiles is what the
+// instruction cache has to hold.
+template <class P>
+__device__ __noinline__ void walk_next(const Walk* from, Walk* to, const AttnArgs* a) {
+    walk_on<P>(from, to, a);
 }
 // The warp's requests go on to its next piece with tiles: {next tile, end}, {0, 0} at the share's end.
 template <class P>

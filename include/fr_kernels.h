@@ -439,9 +439,8 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  *   out         f32 [n_tok][n_head][hd] contiguous
  *   workspace   >= fr_paged_attn_workspace_size bytes, zeroed once
  *               (fr_workspace_init); one for each concurrently running call
- * Few query rows a sequence (decode, speculative tokens) and e4m3 pages take row
- * tiles of 8 to 32 rows, each of which reads the keys; many rows over f16 pages
- * (prompts) take tiles of 128.
+ * Few query rows a sequence (decode, speculative tokens) take row tiles of 8 to
+ * 32 rows, each of which reads the keys; many rows (prompts) take tiles of 128.
  * A weight enters the PV product within 2^-22 of itself, or 2^-32 of its row's
  * largest (e4m3: each times its V scale, against the largest V scale in view).
  * It does so as two terms: infinite values of V in a row's view make the element

@@ -14,7 +14,8 @@ def pow2_scale(amax):
     return s
 
 
-def attention(q16, k, v, tok_start, kv_len, table, n_head, causal=True, window=0, kq_scale=1.0, out=None):
+def attention(q16, k, v, tok_start, kv_len, table, n_head, causal=True, window=0, kq_scale=1.0, out=None,
+              v_scale=None):
     """k, v: float64 [n_pages, n_kv_head, page_size, hd]. Returns (out, tol): the
     rows in 64 bits, and for each element the error a kernel may have that
 
@@ -26,7 +27,16 @@ def attention(q16, k, v, tok_start, kv_len, table, n_head, causal=True, window=0
       * sums weights and weighted values in fp32, a rounding of 2^-23 for each
         16-key step and for each of at most 400 joins of states.
 
-    Both the numerator and the denominator err by that share."""
+    Both the numerator and the denominator err by that share.
+
+    A weight times its V scale (over the largest V scale in view) is held as two
+    f16 terms, with the row's largest weight at 2^7 or more. The second term is
+    rounded to f16's grid, which below 2^-14 has the fixed step 2^-24: it is off by
+    2^-25 at most there, 2^-25 / 2^7 = 2^-32 of the largest weight, and a share of
+    the weight (counted above) elsewhere. With codes c_j = v_j / v_scale_j the
+    numerator errs by another 2^-32 max_j w_j max v_scale sum_j |c_j| (for f16
+    pages the scales are 1). It matters where the keys that carry the weight have
+    zeros in a dim. v_scale: [n_pages, n_kv_head], or None."""
     n_tok, hd = q16.shape[0], q16.shape[2]
     H, ps = k.shape[1], k.shape[2]
     G = n_head // H
@@ -39,6 +49,8 @@ def attention(q16, k, v, tok_start, kv_len, table, n_head, causal=True, window=0
             continue
         ids = table[b, :-(-n // ps)].long()
         for h in range(H):
+            vs = torch.ones(len(ids), dtype=torch.float64) if v_scale is None else v_scale[ids, h].double().abs()
+            per_key = vs.repeat_interleave(ps)[:n, None]
             kh, vh = k[ids, h].reshape(-1, hd)[:n], v[ids, h].reshape(-1, hd)[:n]
             for t in range(t0, t1):
                 p = n - (t1 - t0) + (t - t0)
@@ -54,7 +66,9 @@ def attention(q16, k, v, tok_start, kv_len, table, n_head, causal=True, window=0
                 out[t, h * G:(h + 1) * G] = w @ vv
                 ds = (hd + 4) * eps * (abs(kq_scale) * (q.abs() @ kk.abs().T)).amax(dim=1)
                 share = 2 * ds + 2 * 2.0 ** -21 + ((end - begin) / 16 + 400) * eps
-                tol[t, h * G:(h + 1) * G] = (w @ vv.abs()) * (2 * share)[:, None]
+                code = torch.where(per_key[begin:end] > 0, vv.abs() / per_key[begin:end], 0.0).sum(dim=0)
+                floor = 2.0 ** -32 * w.amax(dim=1)[:, None] * (vs.max() * code)
+                tol[t, h * G:(h + 1) * G] = (w @ vv.abs()) * (2 * share)[:, None] + floor
     return out, tol
 
 

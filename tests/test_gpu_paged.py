@@ -77,7 +77,8 @@ def run_case(kind, hd, H, G, ps, new, kv_len, seed=0, nhd=False, **kw):
     table = make_tables(kv_len, ps, n_pages, seed)
     q = rand_q(sum(new), H * G, hd, seed + 1)
     out = fr.paged_attn(cache, make_batch(new, kv_len, table), q.cuda(), H * G, **kw)
-    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts(new), kv_len, table, H * G, **kw)
+    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts(new), kv_len, table, H * G,
+                              v_scale=vs, **kw)
     check(out, want, tol, f"{kind} hd{hd} H{H} G{G} ps{ps} {kw}")
     return out
 
@@ -787,64 +788,74 @@ def test_a_serving_run(kind):
 PROMPTS = ([70, 1, 129, 0, 300, 64, 33, 5], [70, 65, 129, 40, 300, 1000, 33, 3])     # (the last: more tokens than keys)
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("H,G", [(2, 1), (2, 3), (1, 8), (1, 16), (1, 100)])
-def test_prompt_head_layouts(hd, H, G):
+def test_prompt_head_layouts(kind, hd, H, G):
     new, kv = PROMPTS if G < 16 else ([x // 4 for x in PROMPTS[0]], PROMPTS[1])
-    run_case("f16", hd, H, G, 32, new, kv, seed=hd + G)
+    run_case(kind, hd, H, G, 32, new, kv, seed=hd + G)
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("ps", [16, 64, 128, 256])
 @pytest.mark.parametrize("nhd", [False, True])
-def test_prompt_page_sizes_and_layouts(ps, nhd):
-    run_case("f16", 128, 2, 4, ps, *PROMPTS, seed=ps, nhd=nhd)
+def test_prompt_page_sizes_and_layouts(kind, ps, nhd):
+    run_case(kind, 128, 2, 4, ps, *PROMPTS, seed=ps, nhd=nhd)
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("ps", [16, 32, 256])
 @pytest.mark.parametrize("kw", [dict(causal=False), dict(window=1), dict(window=50), dict(window=130),
                                 dict(window=2 ** 31 - 1), dict(kq_scale=-1.5)],
                          ids=lambda k: "_".join(f"{a}{b}" for a, b in k.items()))
-def test_prompt_masks(ps, kw):
-    run_case("f16", 128, 1, 5, ps, *PROMPTS, seed=3, **kw)
+def test_prompt_masks(kind, ps, kw):
+    run_case(kind, 128, 1, 5, ps, *PROMPTS, seed=3, **kw)
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("hd,G,n,kv", [(128, 8, 16, 20000), (256, 4, 40, 9000), (64, 16, 9, 30011)])
-def test_prompt_behind_a_long_cache(hd, G, n, kv):
+def test_prompt_behind_a_long_cache(kind, hd, G, n, kv):
     """Few row tiles, split over every CTA."""
-    run_case("f16", hd, 1, G, 64, [n], [kv], seed=7)
+    run_case(kind, hd, 1, G, 64, [n], [kv], seed=7)
 
 
-def test_prompts_of_many_sequences():
+@pytest.mark.parametrize("kind", TYPES)
+def test_prompts_of_many_sequences(kind):
     """More sequences than threads of a block; many segments to a CTA."""
     rng = np.random.default_rng(12)
     kv = [int(x) for x in rng.integers(1, 130, 400)]
     new = [int(min(a, b)) for a, b in zip(rng.integers(0, 30, 400), kv)]
-    run_case("f16", 64, 2, 4, 16, new, kv, seed=12)
+    run_case(kind, 64, 2, 4, 16, new, kv, seed=12)
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("hd", [64, 128, 256])
-def test_prompt_places_out_of_view(hd):
+def test_prompt_places_out_of_view(kind, hd):
     """Junk behind the sequences' ends, in V rows that only later tokens see (one
     row NaN, one infinite, in two places of a tile), and in pages of nobody: each
     row of the result has what its own view holds."""
     H, G, ps = 2, 4, 32
     new, kv = [100, 40], [150, 40]
     n_pages = 9
-    (k, _, v, _), _ = make_cache("f16", n_pages, H, ps, hd, 17)
+    (k, ks, v, vs), _ = make_cache(kind, n_pages, H, ps, hd, 17)
     table = make_tables(kv, ps, n_pages, 17)
-    want, tol = ref.attention(rand_q(sum(new), H * G, hd, 18), k.double(), v.double(), starts(new), kv, table, H * G)
+    want, tol = ref.attention(rand_q(sum(new), H * G, hd, 18), ref.values(k, ks), ref.values(v, vs), starts(new), kv, table, H * G,
+                              v_scale=vs)
     used = torch.zeros((n_pages, ps), dtype=torch.bool)
     for b, n in enumerate(kv):
         for j in range(n):
             used[table[b, j // ps], j % ps] = True
-    for d in (k, v):
-        d.transpose(1, 2)[~used] = float("nan")
+    sc = [None, None] if ks is None else [ks.cuda(), vs.cuda()]
+    nan, inf = (0x7e00, 0x7c00) if kind == "f16" else (0x7f, 0x7f)       # (e4m3 has no infinity)
+    kb, vb = (x.view(torch.int16 if kind == "f16" else torch.uint8) for x in (k, v))
+    for d in (kb, vb):
+        d.transpose(1, 2)[~used] = nan
     at = lambda b, j: (int(table[b, j // ps]), j % ps)
     p, r = at(0, 149)
-    v[p, :, r] = float("nan")                           # seen by the last token only
+    vb[p, :, r] = nan                           # seen by the last token only
     p, r = at(0, 130)
-    v[p, 1, r, 5] = float("inf")                        # tokens from 80 on, head 1, one dim
-    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda()), make_batch(new, kv, table), rand_q(sum(new), H * G, hd, 18).cuda(),
+    vb[p, 1, r, 5] = inf                        # tokens from 80 on, head 1, one dim
+    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda(), *sc), make_batch(new, kv, table), rand_q(sum(new), H * G, hd, 18).cuda(),
                         H * G)
     assert torch.isnan(out[99]).all()
     # (a weight is the sum of two f16 terms, the second of either sign or 0: infinity
@@ -857,28 +868,33 @@ def test_prompt_places_out_of_view(hd):
     check(got.float().where(keep, torch.zeros(())), want.where(keep, torch.zeros((), dtype=torch.float64)), tol)
 
 
-def test_prompt_visible_nan_keys():
+@pytest.mark.parametrize("kind", TYPES)
+def test_prompt_visible_nan_keys(kind):
     """A NaN key makes NaN of the rows that see it, and of no others."""
     hd, G, ps, n, kv = 128, 4, 16, 100, 120
-    (k, _, v, _), _ = make_cache("f16", 8, 1, ps, hd, 3)
+    (k, ks, v, vs), _ = make_cache(kind, 8, 1, ps, hd, 3)
     table = make_tables([kv], ps, 8, 3)
     q = rand_q(n, G, hd)
-    want, tol = ref.attention(q, k.double(), v.double(), [0, n], [kv], table, G)
-    k[int(table[0, 90 // ps]), 0, 90 % ps, 7] = float("nan")
-    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda()), make_batch([n], [kv], table), q.cuda(), G)
+    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), [0, n], [kv], table, G, v_scale=vs)
+    sc = [None, None] if ks is None else [ks.cuda(), vs.cuda()]
+    kb = k.view(torch.int16 if kind == "f16" else torch.uint8)
+    kb[int(table[0, 90 // ps]), 0, 90 % ps, 7] = 0x7e00 if kind == "f16" else 0x7f
+    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda(), *sc), make_batch([n], [kv], table), q.cuda(), G)
     assert torch.isnan(out[70:]).all()
     check(out[:70], want[:70], tol[:70])
 
 
+@pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("ps", [16, 32, 128])
-def test_prompt_pages_behind_the_window_and_bad_pages(ps):
+def test_prompt_pages_behind_the_window_and_bad_pages(kind, ps):
     hd, H, G, window = 128, 1, 4, 70
     new, kv = [40, 30], [500, 300]
     n_pages = sum(-(-x // ps) for x in kv) + 2
-    (k, _, v, _), cache = make_cache("f16", n_pages, H, ps, hd, 83)
+    (k, ks, v, vs), cache = make_cache(kind, n_pages, H, ps, hd, 83)
     table = make_tables(kv, ps, n_pages, 83)
     q = rand_q(sum(new), H * G, hd, 84)
-    want, tol = ref.attention(q, k.double(), v.double(), starts(new), kv, table, H * G, window=window)
+    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts(new), kv, table, H * G, window=window,
+                              v_scale=vs)
     gone = table.clone()
     for b in range(2):
         gone[b, :max(0, kv[b] - new[b] + 1 - window) // ps] = -1
@@ -893,7 +909,8 @@ def test_prompt_pages_behind_the_window_and_bad_pages(ps):
     out = fr.paged_attn(cache, make_batch(new, kv, bad), q.cuda(), H * G, workspace=ws)
     with pytest.raises(fr.FrError):
         fr.workspace_check(ws)
-    want, tol = ref.attention(q, k.double(), v.double(), starts(new), kv, table, H * G)
+    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts(new), kv, table, H * G,
+                              v_scale=vs)
     check(out[:40], want[:40], tol[:40])
     cut = first // ps * ps                               # tokens that see nothing of that page
     before = max(0, cut - (kv[1] - new[1]))
@@ -943,13 +960,34 @@ def test_prompt_strided_q_rows_behind_and_repeats():
     fr.workspace_check(ws)
 
 
-def test_prompt_as_its_tokens_one_by_one():
+@pytest.mark.parametrize("kind", TYPES)
+def test_prompt_as_its_tokens_one_by_one(kind):
     """A prompt's rows are those that each token gives by itself over the keys before it."""
     hd, H, G, ps, n = 128, 2, 4, 16, 64
-    (k, _, v, _), cache = make_cache("f16", 8, H, ps, hd, 5)
+    (k, ks, v, vs), cache = make_cache(kind, 8, H, ps, hd, 5)
     table = make_tables([n], ps, 8, 5)
     q = rand_q(n, H * G, hd, 6)
     out = fr.paged_attn(cache, make_batch([n], [n], table), q.cuda(), H * G)
     one = torch.cat([fr.paged_attn(cache, make_batch([1], [i + 1], table), q[i:i + 1].cuda(), H * G) for i in range(n)])
-    _, tol = ref.attention(q, k.double(), v.double(), [0, n], [n], table, H * G)
+    _, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), [0, n], [n], table, H * G, v_scale=vs)
     check(out, one.double().cpu(), 2 * tol)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_prompt_e4m3_scales_of_any_size(hd):
+    """V scales from 2^-60 to 2^60, zero, negative, other than powers of two; a
+    row's result does not depend on the scales of pages behind it."""
+    H, G, ps, new, kv = 2, 4, 16, [60, 37], [160, 37]
+    (k, ks, v, vs), _ = make_cache("e4m3", 16, H, ps, hd, 29)
+    table = make_tables(kv, ps, 16, 29)
+    vs = torch.exp2(torch.randint(-60, 61, vs.shape, generator=torch.Generator().manual_seed(30)).float()) * 1.3
+    vs[:, 1] = -vs[:, 1]
+    vs[table[0, 1].long()] = 0.0
+    ks = ks * 0.7
+    q = rand_q(sum(new), H * G, hd, 31)
+    out = fr.paged_attn(fr.PagedKV(k.cuda(), v.cuda(), ks.cuda(), vs.cuda()), make_batch(new, kv, table), q.cuda(), H * G)
+    want, tol = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts(new), kv, table, H * G,
+                              v_scale=vs)
+    check(out, want, tol)
+    zero = fr.PagedKV(k.cuda(), v.cuda(), ks.cuda(), torch.zeros_like(vs).cuda())
+    assert not fr.paged_attn(zero, make_batch(new, kv, table), q.cuda(), H * G).any()
