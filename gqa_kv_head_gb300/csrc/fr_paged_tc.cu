@@ -154,7 +154,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     if (tid == 0) {
         for (int i = 0; i < C::N_BAR; ++i) {
             const bool full = (i >= C::B_KF && i < C::B_KF + KS) || (i >= C::B_VF && i < C::B_VF + KS);
-            mbar_init(bar(i), i == C::B_PF || i == C::B_PF + 1 || i == C::B_OE ? kSmax : E4 && full ? kConvThreads : i >= C::B_RE ? kConvThreads / 32 : 1);
+            mbar_init(bar(i), i == C::B_PF || i == C::B_PF + 1 || i == C::B_OE ? kSmax / 32 : (E4 && full) || i >= C::B_RE ? kConvThreads / 32 : 1);
         }
         mbar_fence_init();
         prefetch_tmap(&mp.k);
@@ -381,7 +381,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 if (lane == 0) mbar_arrive(bar(C::B_RE + rs));
             }
             fence_proxy_async_cta();
-            mbar_arrive(bar(b_full + st));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b_full + st));
         };
         for (;;) {
             const int2 t = walk_tiles<P>(*w, 0);
@@ -524,7 +525,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     fence_proxy_async_cta();
                 }
                 tc_fence_before();
-                mbar_arrive(bar(C::B_PF + (n & 1)));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_PF + (n & 1)));     // (256 arrivals on one barrier would queue)
             }
             // ---- the piece's end ------------------------------------------------
             const bool any = t.x < t.y;
@@ -593,7 +595,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             }
             if (any) {
                 tc_fence_before();
-                mbar_arrive(bar(C::B_OE));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_OE));
                 ++piece;
             }
             __syncwarp();
