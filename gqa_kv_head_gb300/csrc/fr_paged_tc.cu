@@ -179,7 +179,11 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     if (!work) {
         // nothing of the list
     } else if (warp == kProd) {
-        int n = 0, piece = 0, blk = 0, nk = 0, nv = 0, nq = 0, item = 0;     // tiles; pieces; loads (lane 0)
+        int n = 0, piece = 0, blk = 0, nk = 0, nv = 0, nq = 0, item = 0;     // tiles; pieces; loads
+        auto free_slot = [&](int b, uint32_t parity) {
+            if (lane == 0) wait(b, parity);
+            failed = __shfl_sync(~0u, (int)failed, 0);
+        };
         for (;;) {
             const int2 t = walk_tiles<P>(*w, 0);
             const Seg& s = w->s;
@@ -206,11 +210,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 if (blk == 8) look_up(tile);
                 const int st = n % KS, key = (s.tile0 + tile) * kBN, in_page = (1 << a.page_shift) - 1;
                 // (this wait also keeps the tile within 16 of the softmax's)
-                if (lane == 0) {
-                    if (!E4 && n >= KS) wait(C::B_KE + st, ((n / KS) - 1) & 1);
-                    if (E4 && item >= C::RS) wait(C::B_RE + item % RS, ((item / RS) - 1) & 1);
-                }
-                __syncwarp();
+                if (!E4 && n >= KS) free_slot(C::B_KE + st, ((n / KS) - 1) & 1);
+                if (E4 && item >= C::RS) free_slot(C::B_RE + item % RS, ((item / RS) - 1) & 1);
                 Meta& m = s_meta[n & 15];
                 const unsigned gone = __ballot_sync(~0u, page < 0) >> (blk * 4) & 15u;
                 if (lane == 0) m.none = gone;
@@ -223,55 +224,51 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 }
                 ++blk;
                 __syncwarp();
-                if (lane == 0) {
-                    // rows r0 .. r0 + n_rows - 1 of the tile (page 0 in place of none: masked)
-                    auto tile_loads = [&](const CUtensorMap* map, uint32_t dst, uint32_t b, int r0, int n_rows) {
-                        constexpr int PITCH = E4 ? C::BOXB : 128;
-                        mbar_expect_tx(b, n_rows * HD * (E4 ? 1 : 2));
+                // rows r0 .. r0 + n_rows - 1 of the tile, a box to a lane (page 0 in place of none: masked)
+                auto tile_loads = [&](const CUtensorMap* map, uint32_t dst, int b, int r0, int n_rows) {
+                    constexpr int PITCH = E4 ? C::BOXB : 128, CH = HD * (E4 ? 1 : 2) / PITCH;
+                    if (lane == 0) mbar_expect_tx(bar(b), n_rows * PITCH * CH);
+                    __syncwarp();
+                    const int c = lane % CH, r = lane / CH * pg.box_rows;
+                    if (r < n_rows)
+                        load_box(dst + (c * n_rows + r) * PITCH, map, (key + r0 + r) & in_page, c, s.h,
+                                 max(m.page[(r0 + r) >> 4], 0), bar(b));
+                };
+                auto code_loads = [&](const CUtensorMap* map, bool waited) {
 #pragma unroll 1
-                        for (int r = 0; r < n_rows; r += pg.box_rows) {
-                            const int page_at = max(m.page[(r0 + r) >> 4], 0);
-#pragma unroll
-                            for (int c = 0; c < HD * (E4 ? 1 : 2) / PITCH; ++c)
-                                load_box(dst + (c * n_rows + r) * PITCH, map, (key + r0 + r) & in_page, c, s.h, page_at, b);
-                        }
-                    };
-                    auto code_loads = [&](const CUtensorMap* map, bool waited) {
-#pragma unroll 1
-                        for (int part = 0; part < C::PARTS; ++part) {
-                            const int rs = item % RS;
-                            if (item >= C::RS && !(waited && part == 0)) wait(C::B_RE + rs, ((item / RS) - 1) & 1);
-                            if (failed) return;
-                            tile_loads(map, smem_addr(sm + C::RAW + rs * C::RAW_BYTES), bar(C::B_RF + rs), part * C::RAWR, C::RAWR);
-                            ++item;
-                        }
-                    };
-                    // (after a wait that gave up nothing more is loaded)
-                    if (E4) {
-                        if (!failed) code_loads(&mp.k, true);
-                    } else if (!failed) {
-                        tile_loads(&mp.k, smem_addr(sm + C::K + st * C::TILE), bar(C::B_KF + st), 0, kBN);
-                        ++nk;
+                    for (int part = 0; part < C::PARTS; ++part) {
+                        const int rs = item % RS;
+                        if (item >= C::RS && !(waited && part == 0)) free_slot(C::B_RE + rs, ((item / RS) - 1) & 1);
+                        if (failed) return;
+                        tile_loads(map, smem_addr(sm + C::RAW + rs * C::RAW_BYTES), C::B_RF + rs, part * C::RAWR, C::RAWR);
+                        ++item;
                     }
-                    if (tile == t.x) {
-                        if (piece > 0) wait(C::B_QE, (piece - 1) & 1);
-                        if (!failed) {
-                            mbar_expect_tx(bar(C::B_QF), C::NB * 128 * G * pg.tok_tile);
-                            for (int c = 0; c < C::NB; ++c)
-                                load_q(smem_addr(sm + C::Q + c * C::Q_BOX), &mp.q, c * 64, s.h * G,
-                                       s.tok0 + s.rt * pg.tok_tile, bar(C::B_QF));
-                            ++nq;
-                        }
-                    }
-                    if (!E4 && n >= KS) wait(C::B_VE + st, ((n / KS) - 1) & 1);
-                    if (E4) {
-                        if (!failed) code_loads(&mp.v, false);
-                    } else if (!failed) {
-                        tile_loads(&mp.v, smem_addr(sm + C::V + st * C::TILE), bar(C::B_VF + st), 0, kBN);
-                        ++nv;
+                };
+                // (after a wait that gave up nothing more is loaded)
+                if (E4) {
+                    if (!failed) code_loads(&mp.k, true);
+                } else if (!failed) {
+                    tile_loads(&mp.k, smem_addr(sm + C::K + st * C::TILE), C::B_KF + st, 0, kBN);
+                    ++nk;
+                }
+                if (tile == t.x) {
+                    if (piece > 0) free_slot(C::B_QE, (piece - 1) & 1);
+                    if (!failed) {
+                        if (lane == 0) mbar_expect_tx(bar(C::B_QF), C::NB * 128 * G * pg.tok_tile);
+                        __syncwarp();
+                        if (lane < C::NB)
+                            load_q(smem_addr(sm + C::Q + lane * C::Q_BOX), &mp.q, lane * 64, s.h * G,
+                                   s.tok0 + s.rt * pg.tok_tile, bar(C::B_QF));
+                        ++nq;
                     }
                 }
-                __syncwarp();
+                if (!E4 && n >= KS) free_slot(C::B_VE + st, ((n / KS) - 1) & 1);
+                if (E4) {
+                    if (!failed) code_loads(&mp.v, false);
+                } else if (!failed) {
+                    tile_loads(&mp.v, smem_addr(sm + C::V + st * C::TILE), C::B_VF + st, 0, kBN);
+                    ++nv;
+                }
             }
             if (t.x < t.y) ++piece;
             __syncwarp();
