@@ -175,8 +175,8 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
 
 // Average query rows of a sequence and KV head from which the 128-row kernel is
 // taken. One sequence of 65536 keys, 8 KV heads, hd 128, in tiles of 32 rows and in one
-// of 128: f16, 32 rows 63 and 82 us, 64 rows 106 and 82, 128 rows 178 and 85;
-// e4m3, 32 rows 68 and 99 us, 64 rows 110 and 99, 128 rows 188 and 106.
+// of 128: f16, 32 rows 63 and 80 us, 64 rows 106 and 81, 128 rows 178 and 84;
+// e4m3, 32 rows 68 and 105 us, 64 rows 110 and 106, 128 rows 188 and 110.
 constexpr int kManyRows = 33;
 static int max_nt(int hd) { return hd == 256 ? 2 : 4; }
 // Attention CTAs for row tiles of 8*nt rows on a GPU of sms SMs (the workspace is sized for the most)
@@ -369,7 +369,10 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     // few rows in all: 64 dims to a block, so that more SMs read the fresh states; many: fewer blocks
     const int cols = kv->hd > 64 && entries * rows > 608 ? 32 : 16;
     int64_t threads = (groups * cols + 31) / 32 * 32;
-    cfg.gridDim = dim3((unsigned)entries, (unsigned)rows, (unsigned)(kv->hd / (4 * cols)));
+    // no more blocks than run at a time: prompts have many states of many rows, and
+    // most entries nothing to join (2048 tokens: 23 -> 13 us)
+    const int64_t z = kv->hd / (4 * cols), wave = (int64_t)sms * 32 / (entries * z);
+    cfg.gridDim = dim3((unsigned)entries, (unsigned)(rows <= wave ? rows : wave < 1 ? 1 : wave), (unsigned)z);
     cfg.blockDim = dim3((unsigned)(threads > kMergeThreads ? kMergeThreads : threads));
     cfg.dynamicSmemBytes = cfg.blockDim.x * sizeof(float4) + kMaxCtas * sizeof(float);
     cfg.stream = stream;

@@ -25,13 +25,14 @@
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
 //
-// Measured: 2048 new tokens behind 30720 keys, 32 heads on 8, hd 128, f16: 2.0 ms,
-// 530 TFLOP/s (counted once; P_lo makes it 790 on the tensor cores). Four prompts
-// of 2048: 370 us in f16 and 625 us in e4m3 (1620 us in tiles of 32 rows). A tile
-// takes 1.1 us in f16, about as long in the softmax warps as in the MMAs; e4m3 is
-// bound by the conversion: two warps took 752 us for the four prompts, one
-// load at a time 875; the same four with the registers split by warpgroup (144 and
-// 112) spilled more and took 657.
+// Measured: 2048 new tokens behind 30720 keys, 32 heads on 8, hd 128, f16: 1.96 ms,
+// 540 TFLOP/s (P_lo counted: 810). Four prompts of 2048: 347 us in f16 and 631 us
+// in e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 1.1 us in f16, a
+// chain of S, softmax and PV in which none of the units is busy for more than a
+// third; three S tiles in TMEM in place of two were 3-6 % slower up to hd 128.
+// e4m3 is bound by the conversion: two warps took 752 us for the four prompts,
+// one load at a time 875; the same four with the registers split by warpgroup
+// (144 and 112) spilled more and took 657.
 #include <string.h>
 
 #include <cudaTypedefs.h>
