@@ -991,3 +991,38 @@ def test_prompt_e4m3_scales_of_any_size(hd):
     check(out, want, tol)
     zero = fr.PagedKV(k.cuda(), v.cuda(), ks.cuda(), torch.zeros_like(vs).cuda())
     assert not fr.paged_attn(zero, make_batch(new, kv, table), q.cuda(), H * G).any()
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("G,n", [(128, 3), (129, 1), (160, 4)])
+def test_prompt_groups_as_large_as_a_tile(kind, G, n):
+    """A token's heads fill a 128-row tile, or do not fit one."""
+    run_case(kind, 64, 1, G, 16, [n, 1, n], [50, 17, 129], seed=G)
+
+
+def test_prompt_graphs_share_a_workspace():
+    """Two captured prompts, one workspace, replayed in turn on one stream."""
+    hd, H, G, ps = 128, 2, 4, 16
+    ws = fr.make_paged_workspace(H * G, H, hd)
+    runs = []
+    for seed, kind, new, kv in ((1, "f16", [60, 20], [500, 20]), (2, "e4m3", [33, 90], [64, 700])):
+        n_pages = sum(-(-x // ps) for x in kv) + 2
+        (k, ks, v, vs), cache = make_cache(kind, n_pages, H, ps, hd, seed)
+        table = make_tables(kv, ps, n_pages, seed)
+        q = rand_q(sum(new), H * G, hd, seed)
+        batch, qd, out = make_batch(new, kv, table), q.cuda(), torch.zeros((sum(new), H * G, hd), device="cuda")
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            fr.paged_attn(cache, batch, qd, H * G, out=out, workspace=ws, stream=st)
+        want = ref.attention(q, ref.values(k, ks), ref.values(v, vs), starts(new), kv, table, H * G, v_scale=vs)
+        runs.append((graph, out, want, cache, batch, qd))
+    for _ in range(3):
+        for r in runs:
+            r[1].zero_()
+            r[0].replay()
+    torch.cuda.synchronize()
+    for _, out, (want, tol), *_ in runs:
+        check(out, want, tol)
+    fr.workspace_check(ws)
