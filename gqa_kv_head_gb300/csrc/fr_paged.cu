@@ -174,10 +174,18 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
 }
 
 // Average query rows of a sequence and KV head from which the 128-row kernel is
-// taken. One sequence of 65536 keys, 8 KV heads, hd 128, in tiles of 32 rows and in one
-// of 128: f16, 32 rows 63 and 80 us, 64 rows 106 and 81, 128 rows 178 and 84;
-// e4m3, 32 rows 68 and 105 us, 64 rows 110 and 106, 128 rows 188 and 110.
-constexpr int kManyRows = 33;
+// taken: where the small tiles would read the keys twice, at hd 256 in e4m3 four
+// times. Small tiles and one of 128, us, 64 sequences of 1..8000 keys, 4 KV heads:
+//   f16   hd 128, 36 rows 194 and 147; hd 256, 20 rows 329 and 204, 36 rows 489 and 207
+//   e4m3  hd 128, 36 rows 236 and 240, 64 rows 264 and 243; hd 256, 36 rows 288 and
+//         328, 64 rows 390 and 331
+// and 65536 keys, 8 KV heads, hd 128, 32 rows: f16 63 and 80, e4m3 68 and 105. Two
+// tiles of 16 rows over few long segments run side by side and meet in L2: hd 256,
+// 32 rows, 65536 keys of 1, 2, 4 heads 27 and 30, 37 and 43, 59 and 64; 16 x 8000
+// keys 29 and 32; 64 x 2000 keys 39 and 37.
+static int many_rows(int hd, int type, int64_t segs) {
+    return hd < 256 ? 33 : type == FR_KV_E4M3 ? 49 : segs >= 32 ? 17 : 33;
+}
 static int max_nt(int hd) { return hd == 256 ? 2 : 4; }
 // Attention CTAs for row tiles of 8*nt rows on a GPU of sms SMs (the workspace is sized for the most)
 static int ctas_for(int hd, int nt, int sms) {
@@ -309,7 +317,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     // sequence of the batch fills (a longer one takes several row tiles)
     const int64_t avg = (int64_t)G * ((bt->n_tok + bt->n_seq - 1) / bt->n_seq);
     const int nt = avg <= 8 ? 1 : avg <= 16 ? 2 : max_nt(kv->hd);
-    const bool many = avg >= kManyRows && G <= kTcRows;
+    const bool many = avg >= many_rows(kv->hd, kv->type, (int64_t)bt->n_seq * kv->n_kv_head) && G <= kTcRows;
     const int rt = many ? kTcRows / G * G : 8 * nt;
     const int part_rows = many ? kTcRows : rt;        // rows of a state in the workspace
     // at most this many segments, and units of work, whatever the lengths say

@@ -7,7 +7,7 @@
 //   out_r = sum_j 2^(x_rj - m_r) v_j / sum_j 2^(x_rj - m_r)
 // in one pass over the keys with a running reference m_r.
 //
-// Few rows and many keys: bound by the bytes of K and V. Keys are the MMA's M
+// Few rows and many keys (many rows: fr_paged_tc.cu): bound by the bytes of K and V. Keys are the MMA's M
 // and query rows its N (S^T = K Q^T, O^T = V^T P^T by mma.sync m16n8k16), so a
 // K or V element enters one MMA for up to 8 rows, and every warp works alone
 // on 16-key tiles: its own ring of TMA-filled slots, its own running state, no
@@ -18,7 +18,7 @@
 // synchronises the CTA on every tile.
 //
 // Work split: the keys of all (sequence, KV head, row tile) segments form one
-// list of 64-key units; each CTA (two per SM) takes an equal contiguous share
+// list of 64-key units; each CTA (one to three per SM) takes an equal contiguous share
 // of it, read from kv_len on the device, so uneven lengths balance and a
 // captured graph follows the lengths. A segment inside one CTA is normalised
 // and written there; one cut by a share's end leaves (m, l, O) states in the

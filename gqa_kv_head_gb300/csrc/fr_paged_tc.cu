@@ -25,7 +25,7 @@
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
 //
-// Measured: 2048 new tokens behind 30720 keys, 32 heads on 8, hd 128, f16: 1.96 ms,
+// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.96 ms,
 // 540 TFLOP/s (P_lo counted: 810). Four prompts of 2048: 347 us in f16 and 631 us
 // in e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 1.1 us in f16, a
 // chain of S, softmax and PV in which none of the units is busy for more than a
@@ -62,7 +62,7 @@ struct Cfg {
     static constexpr int Q = 0, K = 128 * HD * 2, V = K + KS * TILE, RAW = V + KS * TILE,
                          AUX = RAW + RS * RAW_BYTES;
     // auxiliary area: half-row maxima and sums, walks, scan, tiles' pages, odd rows of V, barriers
-    static constexpr int A_MAX = 0, A_L = 2048, A_WALK = 3072, A_SCAN = A_WALK + 64 * 17, A_META = A_SCAN + 256,
+    static constexpr int A_MAX = 0, A_L = 2048, A_WALK = A_L + 1024, A_SCAN = A_WALK + 64 * 17, A_META = A_SCAN + 256,
                          A_ODD = A_META + 16 * 64, A_BAR = A_ODD + 528, AUX_BYTES = A_BAR + 512;
     static constexpr int SMEM = AUX + AUX_BYTES + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -430,7 +430,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < HB; ++c) x[c] *= E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2;
-                    if (edge || r >= rows) {
+                    if (edge) {
 #pragma unroll
                         for (int c = 0; c < HB; ++c) {
                             const int j = key0 + c_base + c;
@@ -440,7 +440,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < HB; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c]);
-                    pm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    // (rows behind the tile's last hold anything and are not read: only their reference stays still)
+                    if (r < rows) pm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
                 s_max[((n & 1) * 2 + half) * 128 + r] = pm;
                 asm volatile("bar.sync %0, 64;" :: "r"(qd + 1) : "memory");          // the row's two halves

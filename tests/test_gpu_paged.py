@@ -1026,3 +1026,10 @@ def test_prompt_graphs_share_a_workspace():
     for _, out, (want, tol), *_ in runs:
         check(out, want, tol)
     fr.workspace_check(ws)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("H,G,n", [(3, 5, 4), (3, 7, 7), (1, 5, 4), (1, 3, 17)])
+def test_either_side_of_the_large_tiles(kind, H, G, n):
+    """hd 256: the row tile goes by the rows and, in f16, by the number of segments."""
+    run_case(kind, 256, H, G, 16, [n] * len(LENS), [max(n, x) for x in LENS], seed=G)
