@@ -28,7 +28,7 @@ __host__ __device__ constexpr int cta_smem(int hd, int nt) { return many_warps(h
 constexpr int kMaxCtas = 640;        // attention CTAs at most: the workspace holds two split states for each
 constexpr int kMaxSeq = 65536;
 constexpr int kSegCost = 2;          // units that a segment's start and end count for in the work split
-constexpr int kTcSegCost = 4;        // the same for the 128-row kernel, whose units are shorter
+constexpr int kTcSegCost = 4;        // the same for the 128-row kernel (four prompts of 2048, 2 / 4 / 6 / 9: 368 / 347 / 356 / 375 us)
 constexpr int kTcRows = 128;         // its row tile at most
 constexpr int kTcCtas = 160;         // its CTAs at most, one per SM
 // its loads: rows of a slot of e4m3 codes (what fits beside the f16 tiles), and of a TMA box
