@@ -101,7 +101,9 @@ class PagedBatch:
         self._by_rows = {}
 
     def _desc(self, n_tok):
-        """The descriptor for steps of n_tok rows, as a pointer."""
+        """The descriptor for steps of n_tok rows, as (pointer, struct). The caller
+        holds the pair until its library call returns: the library runs without
+        the interpreter's lock, and another thread may replace what is kept here."""
         d = self._by_rows.get(n_tok)
         if d is None:
             d = _abi.FrPagedBatch()
@@ -113,8 +115,8 @@ class PagedBatch:
                     stride, n_seq, n_tok, max_pages), "fr_paged_batch_init")
             if len(self._by_rows) >= 64:
                 self._by_rows.clear()
-            d = self._by_rows[n_tok] = (ctypes.addressof(d), d)
-        return d[0]
+            d = self._by_rows.setdefault(n_tok, (ctypes.addressof(d), d))
+        return d
 
 
 def _rows(t, name, cache):
@@ -150,9 +152,9 @@ def kv_append_paged(cache, batch, k_new, v_new, pos, rope, workspace=None, strea
         n_v, v_stride = _rows(v_new, "v_new", cache)
     if n_v != n_tok or pos.shape != (n_tok,) or not pos.is_contiguous():
         raise ValueError("k_new, v_new and pos must have one row a token")
-    rope = _as_rope(rope)
+    rope, desc = _as_rope(rope), batch._desc(n_tok)
     st = cache._lib.fr_kv_append_paged(
-        cache._p, batch._desc(n_tok), _ROWS[dtype], k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+        cache._p, desc[0], _ROWS[dtype], k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
         pos.data_ptr(), ctypes.addressof(rope), None if workspace is None else workspace.data_ptr(),
         _stream_of(stream, cache._index))
     if st:
@@ -201,8 +203,9 @@ def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0
         raise ValueError("out must be contiguous float32 [n_tok, n_head, hd]")
     if workspace is None:
         workspace = make_paged_workspace(n_head, cache.n_kv_head, hd, cache.device, stream)
+    desc = batch._desc(n_tok)
     st = cache._lib.fr_paged_attn(
-        cache._p, batch._desc(n_tok), q16.data_ptr(), stride, n_head, 1 if causal else 0, window, kq_scale,
+        cache._p, desc[0], q16.data_ptr(), stride, n_head, 1 if causal else 0, window, kq_scale,
         out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache._index))
     if st:
         _abi.check(st, "fr_paged_attn")
