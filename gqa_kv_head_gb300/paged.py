@@ -203,6 +203,8 @@ def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0
         raise ValueError("out must be contiguous float32 [n_tok, n_head, hd]")
     if workspace is None:
         workspace = make_paged_workspace(n_head, cache.n_kv_head, hd, cache.device, stream)
+    # (a C int would keep the low 32 bits of what does not fit it)
+    window = -1 if window < 0 else 2 ** 31 - 1 if window > 2 ** 31 - 1 else window
     desc = batch._desc(n_tok)
     st = cache._lib.fr_paged_attn(
         cache._p, desc[0], q16.data_ptr(), stride, n_head, 1 if causal else 0, window, kq_scale,

@@ -137,3 +137,18 @@ def test_descriptor_is_kept_between_calls(lib, freed):
         attend(cache, batch)
         append(cache, batch)
     assert len({int(getattr(a, "value", a)) for _, a, _ in lib.calls}) == 1 and not freed
+
+
+@pytest.mark.parametrize("window,handed", [(0, 0), (5, 5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                           (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1)])
+def test_windows_beyond_32_bits_stay_wide(lib, window, handed):
+    attend(make_cache(lib), make_batch(), window=window)
+    (_, _, args), = lib.calls
+    assert ctypes.c_int(args[4]).value == handed
+
+
+def test_negative_windows_stay_negative(lib):
+    """(so that the library refuses them)"""
+    for window in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
+        attend(make_cache(lib), make_batch(), window=window)
+        assert ctypes.c_int(lib.calls[-1][2][4]).value < 0
