@@ -88,7 +88,7 @@ struct Cfg {
     static constexpr int META = W * ENTRIES * 32;
     static constexpr int VIEWS = 2 * RT * 8;
     // alignment slack, buffers above, then barriers, walks, scan words and the warps' V scales
-    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 + 16;
+    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 + (W * 4 + 15) / 16 * 16;
     // 32 keys a slot where three slots of them fit (K, V and the next K), else 16
     static constexpr int SUB = 3 * W * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
     static constexpr int KT = kTile * SUB;                  // keys of a warp's tile
@@ -97,6 +97,9 @@ struct Cfg {
     static constexpr int NS = NS_ > 8 ? 8 : NS_;            // slots of a warp's ring
     static constexpr int SMEM = FIXED + NS * W * SLOT;
     static_assert(NS >= 3 && SMEM <= 232448, "ring");
+    // what the kernel lays out behind the alignment slack
+    static_assert(NS * W * SLOT + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 + W * 4 <= SMEM - 1024,
+                  "shared memory layout");
     // rows of a warp's O^T that one slot holds in fp32: the epilogue's chunk
     static constexpr int CNT = SLOT / (HD * 32) < NT ? SLOT / (HD * 32) : NT;
     static_assert(CNT >= 1 && NT % CNT == 0, "epilogue chunk");
