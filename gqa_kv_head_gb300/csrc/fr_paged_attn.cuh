@@ -28,11 +28,18 @@
 // between 2^7 and 2^15 at the maximum to keep P_lo off f16's subnormals: the result carries fp32 accuracy like
 // fr_decode_attn's. e4m3 codes become f16 in registers, which is exact; K's
 // scale joins the score's factor, V's scale the weights, relative to the
-// largest V scale met so far (the same kind of running reference as m).
+// largest V scale that the row has met in its view (a running reference beside
+// m). It is one number a warp where the rows have met about the same; tiles at
+// the ends of the views may set rows apart, since a scale that only other rows
+// see may be any number of times larger, and then each has its own. (One for
+// every row throughout: 63.4 us at 131072 keys of e4m3 and 54.2 at 32 sequences of
+// ..4096 keys with 16 rows, in place of 60.0 and 49.0.)
 #pragma once
 
 #include <cuda_fp16.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "fr_paged_work.cuh"
 
@@ -46,6 +53,11 @@ using namespace sm100;
 // f16 and P_lo stays off f16's subnormals for all weights that matter.
 constexpr float kBelow = 7.0f, kAbove = 15.0f;
 constexpr float kNoRef = -3.402823466e38f;           // a row without a key so far
+constexpr float kVMin = 0x1p-120f;                   // a V reference at least: its reciprocal stays finite
+// Rows whose V references differ by no more share the largest of them. That costs the
+// weights of the others 4 bits at either end of their views: f16's fixed step is then
+// 2^-24 of the row's largest weight at most, beside 2^-22 of each.
+constexpr float kVSlack = 16.0f;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int head, int page,
@@ -87,8 +99,8 @@ struct Cfg {
     static constexpr int ENTRIES = 8;                       // tiles requested and not used up, at most
     static constexpr int META = W * ENTRIES * 32;
     static constexpr int VIEWS = 2 * RT * 8;
-    // alignment slack, buffers above, then barriers, walks, scan words and the warps' V scales
-    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 + (W * 4 + 15) / 16 * 16;
+    // alignment slack, buffers above, then barriers, walks and scan words
+    static constexpr int FIXED = 1024 + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128;
     // 32 keys a slot where three slots of them fit (K, V and the next K), else 16
     static constexpr int SUB = 3 * W * 32 * ROWB <= LIMIT - FIXED ? 2 : 1;
     static constexpr int KT = kTile * SUB;                  // keys of a warp's tile
@@ -98,7 +110,7 @@ struct Cfg {
     static constexpr int SMEM = FIXED + NS * W * SLOT;
     static_assert(NS >= 3 && SMEM <= 232448, "ring");
     // what the kernel lays out behind the alignment slack
-    static_assert(NS * W * SLOT + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 + W * 4 <= SMEM - 1024,
+    static_assert(NS * W * SLOT + QBYTES + STATE + META + VIEWS + W * 64 + (W + 2) * 64 + 128 <= SMEM - 1024,
                   "shared memory layout");
     // rows of a warp's O^T that one slot holds in fp32: the epilogue's chunk
     static constexpr int CNT = SLOT / (HD * 32) < NT ? SLOT / (HD * 32) : NT;
@@ -106,6 +118,21 @@ struct Cfg {
 };
 
 static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, uint64_t ns) { return mbar_wait(bar, phase, ns); }
+
+// A lane for a row: the row's V reference, raised to the largest scale of the steps of
+// a tile (first key key0, U steps) that it sees, and what its O is to be scaled by.
+template <int U>
+static __device__ __noinline__ float2 raise_v(int2 see, float old, float2* ref, int key0, uint32_t bad, float v0, float v1) {
+    float v = old, f = 1.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int j = key0 + u * kTile;
+        if (!(bad >> u & 1u) && j < see.x && j + kTile > see.y) v = fmaxf(v, fabsf(u ? v1 : v0));
+    }
+    if (v > old) f = old / v;
+    *ref = make_float2(1.f / v, v);
+    return make_float2(v, f);
+}
 
 template <int HD, int TYPE, int NT>
 __global__ void __launch_bounds__(cta_warps(HD, NT) * 32, ctas_per_sm(HD, NT))
@@ -120,7 +147,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     unsigned char* ring = base + warp * NS * C::SLOT;
     unsigned char* after = base + W * NS * C::SLOT;
     unsigned char* q_sm = after;                                                         // [RT][QPITCH]
-    float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);                         // [warp][RT]
+    // [warp][RT]: at a piece's end (reference, sum of weights); before it (1 / v, v), v the V references of rows set apart
+    float2* state = reinterpret_cast<float2*>(q_sm + C::QBYTES);
     struct Entry { float ks[2], vs[2]; uint32_t bad, pad[3]; };                          // of a tile's 16-key halves
     unsigned char* misc = q_sm + C::QBYTES + C::STATE;
     Entry* meta = reinterpret_cast<Entry*>(misc) + warp * C::ENTRIES;
@@ -130,7 +158,6 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     Walk* cws = reinterpret_cast<Walk*>(misc + W * 64);                             // [2]
     Walk* pw = cws + 2 + warp;
     int* scan = reinterpret_cast<int*>(cws + 2 + W);                                // [32]
-    float* v_refs = reinterpret_cast<float*>(scan + 32);                                 // [warp]
     const uint32_t ring_u = smem_addr(ring), bars_u = smem_addr(bars);
 
     if (lane == 0) {
@@ -368,7 +395,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
 
         float o[MT][NT][4];
         float mref[NT][2], l[NT][2];
-        float vref = 0.f;                            // largest V scale so far
+        // 1 / largest V scale in the rows' views so far; of rows set apart (their own are in state[]), the largest of them
+        float vinv = 1.f / kVMin;
+        bool apart = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             mref[n][0] = mref[n][1] = kNoRef;
@@ -462,13 +491,51 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                             }
                     }
             }
-            const bool vup = E4 && vmax > vref;
+            // (somewhat above 1: a scale times its own rounded reciprocal)
+            const bool vup = E4 && vmax * vinv > 1.0001f;
             if (__any_sync(~0u, up) || vup) {
                 float va = 1.f;
                 if (vup) {
-                    const float v = fmaxf(vmax, 0x1p-120f);      // its reciprocal stays finite
-                    va = vref / v;
-                    vref = v;
+                    // One reference for all rows: where all see every key that is looked up, or where those
+                    // that do not see the step are at their end, and see none whose scale is far smaller
+                    const bool one_view = !edge || (min_lim == cw.s.n_kv && view[0].y == max_low);
+                    const bool at_end = max_low <= key0 &&
+                                        (SUB == 1 || key0 + kTile < min_lim || fabsf(vs[SUB - 1]) <= kVSlack * fabsf(vs[0])) &&
+                                        (vinv == 1.f / kVMin || vmax * vinv < 0x1p60f);
+                    if (__builtin_expect(!apart && (one_view || at_end), 1)) {
+                        const float inv = 1.f / vmax;
+                        va = inv / vinv;
+                        vinv = inv;
+                    } else {
+                        // a lane for a row: the largest scale of the steps that it sees
+                        // (lanes behind the last row do a row's work again)
+                        const int row = lane % RT;
+                        float2* ref = state + warp * RT + row;
+                        const float old = apart ? ref->y : 1.f / vinv;
+                        __syncwarp();
+                        const float2 raised = raise_v<SUB>(view[row], old, ref, key0, bad, vs[0], vs[SUB - 1]);
+                        // (not negative: ordered as their bits)
+                        const float v = raised.x, most = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(v))),
+                                    least = __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(v)));
+                        apart = most > kVSlack * least;
+                        vinv = 1.f / (apart ? least : most);
+                        const float vr = apart ? raised.y : raised.y * (v / most);
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+                            if (fabsf(vs[u]) > most) vs[u] = 0.f;        // nobody sees this step
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float f = __shfl_sync(~0u, vr, n * 8 + 2 * t4 + c);
+#pragma unroll
+                                for (int m = 0; m < MT; ++m) {
+                                    o[m][n][c] *= f;
+                                    o[m][n][2 + c] *= f;
+                                }
+                            }
+                        __syncwarp();                // (the references are read by all lanes)
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -487,7 +554,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         al[c] = ex2(mref[n][c] - m);
                         mref[n][c] = m;
                         l[n][c] *= al[c];
-                        al[c] *= va;
+                        if (E4) al[c] *= va;
 #pragma unroll
                         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -503,30 +570,44 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                     }
                 }
             }
-            if (E4) {
-                const float inv = vref > 0.f ? 1.f / vref : 0.f;
+            if (E4 && !apart) {
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) vs[u] *= inv;
+                for (int u = 0; u < SUB; ++u) vs[u] *= vinv;
             }
+            // Of rows set apart, step u's V scale over the row's reference: at most 1 in size where
+            // the row sees the step, and held to 1 where it does not, so that its zero weights stay zeros
+            auto v_share = [&](int u, int n, int c) {
+                return copysignf(__saturatef(fabsf(vs[u]) * state[warp * RT + n * 8 + 2 * t4 + c].x), vs[u]);
+            };
             uint32_t ph[SUB][NT][2], pl[SUB][NT][2];
+            auto weigh = [&](auto rows_apart) {
 #pragma unroll
-            for (int u = 0; u < SUB; ++u)
+                for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float w0 = ex2(y[u][n][2 * e]), w1 = ex2(y[u][n][2 * e + 1]);
-                        l[n][0] += w0;
-                        l[n][1] += w1;
-                        if (E4) {
-                            w0 *= vs[u];
-                            w1 *= vs[u];
+                    for (int n = 0; n < NT; ++n) {
+                        float f0 = vs[u], f1 = vs[u];
+                        if (decltype(rows_apart)::value) {
+                            f0 = v_share(u, n, 0);
+                            f1 = v_share(u, n, 1);
                         }
-                        const __half2 h = __floats2half2_rn(w0, w1);
-                        const float2 hf = __half22float2(h);
-                        ph[u][n][e] = movm(*reinterpret_cast<const uint32_t*>(&h));
-                        pl[u][n][e] = movm(pack_half2(w0 - hf.x, w1 - hf.y));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float w0 = ex2(y[u][n][2 * e]), w1 = ex2(y[u][n][2 * e + 1]);
+                            l[n][0] += w0;
+                            l[n][1] += w1;
+                            if (E4) {
+                                w0 *= f0;
+                                w1 *= f1;
+                            }
+                            const __half2 h = __floats2half2_rn(w0, w1);
+                            const float2 hf = __half22float2(h);
+                            ph[u][n][e] = movm(*reinterpret_cast<const uint32_t*>(&h));
+                            pl[u][n][e] = movm(pack_half2(w0 - hf.x, w1 - hf.y));
+                        }
                     }
+            };
+            if (E4 && __builtin_expect(apart, 0)) weigh(std::true_type());
+            else weigh(std::false_type());
 
             // ---- O^T += V^T P^T ------------------------------------------------
             wait_slot();
@@ -579,6 +660,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                                         x = e ? y[SUB - 1][n][2 + c] : y[SUB - 1][n][c];
                                         vsc = vs[SUB - 1];
                                     }
+                                    if (E4 && apart) vsc = SUB == 2 && u ? v_share(SUB - 1, n, c) : v_share(0, n, c);
                                     x = __shfl_sync(~0u, x, j * 4 + t4);
                                     if (x == -INFINITY) continue;
                                     const float w = ex2(x) * vsc;
@@ -643,7 +725,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             c_tile = (c_tile + 1) % C::ENTRIES;
         }
 
-        // ---- the piece's end: the four warps' states become one ---------------
+        // ---- the piece's end: the warps' states become one --------------------
         const bool had = tiles.x < tiles.y;          // a warp without a tile has no state, and holds no slot
         const int held = c_slot == 0 ? NS - 1 : c_slot - 1;
 #pragma unroll
@@ -655,9 +737,18 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 // no weight: no key seen. Only NaN scores: a state all the same, so that they reach the result
                 if (l[n][e] == 0.f) mref[n][e] = -INFINITY;
                 else if (mref[n][e] == kNoRef) mref[n][e] = 0.f;
-                if (g == 0) state[warp * RT + n * 8 + 2 * t4 + e] = make_float2(mref[n][e], l[n][e]);
+                float2* st = state + warp * RT + n * 8 + 2 * t4 + e;
+                if (E4) {                            // O without its V reference
+                    const float v = apart ? st->y : 1.f / vinv;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        o[m][n][e] *= v;
+                        o[m][n][2 + e] *= v;
+                    }
+                    if (apart) __syncwarp();
+                }
+                if (g == 0) *st = make_float2(mref[n][e], l[n][e]);
             }
-        if (E4 && lane == 0) v_refs[warp] = vref;
         // O^T as fp32 rows in the slot that the warp held back, in chunks of CNT
         // row blocks; dims of a row are moved by its number against bank conflicts
         auto o_at = [](int r, int d) { return r * HD + (d ^ ((r >> 1 & 3) << 3)); };
@@ -689,9 +780,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 for (int v = 0; v < W; ++v) {
                     const float2 st = state[v * RT + r];
                     if (st.x == -INFINITY) continue;             // no key seen, or no tile
-                    float f = ex2(st.x - m);
+                    const float f = ex2(st.x - m);
                     lsum += st.y * f;
-                    if (E4) f *= v_refs[v];
                     const float* src = reinterpret_cast<const float* const*>(scan)[v];
                     const float4 y = *reinterpret_cast<const float4*>(src + o_at(rr, d));
                     x.x += f * y.x;

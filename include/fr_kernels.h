@@ -442,7 +442,8 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  * Few query rows a sequence (decode, speculative tokens) take row tiles of 8 to
  * 32 rows, each of which reads the keys; many rows (prompts) take tiles of 128.
  * A weight enters the PV product within 2^-22 of itself, or 2^-32 of its row's
- * largest (e4m3: each times its V scale, against the largest V scale in view).
+ * largest (e4m3: each times its V scale, against the largest V scale in the row's
+ * view; 2^-24 where other rows see scales of up to 256 times that).
  * It does so as two terms: infinite values of V in a row's view make the element
  * infinite or NaN.
  * The result does not depend on timing: same inputs, same bits.
