@@ -50,7 +50,10 @@ using namespace sm100;
 
 // Weights are 2^(x - mref): a row's reference mref is 7 below its maximum when
 // set, and moves when a score exceeds it by 15, so weights reach 2^15 at most in
-// f16 and P_lo stays off f16's subnormals for all weights that matter.
+// f16 and P_lo stays off f16's subnormals for all weights that matter. x is the
+// rounded product of score and factor wherever it is used: in one FMA with the
+// subtraction it would be off the maximum's x by up to half its last place,
+// more than 15 from 2^28 on, and equal scores would differ.
 constexpr float kBelow = 7.0f, kAbove = 15.0f;
 constexpr float kNoRef = -3.402823466e38f;           // a row without a key so far
 constexpr float kVMin = 0x1p-120f;                   // a V reference at least: its reciprocal stays finite
@@ -461,6 +464,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             pass_slot(false);
 
             // ---- softmax weights: exponents x - mref first -------------------
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][n][e] = __fmul_rn(s[u][n][e], sc[u]);
             const int key0 = (tile0 + t) * KT;
             const bool edge = bad != 0u || key0 + KT > min_lim || key0 < max_low;
             bool up = false;
@@ -471,7 +480,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        y[u][n][e] = fmaf(s[u][n][e], sc[u], -mref[n][e & 1]);
+                        y[u][n][e] = __fsub_rn(s[u][n][e], mref[n][e & 1]);
                         up |= y[u][n][e] > kAbove;
                     }
             if (__builtin_expect(edge, 0)) {
@@ -547,7 +556,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         for (int u = 0; u < SUB; ++u)
 #pragma unroll
                             for (int e = c; e < 4; e += 2)
-                                m = fmaxf(m, y[u][n][e] == -INFINITY ? -INFINITY : s[u][n][e] * sc[u]);
+                                m = fmaxf(m, y[u][n][e] == -INFINITY ? -INFINITY : s[u][n][e]);
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
                         m = fmaxf(m - kBelow, mref[n][c]);
@@ -559,7 +568,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         for (int u = 0; u < SUB; ++u)
 #pragma unroll
                             for (int e = c; e < 4; e += 2)
-                                y[u][n][e] = y[u][n][e] == -INFINITY ? -INFINITY : fmaf(s[u][n][e], sc[u], -m);
+                                y[u][n][e] = y[u][n][e] == -INFINITY ? -INFINITY : __fsub_rn(s[u][n][e], m);
                     }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {

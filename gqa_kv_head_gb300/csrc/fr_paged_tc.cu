@@ -47,7 +47,9 @@ using namespace sm100;
 
 constexpr int kBN = 64;                      // keys of a tile
 constexpr int kSmax = 256, kProd = 8, kMma = 9, kConv = 10, kConvThreads = 128;   // softmax threads; warps
-constexpr float kTau = 8.0f;
+// Weights are 2^(x - reference): a row's reference is 7 below its maximum when set,
+// and moves when a score exceeds it by 15 (P_lo off f16's subnormals, P_hi within f16).
+constexpr float kBelow = 7.0f, kAbove = 15.0f;
 constexpr uint64_t kLimit = 2000000000ull;
 
 template <int HD, bool E4>
@@ -429,7 +431,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     tmem_ld_x32(tbase + lanes + C::T_S + (n & 1) * kBN + c_base, reinterpret_cast<uint32_t*>(x));
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < HB; ++c) x[c] *= E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2;
+                    for (int c = 0; c < HB; ++c) x[c] = __fmul_rn(x[c], E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2);
                     if (edge) {
 #pragma unroll
                         for (int c = 0; c < HB; ++c) {
@@ -447,7 +449,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 asm volatile("bar.sync %0, 64;" :: "r"(qd + 1) : "memory");          // the row's two halves
                 const float mx = fmaxf(pm, s_max[((n & 1) * 2 + (half ^ 1)) * 128 + r]);
                 float m_new = m_ref;
-                if (mx > m_ref + kTau || (m_ref == -INFINITY && mx > -INFINITY)) m_new = fmaxf(mx, m_ref);
+                if (mx - m_ref > kAbove) m_new = fmaxf(mx - kBelow, m_ref);              // (m_ref = -inf: any score)
                 const bool grown = m_ref != -INFINITY && m_new != m_ref;
                 const float alpha = grown ? ex2(m_ref - m_new) : 1.f;
                 // V's scales join the weights relative to the largest that the row has met
@@ -479,13 +481,12 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                         }
                         tmem_wait_st();
                     }
-                    // weights times 2^7: P_lo off f16's subnormals (they reach 2^15 before the reference moves)
-                    const float sub = (m_new == -INFINITY ? 0.f : m_new) - 7.f;
+                    const float sub = m_new == -INFINITY ? 0.f : m_new;
                     float s4[4] = {0.f, 0.f, 0.f, 0.f};
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int c = 0; c < HB; c += 2) {
-                        float p0 = ex2(x[c] - sub), p1 = ex2(x[c + 1] - sub);
+                        float p0 = ex2(__fsub_rn(x[c], sub)), p1 = ex2(__fsub_rn(x[c + 1], sub));
                         s4[(c >> 1) & 3] += p0 + p1;
                         if (E4) {
                             p0 *= v_step[c / 16];
@@ -576,8 +577,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                                 float x = 0.f;
                                 for (int d = 0; d < HD; ++d) x = fmaf(__half2float(q[d]), page_value<E4>(pg.k, k + d), x);
                                 const int64_t sc = (int64_t)page * a.n_kv_head + s.h;
-                                const float x_log2 = x * (E4 ? a.scale_log2 * a.k_scale[sc] : a.scale_log2);
-                                const float p = ex2(x_log2 - (m_out - 7.f)) *
+                                const float x_log2 = __fmul_rn(x, E4 ? a.scale_log2 * a.k_scale[sc] : a.scale_log2);
+                                const float p = ex2(__fsub_rn(x_log2, m_out)) *
                                                 (E4 ? (v_ref > 0.f ? a.v_scale[sc] * (1.f / v_ref) : 0.f) : 1.f);
 #pragma unroll
                                 for (int u = 0; u < 32; ++u) o[u] = fmaf(p, page_value<E4>(pg.v, v + half * OH + c + u), o[u]);
