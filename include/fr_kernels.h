@@ -446,6 +446,9 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  * view; 2^-24 where other rows see scales of up to 256 times that).
  * It does so as two terms: infinite values of V in a row's view make the element
  * infinite or NaN.
+ * Scores (times log2 e) and sums of weights times values, each weight up to 2^15,
+ * are held in fp32: beyond its range, which e4m3 pages can reach with scales whose
+ * values pass 2^80, they are infinite, and the result is infinite or NaN.
  * The result does not depend on timing: same inputs, same bits.
  */
 fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
