@@ -188,6 +188,23 @@ __device__ __noinline__ int2 request_next(Walk* w, const AttnArgs* a, int warp) 
 struct Share {
     int u0, units, total, n_cta;
 };
+// Do the sequences have more tokens than the step has rows? (Only ranges that are not in
+// order can: the backward ones among them are skipped, the others overlap.) Called by
+// the whole block. Their units may then be more than an int counts.
+template <int NTH>
+__device__ __noinline__ bool ranges_overlap(const AttnArgs* a, int* scan) {
+    const int tid = threadIdx.x, most = a->n_tok + 1;              // (enough to tell, and 1024 of them fit)
+    int n = 0;
+    for (int b = tid; b < a->n_seq; b += NTH)
+        n = min(n + seq_info(a->tok_start, a->kv_len, b, a->n_tok, a->max_pages, a->page_shift).n_q, most);
+    n = __reduce_add_sync(~0u, n);
+    __syncthreads();                                               // (scan[] has been read)
+    if ((tid & 31) == 0) scan[tid >> 5] = n;
+    __syncthreads();
+    int64_t sum = 0;
+    for (int w = 0; w < NTH / 32; ++w) sum += scan[w];
+    return sum > a->n_tok;
+}
 // The share of CTA `cta`, and the walk's first piece in cws[0] (more = 0: none),
 // which a barrier of the block has yet to publish. scan: 4 * NTH / 32 words.
 template <class P, int NTH>
@@ -198,8 +215,8 @@ __device__ __forceinline__ Share first_walk(const AttnArgs& a, int cta, int* sca
     Share sh{0, 0, 0, 0};
     Seg seq;
     int per_head = 0, u_b = 0, s_b = 0, more_u = 0, more_s = 0;   // of this thread's sequence; of those behind
+    bool bad_any = false;
     {
-        bool bad_any = false;
         seq.n_rt = 0;
         if (tid < a.n_seq) bad_any = seg_seq<P>(seq, a, tid);
         per_head = seq_units<P>(a, seq);
@@ -227,28 +244,36 @@ __device__ __forceinline__ Share first_walk(const AttnArgs& a, int cta, int* sca
     int inc = u_b, inc_s = s_b;
     scan_warp(inc, inc_s);
     if (a.n_seq > NTH) scan_warp(more_u, more_s);
+    // (segments have two units and more each, so that their counts leave a bit for bad input)
+    const int bad_bit = __any_sync(~0u, bad_any) ? 1 << 30 : 0;
     if (lane == 31) {
         scan[warp] = inc;
-        scan[NW + warp] = inc_s;
+        scan[NW + warp] = (inc_s & ((1 << 30) - 1)) | bad_bit;
         scan[2 * NW + warp] = more_u;
         scan[3 * NW + warp] = more_s;
     }
     if (tid == 0) cws[0].more = 0;
     __syncthreads();
-    int base_u = 0, base_s = 0, total = 0, segs = 0;
+    int base_u = 0, base_s = 0, total = 0, segs = 0, some_bad = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
+        const int n = scan[NW + w] & ((1 << 30) - 1);
+        some_bad |= scan[NW + w];
         if (w < warp) {
             inc += scan[w];
-            inc_s += scan[NW + w];
+            inc_s += n;
         }
         base_u += scan[w];
-        base_s += scan[NW + w];
+        base_s += n;
         total += scan[2 * NW + w];
         segs += scan[3 * NW + w];
     }
-    total += base_u;             // (the host refuses batches whose units could pass 31 bits)
+    total += base_u;             // (the host refuses batches whose ranges in order could pass 31 bits)
     segs += base_s;
+    if (__builtin_expect(some_bad >> 30, 0) && ranges_overlap<NTH>(&a, scan)) {
+        if (cta == 0 && tid == 0) *a.n_split = 0;
+        return sh;
+    }
     const int n_cta = min((int)gridDim.x, total);
     if (cta == 0 && tid == 0)    // entries of split[] that this call writes
         *a.n_split = a.split_by_segment ? min(kMaxCtas, segs) : n_cta;

@@ -389,8 +389,9 @@ fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const int64_t* k_
  * Sequences may share pages that no call writes. The arrays are read on the
  * device by every call. A sequence whose numbers do not fit (tokens outside
  * 0..n_tok, kv_len outside 0..max_pages*page_size, or fewer keys than new
- * tokens in an append) is skipped; keys of a page outside 0..n_pages-1 are
- * treated as masked, and rows for it are not written. Both set the status word
+ * tokens in an append) is skipped, and an attention whose ranges have more
+ * tokens than n_tok does nothing; keys of a page outside 0..n_pages-1 are
+ * treated as masked, and rows for it are not written. Each sets the status word
  * that fr_workspace_check reports as FR_ERR_DEVICE_INPUT.
  */
 fr_status fr_paged_batch_init(fr_paged_batch* batch, const int32_t* tok_start, const int32_t* kv_len,
