@@ -120,7 +120,21 @@ struct Cfg {
     static_assert(CNT >= 1 && NT % CNT == 0, "epilogue chunk");
 };
 
-static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, uint64_t ns) { return mbar_wait(bar, phase, ns); }
+// Waits for a slot of a warp's ring of n, in its phase. One that gives up waits, again with
+// a limit, for the copies that are in flight behind it: the warp asks for no more, and the CTA
+// must not end before they have landed.
+static __device__ __noinline__ bool wait_long(uint32_t bars, int slot, uint32_t phase, int n) {
+    if (mbar_wait(bars + 8 * slot, phase, kWaitNs)) return true;
+    uint64_t limit = kWaitNs;
+    for (int i = 0; i < n; ++i) {
+        if (!mbar_wait(bars + 8 * slot, phase, limit)) limit = 20000ull;
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    return false;
+}
 
 // A lane for a row: the row's V reference, raised to the largest scale of the steps of
 // a tile (first key key0, U steps) that it sees, and what its O is to be scaled by.
@@ -239,7 +253,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     int b_page = -1, p_page[SUB] = {};
     float b_ks = 0.f, b_vs = 0.f;
     int i_slot = 0, i_tile = 0;  // ring slot of the next request; its tile's number mod ENTRIES
-    bool i_v = false, fresh = false, b_has = false;
+    bool i_v = false, fresh = false, b_has = false, timeout = false;
     // Page numbers of the warp's next 32 16-key steps, one a lane; -1: none. Asked
     // for one request ahead of their use.
     auto load_pages = [&]() {
@@ -269,7 +283,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             }
             if (lane == 0) meta[i_tile].bad = bad;
         }
-        if (lane == 0) {
+        if (lane == 0 && !timeout) {
             const uint32_t bar = bars_u + 8 * i_slot;
             const int key = (pw->s.tile0 + pt.x) * KT, in_page = (1 << a.page_shift) - 1, head = pw->s.h;
             mbar_expect_tx(bar, C::SLOT);
@@ -320,11 +334,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
 
     int c_slot = 0, c_tile = 0;
     uint32_t c_phase = 0;
-    bool timeout = false;
     auto wait_slot = [&]() {
         if (mbar_test(bars_u + 8 * c_slot, c_phase)) return;
-        // after one wait that gave up the others do so soon: the kernel ends
-        if (!wait_long(bars_u + 8 * c_slot, c_phase, timeout ? 20000ull : kWaitNs)) timeout = true;
+        // after one wait that gave up there is nothing to wait for: the kernel ends
+        if (!timeout && !wait_long(bars_u, c_slot, c_phase, NS)) timeout = true;
     };
     auto pass_slot = [&](bool hold) {    // this slot is used up: request what comes NS slots later, unless it is held
         __syncwarp();
