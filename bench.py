@@ -128,14 +128,14 @@ def _strip_comments(src):
 
 
 def kernel_source_hash():
-    """Hash of the kernel sources' code (comments excluded, whitespace runs as
-    one space): the traffic figures of a committed ncu summary hold while it
-    is unchanged."""
+    """Hash of the decode-attention kernels' code (comments excluded, whitespace
+    runs as one space): the traffic figures of a committed ncu summary hold
+    while it is unchanged. The paged cache's files are other kernels."""
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "gqa_kv_head_gb300", "csrc")
     for fn in sorted(os.listdir(csrc)):
-        if fn.endswith((".cu", ".cuh")):
+        if fn.endswith((".cu", ".cuh")) and not fn.startswith("fr_paged"):
             code = _strip_comments(open(os.path.join(csrc, fn), encoding="utf-8").read())
             h.update(" ".join(code.split()).encode())          # whitespace runs as one space
     return h.hexdigest()[:16]
