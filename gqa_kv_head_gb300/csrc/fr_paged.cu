@@ -4,8 +4,6 @@
 #include <math.h>
 #include <string.h>
 
-#include <cudaTypedefs.h>
-
 #include "fr_paged.h"
 #include "fr_sm100.cuh"
 
@@ -108,20 +106,6 @@ paged_merge_kernel(const Split* __restrict__ split, const int* __restrict__ n_sp
 }
 
 // ---- descriptors ---------------------------------------------------------------
-
-static PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        else
-            (void)cudaGetLastError();
-    }
-    return fn;
-}
 
 // Strides of a [n_pages][n_kv_head][page_size][hd] view: 16-byte multiples, and
 // no two elements at one address (an expanded view would be written twice).

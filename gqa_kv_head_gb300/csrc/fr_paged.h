@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -114,6 +115,21 @@ fr_status launch_attn_f16(const KvDesc& kv, const AttnArgs& a, int row_tiles8, i
 // either type, row tiles of up to 128 rows (a.row_tile: whole tokens)
 fr_status launch_attn_tc(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st);
 fr_status launch_attn_e4m3(const KvDesc& kv, const AttnArgs& a, int row_tiles8, int ctas, cudaStream_t st);
+// The driver's encoder of TMA descriptors (null: not found). Any thread may come first.
+inline PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
+    static void* fn = nullptr;
+    void* p = __atomic_load_n(&fn, __ATOMIC_ACQUIRE);
+    if (!p) {
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            return nullptr;
+        }
+        __atomic_store_n(&fn, p, __ATOMIC_RELEASE);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+}
 // Pointer checks shared by the entry points.
 inline const KvDesc* kv_desc(const fr_paged_kv* p) {
     const KvDesc* d = reinterpret_cast<const KvDesc*>(p);

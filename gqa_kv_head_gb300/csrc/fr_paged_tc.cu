@@ -35,8 +35,6 @@
 // (144 and 112) spilled more and took 657.
 #include <string.h>
 
-#include <cudaTypedefs.h>
-
 #include "fr_paged_work.cuh"
 
 namespace fr {
@@ -609,18 +607,6 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     __syncwarp();
     __syncthreads();
     if (warp == kMma) tmem_dealloc(tbase, 512);
-}
-
-static PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        cudaDriverEntryPointQueryResult q;
-        void* p = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
 }
 
 template <int HD, bool E4>
