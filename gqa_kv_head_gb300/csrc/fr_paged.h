@@ -26,7 +26,7 @@ __host__ __device__ constexpr bool many_warps(int hd, int nt) { return nt <= 2 &
 __host__ __device__ constexpr int cta_warps(int hd, int nt) { return many_warps(hd, nt) ? 4 : 8; }
 __host__ __device__ constexpr int ctas_per_sm(int hd, int nt) { return many_warps(hd, nt) ? 3 : 1; }
 __host__ __device__ constexpr int cta_smem(int hd, int nt) { return many_warps(hd, nt) ? 65536 : 212992; }
-constexpr int kMaxCtas = 640;        // attention CTAs at most: the workspace holds two split states for each
+constexpr int kMaxCtas = 640;        // entries of split[], and more than the attention CTAs of any launch (two split states each)
 constexpr int kMaxSeq = 65536;
 constexpr int kSegCost = 2;          // units that a segment's start and end count for in the work split
 constexpr int kTcSegCost = 4;        // the same for the 128-row kernel (four prompts of 2048, 2 / 4 / 6 / 9: 368 / 347 / 356 / 375 us)

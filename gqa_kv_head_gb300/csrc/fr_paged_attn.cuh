@@ -18,15 +18,16 @@
 // synchronises the CTA on every tile.
 //
 // Work split: the keys of all (sequence, KV head, row tile) segments form one
-// list of 64-key units; each CTA (one to three per SM) takes an equal contiguous share
-// of it, read from kv_len on the device, so uneven lengths balance and a
-// captured graph follows the lengths. A segment inside one CTA is normalised
+// list of units (a tile for each warp of a CTA, 64 to 256 keys); each CTA (one to
+// three per SM) takes an equal contiguous share of it, read from kv_len on the
+// device, so uneven lengths balance and a captured graph follows the lengths. A
+// segment inside one CTA is normalised
 // and written there; one cut by a share's end leaves (m, l, O) states in the
 // workspace for the merge kernel (fr_paged.cu).
 //
-// P enters the PV product as two f16 terms P_hi + P_lo (22 bits), held
-// between 2^7 and 2^15 at the maximum to keep P_lo off f16's subnormals: the result carries fp32 accuracy like
-// fr_decode_attn's. e4m3 codes become f16 in registers, which is exact; K's
+// P enters the PV product as two f16 terms P_hi + P_lo (22 bits), held between
+// 2^7 and 2^15 at the maximum to keep P_lo off f16's subnormals: the result
+// carries fp32 accuracy like fr_decode_attn's. e4m3 codes become f16 in registers, which is exact; K's
 // scale joins the score's factor, V's scale the weights, relative to the
 // largest V scale that the row has met in its view (a running reference beside
 // m). It is one number a warp where the rows have met about the same; tiles at
@@ -91,7 +92,6 @@ struct Cfg {
     static constexpr int MT = HD / 16;                      // 16-dim blocks of O^T, and k steps of S^T
     static constexpr int W = cta_warps(HD, NT);
     static constexpr int LIMIT = cta_smem(HD, NT);          // shared memory of one CTA
-    // Q fragments stay in registers up to 64 of them beside O's; beyond, in shared memory
     // Q rows lie in shared memory; the fragments stay in registers for a piece
     // where these allow (hd 128 with 16 rows reads them again for each tile: 63 ->
     // 59 us at 131072 keys of e4m3, the registers went to a third CTA)

@@ -88,7 +88,7 @@ struct Meta {                                                // a tile's 16-key 
 struct Pages {                                               // the cache as plain memory (rare rows are read there)
     const void *k, *v;
     int64_t k_page, k_head, k_row, v_page, v_head, v_row;
-    int box_rows;                                            // rows of a K or V box: min(page, 64)
+    int box_rows;                                            // rows of a K or V box (tc_box_rows)
     int tok_tile;                                            // tokens of a row tile
 };
 
@@ -104,9 +104,10 @@ __device__ __forceinline__ void load_q(uint32_t dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(dst), "l"((uint64_t)map), "r"(dim), "r"(head), "r"(tok), "r"(bar) : "memory");
 }
+// Does a pair of f16 hold an infinity or NaN?
 __device__ __forceinline__ bool odd_half2(uint32_t x) { return (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u; }
 
-// Element i of a page row, and whether its pair holds an infinity or NaN.
+// Element i of a page.
 template <bool E4>
 __device__ __forceinline__ float page_value(const void* p, int64_t i) {
     if (!E4) return __half2float(reinterpret_cast<const __half*>(p)[i]);
