@@ -160,10 +160,13 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
 // Average query rows of a sequence and KV head from which the 128-row kernel is
 // taken: where the small tiles would read the keys twice, at hd 256 in e4m3 four
 // times. Small tiles and one of 128, us, 64 sequences of 1..8000 keys, 4 KV heads:
-//   f16   hd 128, 36 rows 194 and 147; hd 256, 20 rows 329 and 204, 36 rows 489 and 207
-//   e4m3  hd 128, 36 rows 236 and 240, 64 rows 264 and 243; hd 256, 36 rows 288 and
-//         328, 64 rows 390 and 331
-// and 65536 keys, 8 KV heads, hd 128, 32 rows: f16 63 and 80, e4m3 68 and 105. Two
+//   f16   hd 64, 32 rows 85 and 115, 36 rows 135 and 133, 64 rows 148 and 135; hd 128, 32
+//         rows 125 and 130, 36 rows 196 and 148; hd 256, 16 rows 174 and 202, 20 rows 327
+//         and 203, 36 rows 480 and 207
+//   e4m3  hd 64, 32 rows 104 and 172, 36 rows 168 and 169, 64 rows 183 and 171; hd 128, 36
+//         rows 247 and 240, 64 rows 279 and 242; hd 256, 36 rows 294 and 326, 52 rows 382
+//         and 329, 64 rows 393 and 331
+// and 65536 keys, 8 KV heads, hd 128, 32 rows: f16 62 and 71, e4m3 68 and 102. Two
 // tiles of 16 rows over few long segments run side by side and meet in L2: hd 256,
 // 32 rows, 65536 keys of 1, 2, 4 heads 27 and 30, 37 and 43, 59 and 64; 16 x 8000
 // keys 29 and 32; 64 x 2000 keys 39 and 37.

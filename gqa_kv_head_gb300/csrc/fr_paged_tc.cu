@@ -25,8 +25,8 @@
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
 //
-// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.96 ms,
-// 540 TFLOP/s (P_lo counted: 810). Four prompts of 2048: 347 us in f16 and 631 us
+// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.97 ms,
+// 540 TFLOP/s (P_lo counted: 810). Four prompts of 2048: 350 us in f16 and 629 us
 // in e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 1.1 us in f16, a
 // chain of S, softmax and PV in which none of the units is busy for more than a
 // third; three S tiles in TMEM in place of two were 3-6 % slower up to hd 128.
