@@ -393,6 +393,7 @@ fr_status fr_paged_kv_init(fr_paged_kv* kv, int type, void* k, const int64_t* k_
  * tokens than n_tok does nothing; keys of a page outside 0..n_pages-1 are
  * treated as masked, and rows for it are not written. Each sets the status word
  * that fr_workspace_check reports as FR_ERR_DEVICE_INPUT.
+ * Supported: n_seq <= 65536, 1 <= n_tok <= 2^20, max_pages <= 2^22.
  */
 fr_status fr_paged_batch_init(fr_paged_batch* batch, const int32_t* tok_start, const int32_t* kv_len,
                               const int32_t* page_table, int64_t page_table_stride, int n_seq, int n_tok,
@@ -451,6 +452,8 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  * are held in fp32: beyond its range, which e4m3 pages can reach with scales whose
  * values pass 2^80, they are infinite, and the result is infinite or NaN.
  * The result does not depend on timing: same inputs, same bits.
+ * Supported: n_head <= 65536, and fewer than 2^31 units of work (64 keys of a row
+ * tile each) in the largest batch of these sizes.
  */
 fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
                         int64_t q_tok_stride, int n_head, int causal, int window, float kq_scale, float* out,
