@@ -279,9 +279,17 @@ extern "C" size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd
     return ws_bytes(hd);
 }
 
-extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch* batch_, const uint16_t* q16,
+extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
                                    int64_t q_tok_stride, int n_head, int causal, int window, float kq_scale, float* out,
                                    void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    return fr_paged_attn_sinks(kv, batch, q16, q_tok_stride, n_head, causal, window, 0, kq_scale, out, workspace,
+                               workspace_bytes, stream);
+}
+
+extern "C" fr_status fr_paged_attn_sinks(const fr_paged_kv* kv_, const fr_paged_batch* batch_, const uint16_t* q16,
+                                         int64_t q_tok_stride, int n_head, int causal, int window, int n_sink,
+                                         float kq_scale, float* out, void* workspace, size_t workspace_bytes,
+                                         cudaStream_t stream) {
     const KvDesc* kv = kv_desc(kv_);
     const BatchDesc* bt = batch_desc(batch_);
     if (!kv || !bt || !q16 || !out || !workspace) return FR_ERR_INVALID_ARG;
@@ -290,6 +298,7 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     if (q_tok_stride < (int64_t)n_head * kv->hd || (q_tok_stride & 7)) return FR_ERR_INVALID_ARG;
     const float scale_log2 = (float)((double)kq_scale * 1.4426950408889634);
     if (window < 0 || (window > 0 && !causal) || !isfinite(scale_log2)) return FR_ERR_INVALID_ARG;
+    if (n_sink < 0 || (n_sink > 0 && window == 0)) return FR_ERR_INVALID_ARG;
     if (!aligned16(q16) || !aligned16(out) || !aligned16(workspace)) return FR_ERR_INVALID_ARG;
     if (((int64_t)bt->max_pages << kv->page_shift) > 0x7fff0000) return FR_ERR_UNSUPPORTED;
     if (workspace_bytes < ws_bytes(kv->hd)) return FR_ERR_WORKSPACE;
@@ -345,7 +354,9 @@ extern "C" fr_status fr_paged_attn(const fr_paged_kv* kv_, const fr_paged_batch*
     a.row_tile = rt;
     a.causal = causal ? 1 : 0;
     // a window that no sequence outgrows is none (and positions less it stay in 32 bits)
-    a.window = window >= ((int64_t)bt->max_pages << kv->page_shift) ? 0 : window;
+    const int64_t most_keys = (int64_t)bt->max_pages << kv->page_shift;
+    a.window = window >= most_keys ? 0 : window;
+    a.sink = a.window == 0 ? 0 : n_sink < most_keys ? n_sink : (int)most_keys;
     a.split_by_segment = segs <= ctas ? 1 : 0;
     a.scale_log2 = scale_log2;
     const fr_status st = many                     ? launch_attn_tc(*kv, a, (int)ctas, stream)

@@ -83,6 +83,7 @@ struct AttnArgs {
     int* n_split;                    // entries of it that the call wrote
     unsigned* status;
     int n_seq, n_tok, max_pages, n_pages, page_shift, n_kv_head, group, causal, window;
+    int sink;                        // with a window: keys 0 .. sink - 1 stay visible
     int row_tile;                    // rows of a row tile where the kernel does not fix them
     unsigned group_magic;            // ceil(2^32 / group) where a multiplication by it divides rows exactly, else 0
     int split_by_segment;            // split[] is indexed by the segment's number, else by its first CTA

@@ -138,26 +138,27 @@ static __device__ __noinline__ bool wait_long(uint32_t bars, int slot, uint32_t 
 
 // A lane for a row: the row's V reference, raised to the largest scale of the steps of
 // a tile (first key key0, U steps) that it sees, and what its O is to be scaled by.
-template <int U>
-static __device__ __noinline__ float2 raise_v(int2 see, float old, float2* ref, int key0, uint32_t bad, float v0, float v1) {
+template <int U, bool SINK>
+static __device__ __noinline__ float2 raise_v(int2 see, int sink, float old, float2* ref, int key0, uint32_t bad, float v0,
+                                              float v1) {
     float v = old, f = 1.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int j = key0 + u * kTile;
-        if (!(bad >> u & 1u) && j < see.x && j + kTile > see.y) v = fmaxf(v, fabsf(u ? v1 : v0));
+        if (!(bad >> u & 1u) && j < see.x && (j + kTile > see.y || (SINK && j < sink))) v = fmaxf(v, fabsf(u ? v1 : v0));
     }
     if (v > old) f = old / v;
     *ref = make_float2(1.f / v, v);
     return make_float2(v, f);
 }
 
-template <int HD, int TYPE, int NT>
+template <int HD, int TYPE, int NT, bool SINK>
 __global__ void __launch_bounds__(cta_warps(HD, NT) * 32, ctas_per_sm(HD, NT))
 paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using C = Cfg<HD, TYPE, NT>;
     constexpr int W = C::W, RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
     constexpr bool E4 = C::E4;
-    using P = Units<RT, KT, W, kSegCost>;
+    using P = Units<RT, KT, W, kSegCost, SINK>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -258,9 +259,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     // for one request ahead of their use.
     auto load_pages = [&]() {
         blk = 0;
-        const int tl = pt.x + lane / SUB * W, key = (pw->s.tile0 + tl) * KT + lane % SUB * kTile;
+        const int tl = pt.x + lane / SUB * W, key = tile_key<P>(pw->s, tl, sink_tiles<P>(pw->s, a)) + lane % SUB * kTile;
         // (16 keys that no row sees: their page may be gone)
-        b_has = tl < pt.y && key < pw->s.n_kv && key + kTile > pw->s.lo;
+        b_has = tl < pt.y && key < pw->s.n_kv && (key + kTile > pw->s.lo || P::is_sink(key, a));
         b_page = -1;
         if (b_has) b_page = __ldcg(a.table + pw->s.b * a.table_stride + (key >> a.page_shift));
         fresh = true;
@@ -285,7 +286,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         }
         if (lane == 0 && !timeout) {
             const uint32_t bar = bars_u + 8 * i_slot;
-            const int key = (pw->s.tile0 + pt.x) * KT, in_page = (1 << a.page_shift) - 1, head = pw->s.h;
+            const int key = tile_key<P>(pw->s, pt.x, sink_tiles<P>(pw->s, a)), in_page = (1 << a.page_shift) - 1, head = pw->s.h;
             mbar_expect_tx(bar, C::SLOT);
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
@@ -423,7 +424,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
         }
 
         const int2 tiles = walk_tiles<P>(cw, warp);
-        const int tile0 = cw.s.tile0;
+        const int first_tiles = sink_tiles<P>(cw.s, a), tile0 = cw.s.tile0 - first_tiles;
         for (int t = tiles.x; t < tiles.y; t += W) {
             // ---- S^T = K Q^T ------------------------------------------------
             wait_slot();
@@ -483,8 +484,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[u][n][e] = __fmul_rn(s[u][n][e], sc[u]);
-            const int key0 = (tile0 + t) * KT;
-            const bool edge = bad != 0u || key0 + KT > min_lim || key0 < max_low;
+            const int key0 = SINK && t < first_tiles ? t * KT : (tile0 + t) * KT;
+            const bool edge = bad != 0u || key0 + KT > min_lim || (key0 < max_low && P::hidden(key0 + KT - 1, a));
             bool up = false;
             float y[SUB][NT][4];
 #pragma unroll
@@ -508,7 +509,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
 #pragma unroll
                             for (int e = c; e < 4; e += 2) {
                                 const int j = key0 + u * kTile + g + (e >> 1) * 8;
-                                if ((bad >> u & 1u) || j >= see.x || j < see.y) y[u][n][e] = -INFINITY;
+                                if ((bad >> u & 1u) || j >= see.x || (j < see.y && P::hidden(j, a))) y[u][n][e] = -INFINITY;
                                 up |= y[u][n][e] > kAbove;
                             }
                     }
@@ -518,9 +519,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
             if (__any_sync(~0u, up) || vup) {
                 float va = 1.f;
                 if (vup) {
-                    // One reference for all rows: where all see every key that is looked up, or where those
-                    // that do not see the step are at their end, and see none whose scale is far smaller
-                    const bool one_view = !edge || (min_lim == cw.s.n_kv && view[0].y == max_low);
+                    // One reference for all rows: where all see every key that is looked up (of a tile ahead of
+                    // all windows those before the sinks' end), or where those that do not see the step are at
+                    // their end, and see none whose scale is far smaller
+                    const bool one_view = !edge || (min_lim == cw.s.n_kv && view[0].y == max_low) ||
+                                          (SINK && key0 + KT <= view[0].y);
                     const bool at_end = max_low <= key0 &&
                                         (SUB == 1 || key0 + kTile < min_lim || fabsf(vs[SUB - 1]) <= kVSlack * fabsf(vs[0])) &&
                                         (vinv == 1.f / kVMin || vmax * vinv < 0x1p60f);
@@ -535,7 +538,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         float2* ref = state + warp * RT + row;
                         const float old = apart ? ref->y : 1.f / vinv;
                         __syncwarp();
-                        const float2 raised = raise_v<SUB>(view[row], old, ref, key0, bad, vs[0], vs[SUB - 1]);
+                        const float2 raised = raise_v<SUB, SINK>(view[row], a.sink, old, ref, key0, bad, vs[0], vs[SUB - 1]);
                         // (not negative: ordered as their bits)
                         const float v = raised.x, most = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(v))),
                                     least = __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(v)));
@@ -646,7 +649,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                         bool vis = false, msk = false;
                         for (int r = 2 * t4; r < rows; r += (r & 1) ? 7 : 1) {
                             const int2 see = view[r];
-                            const bool m = no_page || j0 + g >= see.x || j0 + g < see.y;
+                            const bool m = no_page || j0 + g >= see.x || (j0 + g < see.y && P::hidden(j0 + g, a));
                             vis |= !m;
                             msk |= m;
                         }
@@ -836,12 +839,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
 }
 
 // Programmatic launch: set-up overlaps the kernel before it on the stream.
-template <int HD, int TYPE, int NT>
+template <int HD, int TYPE, int NT, bool SINK>
 static fr_status launch_one(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
     using C = Cfg<HD, TYPE, NT>;
     static unsigned long long done = 0ull;           // devices whose shared-memory limit is raised
     if (kv.dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> kv.dev & 1ull)) {
-        if (cudaFuncSetAttribute(paged_attn_kernel<HD, TYPE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(paged_attn_kernel<HD, TYPE, NT, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::SMEM) != cudaSuccess)
             return FR_ERR_CUDA;
         if (kv.dev < 64) __atomic_fetch_or(&done, 1ull << kv.dev, __ATOMIC_RELEASE);
@@ -860,18 +863,22 @@ static fr_status launch_one(const KvDesc& kv, const AttnArgs& a, int ctas, cudaS
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<HD, TYPE, NT>, a, km, vm) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<HD, TYPE, NT, SINK>, a, km, vm) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }
 
+template <int TYPE, bool SINK>
+static fr_status launch_hd(const KvDesc& kv, const AttnArgs& a, int nt, int ctas, cudaStream_t st) {
+    switch (kv.hd) {
+        case 64: return nt == 1 ? launch_one<64, TYPE, 1, SINK>(kv, a, ctas, st)
+                      : nt == 2 ? launch_one<64, TYPE, 2, SINK>(kv, a, ctas, st) : launch_one<64, TYPE, 4, SINK>(kv, a, ctas, st);
+        case 128: return nt == 1 ? launch_one<128, TYPE, 1, SINK>(kv, a, ctas, st)
+                       : nt == 2 ? launch_one<128, TYPE, 2, SINK>(kv, a, ctas, st) : launch_one<128, TYPE, 4, SINK>(kv, a, ctas, st);
+        default: return nt == 1 ? launch_one<256, TYPE, 1, SINK>(kv, a, ctas, st) : launch_one<256, TYPE, 2, SINK>(kv, a, ctas, st);
+    }
+}
 template <int TYPE>
 static fr_status launch_type(const KvDesc& kv, const AttnArgs& a, int nt, int ctas, cudaStream_t st) {
-    switch (kv.hd) {
-        case 64: return nt == 1 ? launch_one<64, TYPE, 1>(kv, a, ctas, st)
-                      : nt == 2 ? launch_one<64, TYPE, 2>(kv, a, ctas, st) : launch_one<64, TYPE, 4>(kv, a, ctas, st);
-        case 128: return nt == 1 ? launch_one<128, TYPE, 1>(kv, a, ctas, st)
-                       : nt == 2 ? launch_one<128, TYPE, 2>(kv, a, ctas, st) : launch_one<128, TYPE, 4>(kv, a, ctas, st);
-        default: return nt == 1 ? launch_one<256, TYPE, 1>(kv, a, ctas, st) : launch_one<256, TYPE, 2>(kv, a, ctas, st);
-    }
+    return a.sink ? launch_hd<TYPE, true>(kv, a, nt, ctas, st) : launch_hd<TYPE, false>(kv, a, nt, ctas, st);
 }
 
 }  // namespace paged

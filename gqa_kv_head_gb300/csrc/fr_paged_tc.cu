@@ -125,11 +125,11 @@ __device__ __forceinline__ int2 row_view(const Seg& s, int row, const AttnArgs& 
     return make_int2(lo, hi);
 }
 
-template <int HD, bool E4>
+template <int HD, bool E4, bool SINK>
 __global__ void __launch_bounds__((Cfg<HD, E4>::THREADS), 1)
 paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMaps mp, const __grid_constant__ Pages pg) {
     using C = Cfg<HD, E4>;
-    using P = Units<0, kBN, 1, kTcSegCost>;
+    using P = Units<0, kBN, 1, kTcSegCost, SINK>;
     constexpr int KS = C::KS, RS = E4 ? C::RS : 1, HB = kBN / 2, OH = HD / 2;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -189,13 +189,15 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
         for (;;) {
             const int2 t = walk_tiles<P>(*w, 0);
             const Seg& s = w->s;
+            const int first = sink_tiles<P>(s, a);
             int page = -1;
             bool has = false;
             float ks = 0.f, vs = 0.f;
             auto look_up = [&](int tile) {       // pages of the next 32 16-key steps, one a lane
-                const int key = (s.tile0 + tile) * kBN + lane * kTile;
+                const int key = tile_key<P>(s, tile + lane / 4, first) + lane % 4 * kTile;
                 // (a box is looked up for its first key, also where only its last ones are in view)
-                has = key < s.n_kv && (key | (pg.box_rows - 1)) >= s.lo && tile + lane / 4 < t.y;
+                has = key < s.n_kv && ((key | (pg.box_rows - 1)) >= s.lo || P::is_sink(key & ~(pg.box_rows - 1), a)) &&
+                      tile + lane / 4 < t.y;
                 page = has ? a.table[s.b * a.table_stride + (key >> a.page_shift)] : -1;
                 if (has && (page < 0 || page >= a.n_pages)) {
                     atomicOr(a.status, kStatusInput);
@@ -210,7 +212,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             if (t.x < t.y) look_up(t.x);
             for (int tile = t.x; tile < t.y; ++tile, ++n) {
                 if (blk == 8) look_up(tile);
-                const int st = n % KS, key = (s.tile0 + tile) * kBN, in_page = (1 << a.page_shift) - 1;
+                const int st = n % KS, key = tile_key<P>(s, tile, first), in_page = (1 << a.page_shift) - 1;
                 // (this wait also keeps the tile within 16 of the softmax's)
                 if (!E4 && n >= KS) free_slot(C::B_KE + st, ((n / KS) - 1) & 1);
                 if (E4 && item >= C::RS) free_slot(C::B_RE + item % RS, ((item / RS) - 1) & 1);
@@ -403,6 +405,9 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             const Seg& s = w->s;
             const int row0 = s.rt * a.row_tile, rows = min(a.row_tile, s.n_q * G - row0);
             const int2 first = row_view(s, row0, a), end = row_view(s, row0 + rows - 1, a);
+            const int first_tiles = sink_tiles<P>(s, a);
+            // does some row not see all of the tile's keys?
+            auto is_edge = [&](int key0) { return key0 + kBN > first.y || (key0 < end.x && P::hidden(key0 + kBN - 1, a)); };
             const int2 view = r < rows ? row_view(s, row0 + r, a) : make_int2(0, 0);
             const bool active = qd * 32 < rows;
             if (tid == 0) put_split(a, share, cta, *w, row0, rows);
@@ -411,16 +416,16 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 wait(C::B_SF + (n & 1), (n >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
-                const int key0 = (s.tile0 + tile) * kBN;
+                const int key0 = tile_key<P>(s, tile, first_tiles);
                 const Meta& m = s_meta[n & 15];
                 const uint32_t none = m.none;
-                const bool edge = none || key0 + kBN > first.y || key0 < end.x;
+                const bool edge = none || is_edge(key0);
                 float v_max = 0.f, v_step[2] = {1.f, 1.f};        // e4m3: V's scales, of the steps that the row sees
                 if (E4) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = key0 + i * kTile;
-                        const float v = edge && (j >= view.y || j + kTile <= view.x || (none >> i & 1u)) ? 0.f : m.vs[i];
+                        const float v = edge && (j >= view.y || (j + kTile <= view.x && P::hidden(j, a)) || (none >> i & 1u)) ? 0.f : m.vs[i];
                         v_max = fmaxf(v_max, fabsf(v));
                         if (i >> 1 == half) v_step[i & 1] = v;
                     }
@@ -435,7 +440,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
 #pragma unroll
                         for (int c = 0; c < HB; ++c) {
                             const int j = key0 + c_base + c;
-                            if (j < view.x || j >= view.y || (none >> ((c_base + c) >> 4) & 1u)) x[c] = -INFINITY;
+                            if ((j < view.x && P::hidden(j, a)) || j >= view.y || (none >> ((c_base + c) >> 4) & 1u)) x[c] = -INFINITY;
                         }
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -506,10 +511,12 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     wait(C::B_VF + n % KS, (n / KS) & 1);
                     unsigned char* v = sm + C::V + n % KS * C::TILE;
                     auto at = [&](int i) { return reinterpret_cast<uint4*>(v + (i >> 9) * C::KV_BOX + (i & 511) * 16); };
-                    auto dead = [&](int j) { return key0 + j >= end.y || key0 + j < first.x || (none >> (j >> 4) & 1u); };
+                    auto dead = [&](int j) {
+                        return key0 + j >= end.y || (key0 + j < first.x && P::hidden(key0 + j, a)) || (none >> (j >> 4) & 1u);
+                    };
                     for (int i = tid; i < kBN * HD / 8; i += kSmax) {
                         const int j = (i & 511) >> 3;
-                        if (dead(j) || (key0 + j < first.y && key0 + j >= end.x)) continue;
+                        if (dead(j) || (key0 + j < first.y && (key0 + j >= end.x || P::is_sink(key0 + j, a)))) continue;
                         const uint4 z = *at(i);
                         if (odd_half2(z.x) || odd_half2(z.y) || odd_half2(z.z) || odd_half2(z.w)) {
                             s_odd[(n & 1) * kBN + j] = n + 1;
@@ -561,10 +568,13 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                         } else if (odd) {
                             // the cleared rows that this row sees: one by one, from memory
                             const __half* q = a.q16 + (int64_t)(s.tok0 + tok) * a.q_stride + (int64_t)(s.h * G + hh) * HD;
-                            const int from = max(view.x, (s.tile0 + t.x) * kBN), to = min(view.y, (s.tile0 + t.y) * kBN);
-                            for (int j = from; j < to; ++j) {
-                                const int j0 = j / kBN * kBN;              // (only tiles with keys that some row does not see were cleared)
-                                if (!(j0 + kBN > first.y || j0 < end.x) || (j >= end.x && j < first.y)) continue;
+                            const int key_t = (s.tile0 - first_tiles) * kBN;       // (tile t of the window starts at key_t + t kBN)
+                            const int from = SINK ? t.x * kBN : max(view.x - key_t, t.x * kBN), to = min(view.y - key_t, t.y * kBN);
+                            for (int i = from; i < to; ++i) {
+                                const int j = SINK && i < first_tiles * kBN ? i : key_t + i, j0 = j / kBN * kBN;
+                                if (SINK && j < view.x && P::hidden(j, a)) continue;
+                                // (only tiles with keys that some row does not see were cleared)
+                                if (!is_edge(j0) || (j < first.y && (j >= end.x || P::is_sink(j, a)))) continue;
                                 const int page = a.table[s.b * a.table_stride + (j >> a.page_shift)];
                                 if (page < 0 || page >= a.n_pages) continue;
                                 const int in = j & ((1 << a.page_shift) - 1);
@@ -610,12 +620,12 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     if (warp == kMma) tmem_dealloc(tbase, 512);
 }
 
-template <int HD, bool E4>
+template <int HD, bool E4, bool SINK>
 static fr_status launch(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
     using C = Cfg<HD, E4>;
     static unsigned long long done = 0ull;           // devices whose shared-memory limit is raised
     if (kv.dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> kv.dev & 1ull)) {
-        if (cudaFuncSetAttribute(paged_tc_kernel<HD, E4>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        if (cudaFuncSetAttribute(paged_tc_kernel<HD, E4, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
             cudaSuccess)
             return FR_ERR_CUDA;
         if (kv.dev < 64) __atomic_fetch_or(&done, 1ull << kv.dev, __ATOMIC_RELEASE);
@@ -649,19 +659,22 @@ static fr_status launch(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_tc_kernel<HD, E4>, a, mp, pg) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, paged_tc_kernel<HD, E4, SINK>, a, mp, pg) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
+}
+
+template <bool E4, bool SINK>
+static fr_status launch_hd(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
+    return kv.hd == 64    ? launch<64, E4, SINK>(kv, a, ctas, st)
+           : kv.hd == 128 ? launch<128, E4, SINK>(kv, a, ctas, st)
+                          : launch<256, E4, SINK>(kv, a, ctas, st);
 }
 
 }  // namespace tc
 
 fr_status launch_attn_tc(const KvDesc& kv, const AttnArgs& a, int ctas, cudaStream_t st) {
     if (kv.type == FR_KV_E4M3)
-        return kv.hd == 64    ? tc::launch<64, true>(kv, a, ctas, st)
-               : kv.hd == 128 ? tc::launch<128, true>(kv, a, ctas, st)
-                              : tc::launch<256, true>(kv, a, ctas, st);
-    return kv.hd == 64    ? tc::launch<64, false>(kv, a, ctas, st)
-           : kv.hd == 128 ? tc::launch<128, false>(kv, a, ctas, st)
-                          : tc::launch<256, false>(kv, a, ctas, st);
+        return a.sink ? tc::launch_hd<true, true>(kv, a, ctas, st) : tc::launch_hd<true, false>(kv, a, ctas, st);
+    return a.sink ? tc::launch_hd<false, true>(kv, a, ctas, st) : tc::launch_hd<false, false>(kv, a, ctas, st);
 }
 
 }  // namespace paged

@@ -27,10 +27,16 @@ __device__ __forceinline__ int token_of(int r, const AttnArgs& a) {
 }
 
 // A kernel's units: RT rows of a row tile (0: as the launch says), tiles of KT
-// keys, W of them (one for each warp) a unit, SEG more units for a segment.
-template <int RT_, int KT_, int W_, int SEG_>
+// keys, W of them (one for each warp) a unit, SEG more units for a segment. SINK:
+// compiled for windows with sinks (as a number of the launch alone, which is then
+// 0, the look at it cost the calls without sinks 0.5-2 %, 4x1000 in e4m3 4 %).
+template <int RT_, int KT_, int W_, int SEG_, bool SINK>
 struct Units {
     static constexpr int KT = KT_, W = W_, SEG = SEG_;
+    static constexpr bool HAS_SINK = SINK;
+    // Is a key below a window (one that starts behind it) hidden? Is key j a sink?
+    __device__ static __forceinline__ bool hidden(int j, const AttnArgs& a) { return !SINK || j >= a.sink; }
+    __device__ static __forceinline__ bool is_sink(int j, const AttnArgs& a) { return SINK && j < a.sink; }
     __device__ static __forceinline__ int rows(const AttnArgs& a) { return RT_ ? RT_ : a.row_tile; }
 };
 
@@ -39,8 +45,20 @@ struct Seg {
     int b, h, rt, n_rt;
     int tok0, n_q, n_kv;
     int tile0, n_tiles, n_units;
-    int lo;             // first key in some row's view
+    int lo;             // first key in some row's window
 };
+
+// Keys 0 .. sink - 1 stay visible behind a window: their tiles come first in the
+// segment's list where the window's own do not hold them.
+template <class P>
+__device__ __forceinline__ int sink_tiles(const Seg& s, const AttnArgs& a) {
+    return P::HAS_SINK ? min((a.sink + P::KT - 1) / P::KT, s.tile0) : 0;
+}
+// First key of the segment's tile t, with `first` of them ahead of the window's.
+template <class P>
+__device__ __forceinline__ int tile_key(const Seg& s, int t, int first) {
+    return P::HAS_SINK && t < first ? t * P::KT : (s.tile0 - first + t) * P::KT;
+}
 
 template <class P>
 __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
@@ -55,7 +73,7 @@ __device__ __forceinline__ void seg_keys(Seg& s, const AttnArgs& a) {
     }
     s.lo = lo;
     s.tile0 = lo / P::KT;
-    s.n_tiles = hi > lo ? (hi + P::KT - 1) / P::KT - s.tile0 : 0;
+    s.n_tiles = hi > lo ? (hi + P::KT - 1) / P::KT - s.tile0 + sink_tiles<P>(s, a) : 0;
     // a segment's start and end cost a CTA as much as some units of its keys: it
     // counts those ahead of them (rows without keys still get their zeros)
     s.n_units = P::SEG + (s.n_tiles + P::W - 1) / P::W;

@@ -176,13 +176,15 @@ def make_paged_workspace(n_head, n_kv_head, hd, device="cuda", stream=None):
     return ws
 
 
-def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0, out=None, workspace=None, stream=None):
+def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0, out=None, workspace=None, stream=None,
+               sinks=0):
     """fr_paged_attn: attention of the step's query rows over the paged cache.
     q16: f16 [n_tok, n_head, hd] (the token stride may be larger) or [n_tok *
     n_head, hd] contiguous, as qkv_post returns it. causal: token i of a
     sequence sees the keys up to its own; window > 0: only the last `window` of
-    them. Returns out [n_tok, n_head, hd] f32; rows behind the last sequence are
-    left as they were."""
+    them, and with sinks > 0 the sequence's first `sinks` keys beside these
+    (fr_paged_attn_sinks). Returns out [n_tok, n_head, hd] f32; rows behind the
+    last sequence are left as they were."""
     if not (q16.is_cuda and (out is None or out.is_cuda) and (workspace is None or workspace.is_cuda)):
         raise ValueError("tensors must be CUDA tensors")
     hd, shape, strides = cache.hd, q16.shape, q16.stride()
@@ -212,3 +214,11 @@ def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0
     if st:
         _abi.check(st, "fr_paged_attn")
     return out
+    if sinks:
+        sinks = -1 if sinks < 0 else min(sinks, 2 ** 31 - 1)
+        st = cache._lib.fr_paged_attn_sinks(
+            cache._p, desc[0], q16.data_ptr(), stride, n_head, 1 if causal else 0, window, sinks, kq_scale,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache._index))
+        if st:
+            _abi.check(st, "fr_paged_attn_sinks")
+        return out

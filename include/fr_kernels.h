@@ -464,3 +464,16 @@ fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, cons
 #endif
 
 #endif /* FR_KERNELS_H */
+/*
+ * fr_paged_attn_sinks -- fr_paged_attn with a sliding window and a few first tokens
+ * that stay visible: token i of sequence b, at p = kv_len[b] - n_b + i, sees the keys
+ *   j <= p  with  j > p - window  or  j < n_sink.
+ * Pages that hold neither a sink nor a key of some row's window are not looked up, so
+ * they may be gone (their table entries anything). Everything else is as in
+ * fr_paged_attn, which is this call with n_sink = 0.
+ *   n_sink      >= 0; > 0 only with window > 0
+ */
+fr_status fr_paged_attn_sinks(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
+                              int64_t q_tok_stride, int n_head, int causal, int window, int n_sink, float kq_scale,
+                              float* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
