@@ -26,6 +26,7 @@ FR_KV_F16 = 0
 FR_KV_E4M3 = 1
 FR_ROWS_F32 = 0
 FR_ROWS_F16 = 1
+FR_ROWS_BF16 = 2
 
 
 class FrRopeParams(ctypes.Structure):
@@ -84,9 +85,9 @@ SIGNATURES = {
     "fr_kv_append_paged": (_I, [_P, _P, _I, _P, _I64, _P, _I64, _P, _P, _P, _P]),
     "fr_paged_attn_workspace_size": (_SZ, [_I, _I, _I]),
     "fr_paged_attn": (_I, [_P, _P, _P, _I64, _I, _I, _I, _F, _P, _P, _SZ, _P]),
-    "fr_decode_attn_plan": (_I, [_I, _I, _I, _I, _I, _SZ, ctypes.POINTER(FrAttnOpts),
     "fr_qkv_post_paged": (_I, [_P, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _P, _F, _P, _I, _F, _P, _P, _P]),
     "fr_paged_attn_sinks": (_I, [_P, _P, _P, _I64, _I, _I, _I, _I, _F, _P, _P, _SZ, _P]),
+    "fr_decode_attn_plan": (_I, [_I, _I, _I, _I, _I, _SZ, ctypes.POINTER(FrAttnOpts),
                                  ctypes.POINTER(FrAttnPlan)]),
 }
 

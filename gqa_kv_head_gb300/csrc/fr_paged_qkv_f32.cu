@@ -1,0 +1,12 @@
+// fr_paged_qkv_f32.cu -- the kernels of fr_qkv_post_paged over f32 rows.
+#include "fr_paged_qkv.cuh"
+
+namespace fr {
+namespace paged {
+
+fr_status launch_qkv_f32(const QkvArgs& g, const RopeTable& tb, int hd, bool e4, cudaStream_t st) {
+    return launch_qkv<float>(g, tb, hd, e4, st);
+}
+
+}  // namespace paged
+}  // namespace fr

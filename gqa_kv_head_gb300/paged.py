@@ -10,10 +10,11 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import FR_KV_E4M3, FR_KV_F16, FR_ROWS_F16, FR_ROWS_F32, FrError
-from .ops import _as_rope, _check_dev
+from ._abi import FR_KV_E4M3, FR_KV_F16, FR_ROWS_BF16, FR_ROWS_F16, FR_ROWS_F32, FrError
+from .ops import _as_rope, _check_dev, _q_scale
 
 _ROWS = {torch.float32: FR_ROWS_F32, torch.float16: FR_ROWS_F16}
+_QKV_ROWS = {**_ROWS, torch.bfloat16: FR_ROWS_BF16}
 _KV = {torch.float16: FR_KV_F16, torch.float8_e4m3fn: FR_KV_E4M3}
 
 
@@ -161,6 +162,61 @@ def kv_append_paged(cache, batch, k_new, v_new, pos, rope, workspace=None, strea
         _abi.check(st, "fr_kv_append_paged")
 
 
+def qkv_post_paged(cache, batch, q, k_new, v_new, pos, rope, *, q_norm=None, k_norm=None, eps=1e-6, interleaved=False,
+                   q_scale=None, q16_out=None, workspace=None, stream=None):
+    """fr_qkv_post_paged: a step's query, key and value rows in one launch. Query
+    and key heads are normed (RMS over the head, with weights q_norm and k_norm:
+    f32 [hd], or None for no norm), rotated (pairs of halves, or interleaved) and,
+    the queries, scaled; keys and values go into the pages of their sequences as
+    kv_append_paged writes them. q: f32, f16 or bf16 [n_tok, n_head, hd] or [n_tok,
+    n_head * hd]; k_new, v_new: the same type, [n_tok, n_kv_head, hd]; token
+    strides may be larger (columns of a fused QKV buffer); pos: int32 [n_tok].
+    Returns q16 [n_tok * n_head, hd] f16, as qkv_post does; rows behind the last
+    sequence are left as they were."""
+    if not (q.is_cuda and k_new.is_cuda and v_new.is_cuda and pos.is_cuda):
+        raise ValueError("tensors must be CUDA tensors")
+    _check_dev(q_norm, k_norm, q16_out, workspace)
+    dtype, hd = q.dtype, cache.hd
+    if dtype not in _QKV_ROWS or k_new.dtype != dtype or v_new.dtype != dtype:
+        raise TypeError("q, k_new and v_new must all be float32, float16 or bfloat16")
+    if pos.dtype != torch.int32:
+        raise TypeError("pos must be int32")
+    shape, strides = q.shape, q.stride()
+    if len(shape) == 3 and shape[2] == hd and shape[1] > 0 and strides[2] == 1 and (shape[1] == 1 or strides[1] == hd):
+        n_head = shape[1]
+    elif len(shape) == 2 and shape[1] > 0 and shape[1] % hd == 0 and strides[1] == 1:
+        n_head = shape[1] // hd
+    else:
+        raise ValueError("q must be [n_tok, n_head, hd] with contiguous heads, or [n_tok, n_head * hd]")
+    n_tok = shape[0]
+    n_k, k_stride = _rows(k_new, "k_new", cache)
+    n_v, v_stride = _rows(v_new, "v_new", cache)
+    if n_k != n_tok or n_v != n_tok or pos.shape != (n_tok,) or not pos.is_contiguous():
+        raise ValueError("q, k_new, v_new and pos must have one row a token")
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is None:
+            continue
+        if w.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32")
+        if w.shape != (hd,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [hd]")
+    if q16_out is None:
+        with torch.cuda.stream(stream):
+            q16_out = torch.empty((n_tok * n_head, hd), dtype=torch.float16, device=q.device)
+    elif q16_out.dtype != torch.float16 or q16_out.shape != (n_tok * n_head, hd) or not q16_out.is_contiguous():
+        raise ValueError("q16_out must be contiguous float16 [n_tok * n_head, hd]")
+    rope, desc = _as_rope(rope), batch._desc(n_tok)
+    st = cache._lib.fr_qkv_post_paged(
+        cache._p, desc[0], _QKV_ROWS[dtype], q.data_ptr(), strides[0] if n_tok > 1 else n_head * hd, k_new.data_ptr(),
+        k_stride, v_new.data_ptr(), v_stride, pos.data_ptr(), n_head, None if q_norm is None else q_norm.data_ptr(),
+        None if k_norm is None else k_norm.data_ptr(), eps, ctypes.addressof(rope), 1 if interleaved else 0,
+        _q_scale(q_scale), q16_out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        _stream_of(stream, cache._index))
+    if st:
+        _abi.check(st, "fr_qkv_post_paged")
+    return q16_out
+
+
 def paged_attn_workspace_size(n_head, n_kv_head, hd):
     return int(_abi.load().fr_paged_attn_workspace_size(n_head, n_kv_head, hd))
 
@@ -208,12 +264,6 @@ def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0
     # (a C int would keep the low 32 bits of what does not fit it)
     window = -1 if window < 0 else 2 ** 31 - 1 if window > 2 ** 31 - 1 else window
     desc = batch._desc(n_tok)
-    st = cache._lib.fr_paged_attn(
-        cache._p, desc[0], q16.data_ptr(), stride, n_head, 1 if causal else 0, window, kq_scale,
-        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache._index))
-    if st:
-        _abi.check(st, "fr_paged_attn")
-    return out
     if sinks:
         sinks = -1 if sinks < 0 else min(sinks, 2 ** 31 - 1)
         st = cache._lib.fr_paged_attn_sinks(
@@ -222,3 +272,9 @@ def paged_attn(cache, batch, q16, n_head, *, causal=True, window=0, kq_scale=1.0
         if st:
             _abi.check(st, "fr_paged_attn_sinks")
         return out
+    st = cache._lib.fr_paged_attn(
+        cache._p, desc[0], q16.data_ptr(), stride, n_head, 1 if causal else 0, window, kq_scale,
+        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(stream, cache._index))
+    if st:
+        _abi.check(st, "fr_paged_attn")
+    return out

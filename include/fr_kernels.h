@@ -424,6 +424,36 @@ fr_status fr_kv_append_paged(const fr_paged_kv* kv, const fr_paged_batch* batch,
                              int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* pos,
                              const fr_rope_params* rp, void* workspace, cudaStream_t stream);
 
+/*
+ * fr_qkv_post_paged -- fr_qkv_post and fr_kv_append_paged for a step's rows in one
+ * launch, with RMS norms of the query and key heads ahead of the rotation, pairs of
+ * either layout, and bf16 rows:
+ *   n(x)     = w x / sqrt(mean(x^2) + eps) over a head's hd elements (x without weights)
+ *   q16_out  = f16(q_scale * RoPE(n(q), pos)),  K = RoPE(n(k_new), pos),  V = v_new,
+ * K and V as fr_kv_append_paged writes them. Norms, rotation and scale in fp32, one
+ * rounding at the end; without weights and with pairs (i, i + n_dims/2) the bits are
+ * those of the two calls. A row whose squares pass fp32's range is normed all the same.
+ * Rows of q from tok_start[n_seq] on are padding: not used, their q16_out left as it was.
+ *   row_type    FR_ROWS_F32, FR_ROWS_F16 or FR_ROWS_BF16: type of q, k_new and v_new
+ *               (bf16 and f32 values beyond f16's range become infinite in f16)
+ *   q, k_new, v_new  element (t, h, d) at t*stride + h*hd + d; strides at least the
+ *               heads' elements, multiples of 16 bytes
+ *   n_head      query heads, 1 .. 65536
+ *   q_norm, k_norm  nullable: f32 [hd] weights of the heads' norms
+ *   eps         finite, >= 0 (0: a row of zeros gives NaN)
+ *   interleaved 0: pair i is (x[i], x[i + n_dims/2]); 1: (x[2i], x[2i + 1]); dims from
+ *               n_dims on pass through
+ *   q_scale     as in fr_qkv_post
+ *   q16_out     f16 [n_tok*n_head][hd], contiguous; must not overlap the rows
+ *   workspace   as in fr_kv_append_paged
+ */
+#define FR_ROWS_BF16 2
+fr_status fr_qkv_post_paged(const fr_paged_kv* kv, const fr_paged_batch* batch, int row_type, const void* q,
+                            int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                            const int32_t* pos, int n_head, const float* q_norm, const float* k_norm, float eps,
+                            const fr_rope_params* rp, int interleaved, float q_scale, uint16_t* q16_out,
+                            void* workspace, cudaStream_t stream);
+
 /* Workspace bytes of fr_paged_attn, for any batch (0 for unsupported heads). */
 size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
 
@@ -459,11 +489,6 @@ fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, cons
                         int64_t q_tok_stride, int n_head, int causal, int window, float kq_scale, float* out,
                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-#ifdef __cplusplus
-}
-#endif
-
-#endif /* FR_KERNELS_H */
 /*
  * fr_paged_attn_sinks -- fr_paged_attn with a sliding window and a few first tokens
  * that stay visible: token i of sequence b, at p = kv_len[b] - n_b + i, sees the keys
@@ -477,3 +502,8 @@ fr_status fr_paged_attn_sinks(const fr_paged_kv* kv, const fr_paged_batch* batch
                               int64_t q_tok_stride, int n_head, int causal, int window, int n_sink, float kq_scale,
                               float* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FR_KERNELS_H */
