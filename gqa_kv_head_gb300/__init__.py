@@ -13,10 +13,14 @@ from .ops import (decode_attn, decode_attn_noalloc, decode_attn_noalloc_check, d
                   workspace_check, workspace_size)
 from .paged import (PagedBatch, PagedKV, kv_append_paged, make_paged_workspace, paged_attn,
                     paged_attn_workspace_size, qkv_post_paged)
+from .pages import (PagePool, pages_check, pages_compact, pages_copy, pages_fork, pages_free, pages_reserve, pages_trim,
+                    pages_workspace_size)
 
 __all__ = ["FR_ROPE_EXACT", "FR_ROPE_GGML_F32", "FrError", "FrRopeParams", "library_path", "load", "decode_attn", "decode_attn_noalloc",
            "decode_attn_noalloc_check",
            "decode_attn_plan", "kv_append", "make_workspace",
            "qkv_post", "rope_params", "workspace_check", "workspace_size",
            "FR_KV_E4M3", "FR_KV_F16", "PagedBatch", "PagedKV", "kv_append_paged", "make_paged_workspace", "paged_attn",
-           "paged_attn_workspace_size", "qkv_post_paged"]
+           "paged_attn_workspace_size", "qkv_post_paged",
+           "PagePool", "pages_check", "pages_compact", "pages_copy", "pages_fork", "pages_free", "pages_reserve", "pages_trim",
+           "pages_workspace_size"]

@@ -11,7 +11,7 @@ from . import build as _build
 FR_OK = 0
 STATUS_NAMES = {0: "FR_OK", 1: "FR_ERR_INVALID_ARG", 2: "FR_ERR_UNSUPPORTED",
                 3: "FR_ERR_WORKSPACE", 4: "FR_ERR_CUDA", 5: "FR_ERR_DEVICE_TIMEOUT",
-                6: "FR_ERR_DEVICE_INPUT"}
+                6: "FR_ERR_DEVICE_INPUT", 7: "FR_ERR_DEVICE_PAGES"}
 
 
 class FrError(RuntimeError):
@@ -57,6 +57,10 @@ class FrPagedBatch(ctypes.Structure):
     _fields_ = [("opaque", ctypes.c_uint64 * 16)]
 
 
+class FrPagePool(ctypes.Structure):
+    _fields_ = [("opaque", ctypes.c_uint64 * 16)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -87,6 +91,15 @@ SIGNATURES = {
     "fr_paged_attn": (_I, [_P, _P, _P, _I64, _I, _I, _I, _F, _P, _P, _SZ, _P]),
     "fr_qkv_post_paged": (_I, [_P, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _P, _F, _P, _I, _F, _P, _P, _P]),
     "fr_paged_attn_sinks": (_I, [_P, _P, _P, _I64, _I, _I, _I, _I, _F, _P, _P, _SZ, _P]),
+    "fr_pages_workspace_size": (_SZ, [_I, _I]),
+    "fr_page_pool_init": (_I, [_P, _P, _I, _I, _P, _P, _I64, _I, _I, _P, _SZ]),
+    "fr_pages_reserve": (_I, [_P, _P, _P]),
+    "fr_pages_fork": (_I, [_P, _P, _P, _P, _I, _P]),
+    "fr_pages_free": (_I, [_P, _P, _P, _I, _P]),
+    "fr_pages_trim": (_I, [_P, _P, _I, _I, _P]),
+    "fr_pages_compact": (_I, [_P, _P]),
+    "fr_pages_copy": (_I, [_P, _P, _P]),
+    "fr_pages_check": (_I, [_P, _P]),
     "fr_decode_attn_plan": (_I, [_I, _I, _I, _I, _I, _SZ, ctypes.POINTER(FrAttnOpts),
                                  ctypes.POINTER(FrAttnPlan)]),
 }

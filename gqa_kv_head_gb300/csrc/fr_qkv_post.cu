@@ -316,6 +316,7 @@ extern "C" const char* fr_status_string(fr_status s) {
         case FR_ERR_CUDA: return "FR_ERR_CUDA: a CUDA call or kernel launch failed";
         case FR_ERR_DEVICE_TIMEOUT: return "FR_ERR_DEVICE_TIMEOUT: a bounded device wait gave up";
         case FR_ERR_DEVICE_INPUT: return "FR_ERR_DEVICE_INPUT: a bad page, length or token range on the device";
+        case FR_ERR_DEVICE_PAGES: return "FR_ERR_DEVICE_PAGES: fewer free pages than a step needed";
     }
     return "unknown fr_status";
 }

@@ -60,7 +60,8 @@ typedef enum fr_status {
     FR_ERR_WORKSPACE = 3,      /* workspace missing or smaller than required */
     FR_ERR_CUDA = 4,           /* a CUDA runtime call or a launch failed */
     FR_ERR_DEVICE_TIMEOUT = 5, /* a bounded device-side wait gave up (see fr_workspace_check) */
-    FR_ERR_DEVICE_INPUT = 6    /* a paged call met a bad page or length on the device (see fr_workspace_check) */
+    FR_ERR_DEVICE_INPUT = 6,   /* a paged call met a bad page or length on the device (see fr_workspace_check) */
+    FR_ERR_DEVICE_PAGES = 7    /* fr_pages_reserve found fewer free pages than it needed (see fr_pages_check) */
 } fr_status;
 
 /* RoPE parameters, NEOX mode, with the YaRN terms as ggml's rope_ext takes
@@ -501,6 +502,117 @@ fr_status fr_paged_attn(const fr_paged_kv* kv, const fr_paged_batch* batch, cons
 fr_status fr_paged_attn_sinks(const fr_paged_kv* kv, const fr_paged_batch* batch, const uint16_t* q16,
                               int64_t q_tok_stride, int n_head, int causal, int window, int n_sink, float kq_scale,
                               float* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * ---- Pages of a cache --------------------------------------------------------
+ * Which pages belong to whom, kept on the device, so that a captured graph can give
+ * sequences their pages, let them share those of a prefix and take them back. A pool
+ * counts the holders of every page; tables and lengths are the arrays that the paged
+ * calls above read (every slot of the host's batch, empty ones included). One pool
+ * serves the caches of all layers: the calls below change refs, kv_len and the table
+ * alone, and fr_pages_copy carries out the copies that reserve and compact ask for,
+ * once for each layer's cache.
+ *
+ * A step of several sequences:
+ *   kv_len[b] += n_b                                  (the host's, as for fr_paged_attn)
+ *   fr_pages_reserve(pool, tok_start, stream)
+ *   for each layer: fr_pages_copy(&kv[layer], pool, stream); then the paged calls
+ *
+ * The host's part: refs start at 0 and lengths at 0, entries behind a sequence's
+ * pages are free to hold anything, and -1 stands for a page that is gone (a
+ * trimmed one). A host that holds pages by other means (a kept prefix without a
+ * slot) adds its own count to refs. The calls of one pool follow one another on the
+ * GPU (one stream, or streams ordered by events). Results do not depend on timing.
+ * Numbers that do not fit (a slot, length or page out of range, a page that counts no
+ * holder) are skipped and reported by fr_pages_check as FR_ERR_DEVICE_INPUT; nothing
+ * is read or written out of the arrays. Lists of slots may hold -1 (nothing), so that a captured call has a
+ * fixed length.
+ */
+typedef struct fr_page_pool { uint64_t opaque[16]; } fr_page_pool;
+
+/* Workspace bytes of a pool (0 for unsupported sizes). */
+size_t fr_pages_workspace_size(int n_pages, int n_seq);
+
+/*
+ * fr_page_pool_init -- describe a pool, as the descriptors above do (plain memory of the
+ * caller's, for the GPU that is current now).
+ *   refs        int32 [n_pages]: holders of each page (table entries, and the host's own)
+ *   kv_len      int32 [n_seq]: keys of each slot
+ *   page_table  int32 [n_seq][max_pages], row stride page_table_stride
+ *   workspace   >= fr_pages_workspace_size bytes, 16-byte aligned, zeroed once
+ *               (fr_workspace_init), the pool's own while it lives. A host may read
+ *               there: int32 at byte 64, the number of moves of the last reserve or
+ *               compact; from byte 1024 on the moves, int32 {from, to, rows, 0}, room
+ *               for max(n_seq, n_pages/2 + 1); behind these the map of the last compact,
+ *               int32 [n_pages]: where each page went (-1: it was free).
+ * Supported: page_size in {16, 32, 64, 128, 256}, n_pages <= 2^28, n_seq <= 65536,
+ * max_pages <= 2^22.
+ */
+fr_status fr_page_pool_init(fr_page_pool* pool, int32_t* refs, int n_pages, int page_size, int32_t* kv_len,
+                            int32_t* page_table, int64_t page_table_stride, int n_seq, int max_pages, void* workspace,
+                            size_t workspace_bytes);
+
+/*
+ * fr_pages_reserve -- pages for the rows of a step: tok_start as in fr_paged_batch_init,
+ * kv_len with the new tokens counted. In the order of the slots, and of the rows:
+ *   a page that the slot's earlier rows share with another holder is replaced: the slot
+ *     takes a new page, with a move of the earlier rows, and one holder less is counted;
+ *     of the last holders, when all go on in the page, the last slot keeps it;
+ *   every further page that the new rows need is a new one.
+ * New pages are those that were free before the call, the lowest first. Where none is
+ * left the entry becomes -1 (rows are then not written, keys are masked), and
+ * fr_pages_check reports FR_ERR_DEVICE_PAGES; such a slot is to be freed.
+ */
+fr_status fr_pages_reserve(const fr_page_pool* pool, const int32_t* tok_start, cudaStream_t stream);
+
+/*
+ * fr_pages_fork -- slot child[i] becomes a copy of the first length[i] keys of slot
+ * parent[i] (all of them where length is NULL) by holding the same pages, the last one
+ * in part. The child has to be empty (kv_len 0). Pairs with -1 are none; of several
+ * pairs with one child the first counts, the others are reported. Lengths are those
+ * before the call.  1 <= n <= n_seq.
+ */
+fr_status fr_pages_fork(const fr_page_pool* pool, const int32_t* parent, const int32_t* child, const int32_t* length,
+                        int n, cudaStream_t stream);
+
+/*
+ * fr_pages_free -- slot seq[i] keeps its first keep[i] keys (none where keep is NULL; a
+ * slot with fewer is left as it is): kv_len becomes that, the pages behind are given
+ * back and their entries become -1. A slot named more than once keeps the fewest.
+ * n >= 1.
+ */
+fr_status fr_pages_free(const fr_page_pool* pool, const int32_t* seq, const int32_t* keep, int n, cudaStream_t stream);
+
+/*
+ * fr_pages_trim -- every slot gives back the pages that fr_paged_attn_sinks with this
+ * window and n_sink no longer looks up, in the step that tok_start describes (NULL:
+ * from the key behind the slot's last on) and later ones; their entries become -1.
+ * window >= 1, n_sink >= 0.
+ */
+fr_status fr_pages_trim(const fr_page_pool* pool, const int32_t* tok_start, int window, int n_sink, cudaStream_t stream);
+
+/*
+ * fr_pages_compact -- the U held pages move into places 0 .. U - 1: the highest of those
+ * behind into the lowest hole, and so on. refs and the tables follow; the moves are left
+ * for fr_pages_copy, the map for holders that the tables do not show. Every key that
+ * kv_len counts has to have its page (or -1).
+ */
+fr_status fr_pages_compact(const fr_page_pool* pool, cudaStream_t stream);
+
+/*
+ * fr_pages_copy -- carry out the moves of the pool's last reserve or compact in one cache
+ * (rows of K and V, and the scales of e4m3 pages); a move without a page is none. The
+ * cache has the pool's n_pages and page_size, any type, heads and strides. Once for each
+ * cache, before the next reserve or compact.
+ */
+fr_status fr_pages_copy(const fr_paged_kv* kv, const fr_page_pool* pool, cudaStream_t stream);
+
+/*
+ * Reads the pool's status word (synchronises `stream`), clears it and returns
+ * FR_ERR_DEVICE_INPUT or FR_ERR_DEVICE_PAGES (above) if an earlier call on this pool met
+ * that, else FR_OK.
+ */
+fr_status fr_pages_check(const fr_page_pool* pool, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
