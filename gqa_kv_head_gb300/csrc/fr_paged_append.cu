@@ -14,7 +14,7 @@ kv_append_paged_kernel(const __grid_constant__ AppendArgs a, const __grid_consta
 template <typename T, int HD, bool E4>
 __global__ void __launch_bounds__((Prompt<T, E4>::THREADS), (E4 ? 2 : 3))
 kv_append_prompt_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ RopeTable tb, int shift, int heads) {
-    append_prompt<T, HD, E4, false>(a, tb, Norm{nullptr, 0.f, 0}, shift, heads, blockIdx.x & 1, (int)(blockIdx.x >> 1),
+    append_prompt<T, HD, E4, false, Prompt<T, E4>::KR, Prompt<T, E4>::HC>(a, tb, Norm{nullptr, 0.f, 0}, shift, heads, blockIdx.x & 1, (int)(blockIdx.x >> 1),
                                     blockIdx.y * heads);
 }
 

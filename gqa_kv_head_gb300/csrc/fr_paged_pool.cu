@@ -1,4 +1,4 @@
-// fr_pages.cu -- the bookkeeping of a paged cache's pages on the device: sequences
+// fr_paged_pool.cu -- the bookkeeping of a paged cache's pages on the device: sequences
 // that share the pages of a prefix (fork), pages for a step's new rows (reserve),
 // pages given back (free, trim), a pool moved together (compact), and the copies
 // that reserve and compact ask for (copy).

@@ -225,7 +225,7 @@ __device__ __forceinline__ void slot_dims(int c, const RopeTable& tb, const Norm
     }
 }
 // 1 / sqrt(mean of squares + eps) of a row whose elements the ITEMS lanes of an
-// aligned group hold, 8 each. Squares past fp32's range: the elements at 2^-70,
+// aligned group hold, E each. Squares past fp32's range: the elements at 2^-70,
 // which `small` says (eps is nothing beside them).
 constexpr float kSmall = 0x1p-70f;
 template <int ITEMS>
@@ -235,21 +235,24 @@ __device__ __forceinline__ float row_sum(float x) {
     for (int o = ITEMS / 2; o; o >>= 1) x += __shfl_xor_sync(group, x, o);
     return x;
 }
-template <int ITEMS>
+template <int ITEMS, int E = 8>
 __device__ __forceinline__ float row_rms(const float* y, float eps, bool& small) {
-    float s = 0.f;
+    float s = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s = fmaf(y[u], y[u], s);
-    s = row_sum<ITEMS>(s);
+    for (int u = 0; u < E; u += 2) {
+        s = fmaf(y[u], y[u], s);
+        s1 = fmaf(y[u + 1], y[u + 1], s1);
+    }
+    s = row_sum<ITEMS>(s + s1);
     small = !(s <= 3.402823466e38f);
     if (__builtin_expect(small, 0)) {     // (the group's lanes agree)
         s = 0.f;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) s = fmaf(y[u] * kSmall, y[u] * kSmall, s);
+        for (int u = 0; u < E; ++u) s = fmaf(y[u] * kSmall, y[u] * kSmall, s);
         s = row_sum<ITEMS>(s);
         eps = 0.f;
     }
-    return __frsqrt_rn(fmaf(s, 1.f / (8 * ITEMS), eps));
+    return rsqrtf(fmaf(s, 1.f / (E * ITEMS), eps));      // (off by 2^-22.9 at most)
 }
 // y times the row's factor and the weights of its dims (d0 .. d0 + 3 and d1 .. d1 + 3).
 __device__ __forceinline__ void scale_row(float* y, float inv, bool small, const float4& w0, const float4& w1) {
@@ -467,10 +470,11 @@ struct Prompt {
     static constexpr int HC = (E4 ? 2 : 8) / (sizeof(T) == 4 ? 2 : 1);
 };
 // Piece `nth` (of 2^shift rows) of heads h0 .. h0 + heads - 1.
-template <typename T, int HD, bool E4, bool EXT>
+// KR rows of a thread, HC heads at a time.
+template <typename T, int HD, bool E4, bool EXT, int KR, int HC>
 __device__ __forceinline__ void append_prompt(const AppendArgs& a, const RopeTable& tb, const Norm& nm, int shift, int heads,
                                               bool is_v, int nth, int h0) {
-    constexpr int ITEMS = HD / 8, NTH = Prompt<T, E4>::THREADS, KR = Prompt<T, E4>::KR, HC = Prompt<T, E4>::HC;
+    constexpr int ITEMS = HD / 8, NTH = Prompt<T, E4>::THREADS;
     using V = typename Raw<T>::V;
     __shared__ float red[2][HC][NTH / 32];
     Angles angles;
@@ -607,11 +611,12 @@ __device__ __forceinline__ void append_prompt(const AppendArgs& a, const RopeTab
 
 // Programmatic launch: set-up overlaps the kernel before it on the stream.
 template <typename K, typename... A>
-static cudaError_t launch(K kernel, int64_t x, int y, int threads, cudaStream_t st, const A&... args) {
+static cudaError_t launch_smem(K kernel, int64_t x, int y, int threads, int smem, cudaStream_t st, const A&... args) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3((unsigned)x, (unsigned)y);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -619,6 +624,10 @@ static cudaError_t launch(K kernel, int64_t x, int y, int threads, cudaStream_t 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename K, typename... A>
+static cudaError_t launch(K kernel, int64_t x, int y, int threads, cudaStream_t st, const A&... args) {
+    return launch_smem(kernel, x, y, threads, 0, st, args...);
 }
 // At most this many pieces of 2^shift rows: one a token, and for each sequence
 // its whole ones and two that its rows fill in part.
@@ -635,12 +644,12 @@ template <typename T, int HD, bool E4>
 static PromptPlan plan_prompt(const AppendArgs& a, int n_dims) {
     using P = Prompt<T, E4>;
     constexpr int kRows = P::THREADS * P::KR / (HD / 8);                 // rows of a prompt block
+    constexpr int64_t kBlocks = E4 ? 456 : 608;
     PromptPlan p{a.page_shift, 0, 0};
     if (!E4)
         while ((1 << p.shift) > kRows) --p.shift;                        // an f16 piece may be a part of a page
     if ((1 << p.shift) > kRows || (n_dims & 7)) return p;
     // all heads to a block, or as few as leave kBlocks blocks
-    constexpr int64_t kBlocks = E4 ? 456 : 608;
     const int64_t n = 2 * most_pieces(a, p.shift);
     int64_t heads = n * a.n_kv_head / kBlocks;
     heads = heads < P::HC ? P::HC : heads;

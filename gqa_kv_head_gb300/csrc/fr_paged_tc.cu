@@ -49,6 +49,11 @@ constexpr int kSmax = 256, kProd = 8, kMma = 9, kConv = 10, kConvThreads = 128; 
 // and moves when a score exceeds it by 15 (P_lo off f16's subnormals, P_hi within f16).
 constexpr float kBelow = 7.0f, kAbove = 15.0f;
 constexpr uint64_t kLimit = 2000000000ull;
+// The MMA's accumulator drops bits at each of a tile's 8 steps, always towards zero: after
+// 264 steps rows are 4e-6 too small. With sinks (calls without keep their sums' order) and
+// up to hd 128 the softmax warps add O to sums of their own in TMEM after so many tiles,
+// and it starts anew: 5e-7, for F_COST.
+constexpr int kSumTiles = 4;
 
 template <int HD, bool E4>
 struct Cfg {
@@ -72,8 +77,9 @@ struct Cfg {
                          B_RF = B_SF + 11, B_RE = B_RF + RS, N_BAR = B_RE + RS;
     static_assert(N_BAR <= 60, "barriers");
     // TMEM columns: O, two S tiles, two tiles of P_hi and of P_lo words (two keys a column)
-    static constexpr int T_O = 0, T_S = HD, T_P = HD + 2 * kBN, T_PL = T_P + kBN;
+    static constexpr int T_O = 0, T_S = HD, T_P = HD + 2 * kBN, T_PL = T_P + kBN, T_A = T_PL + kBN;
     static_assert(T_PL + kBN <= 512, "TMEM");
+    static constexpr bool SUMS = T_A + HD <= 512;             // room for sums of O (kSumTiles)
 };
 
 struct TcMaps {
@@ -131,6 +137,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     using C = Cfg<HD, E4>;
     using P = Units<0, kBN, 1, kTcSegCost, SINK>;
     constexpr int KS = C::KS, RS = E4 ? C::RS : 1, HB = kBN / 2, OH = HD / 2;
+    constexpr bool SUMS = SINK && C::SUMS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     unsigned char* aux = sm + C::AUX;
@@ -331,7 +338,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                             // P words: [buffer][half of the keys][16 columns]
                             const uint32_t col = (m & 1) * HB + ks * 8;
                             const uint64_t vd = sdesc_sw128(v_base + ks * 2048, C::KV_BOX, 1024);
-                            mma_ts(tbase + C::T_O, tbase + C::T_P + col, vd, id_o, i > 0 || ks > 0 ? 1u : 0u);
+                            mma_ts(tbase + C::T_O, tbase + C::T_P + col, vd, id_o, (SUMS ? i % kSumTiles : i) > 0 || ks > 0 ? 1u : 0u);
                             mma_ts(tbase + C::T_O, tbase + C::T_PL + col, vd, id_o, 1u);
                         }
                         mma_commit(bar(C::B_OD + (m & 1)));
@@ -470,10 +477,28 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     v_step[1] *= v_inv;
                 }
                 if (active) {
-                    if (__any_sync(~0u, grown || v_up) && tile > t.x) {
+                    const int i = tile - t.x;
+                    const bool sum = SUMS && i > 0 && i % kSumTiles == 0;            // O goes into the sums
+                    if ((__any_sync(~0u, grown || v_up) || sum) && i > 0) {
                         wait(C::B_OD + ((n - 1) & 1), ((n - 1) >> 1) & 1);           // O holds PV up to the tile before
                         __syncwarp();
                         tc_fence_after();
+                        if (SUMS && i >= kSumTiles) {
+#pragma unroll 1
+                            for (int c = 0; c < OH; c += 16) {
+                                uint32_t o[16], s[16];
+                                tmem_ld_x16(tbase + lanes + C::T_O + half * OH + c, o);
+                                tmem_ld_x16(tbase + lanes + C::T_A + half * OH + c, s);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) {
+                                    const float was = i > kSumTiles ? __uint_as_float(s[u]) : 0.f;   // (nothing so far)
+                                    s[u] = __float_as_uint((sum ? was + __uint_as_float(o[u]) : was) * o_scale);
+                                }
+                                tmem_st_x16(tbase + lanes + C::T_A + half * OH + c, s);
+                            }
+                        }
+                        if (!sum)
 #pragma unroll 1
                         for (int c = 0; c < OH; c += 32) {
                             uint32_t o[32];
@@ -560,6 +585,16 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     if (any) {
                         tmem_ld_x32(tbase + lanes + C::T_O + half * OH + c, reinterpret_cast<uint32_t*>(o));
                         tmem_wait_ld();
+                        if (SUMS && t.y - t.x > kSumTiles) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t s[16];
+                                tmem_ld_x16(tbase + lanes + C::T_A + half * OH + c + h, s);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) o[h + u] += __uint_as_float(s[u]);
+                            }
+                        }
                     }
                     if (r < rows) {
                         if (!any || l == 0.f) {

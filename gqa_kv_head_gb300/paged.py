@@ -173,48 +173,54 @@ def qkv_post_paged(cache, batch, q, k_new, v_new, pos, rope, *, q_norm=None, k_n
     strides may be larger (columns of a fused QKV buffer); pos: int32 [n_tok].
     Returns q16 [n_tok * n_head, hd] f16, as qkv_post does; rows behind the last
     sequence are left as they were."""
-    if not (q.is_cuda and k_new.is_cuda and v_new.is_cuda and pos.is_cuda):
+    if not (q.is_cuda and k_new.is_cuda and v_new.is_cuda and pos.is_cuda and (workspace is None or workspace.is_cuda)):
         raise ValueError("tensors must be CUDA tensors")
-    _check_dev(q_norm, k_norm, q16_out, workspace)
     dtype, hd = q.dtype, cache.hd
-    if dtype not in _QKV_ROWS or k_new.dtype != dtype or v_new.dtype != dtype:
+    kind = _QKV_ROWS.get(dtype)
+    if kind is None or k_new.dtype != dtype or v_new.dtype != dtype:
         raise TypeError("q, k_new and v_new must all be float32, float16 or bfloat16")
     if pos.dtype != torch.int32:
         raise TypeError("pos must be int32")
     shape, strides = q.shape, q.stride()
     if len(shape) == 3 and shape[2] == hd and shape[1] > 0 and strides[2] == 1 and (shape[1] == 1 or strides[1] == hd):
-        n_head = shape[1]
+        n_tok, n_head, _ = shape
     elif len(shape) == 2 and shape[1] > 0 and shape[1] % hd == 0 and strides[1] == 1:
-        n_head = shape[1] // hd
+        n_tok, n_head = shape[0], shape[1] // hd
     else:
         raise ValueError("q must be [n_tok, n_head, hd] with contiguous heads, or [n_tok, n_head * hd]")
-    n_tok = shape[0]
     n_k, k_stride = _rows(k_new, "k_new", cache)
-    n_v, v_stride = _rows(v_new, "v_new", cache)
+    if v_new.shape == k_new.shape and v_new.stride() == k_new.stride():
+        n_v, v_stride = n_k, k_stride
+    else:
+        n_v, v_stride = _rows(v_new, "v_new", cache)
     if n_k != n_tok or n_v != n_tok or pos.shape != (n_tok,) or not pos.is_contiguous():
         raise ValueError("q, k_new, v_new and pos must have one row a token")
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is None:
-            continue
-        if w.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32")
-        if w.shape != (hd,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [hd]")
     if q16_out is None:
         with torch.cuda.stream(stream):
             q16_out = torch.empty((n_tok * n_head, hd), dtype=torch.float16, device=q.device)
-    elif q16_out.dtype != torch.float16 or q16_out.shape != (n_tok * n_head, hd) or not q16_out.is_contiguous():
+    elif (q16_out.dtype != torch.float16 or q16_out.shape != (n_tok * n_head, hd) or not q16_out.is_contiguous() or
+          not q16_out.is_cuda):
         raise ValueError("q16_out must be contiguous float16 [n_tok * n_head, hd]")
+    q_weights = None if q_norm is None else _weights(q_norm, "q_norm", hd)
+    k_weights = None if k_norm is None else _weights(k_norm, "k_norm", hd)
     rope, desc = _as_rope(rope), batch._desc(n_tok)
     st = cache._lib.fr_qkv_post_paged(
-        cache._p, desc[0], _QKV_ROWS[dtype], q.data_ptr(), strides[0] if n_tok > 1 else n_head * hd, k_new.data_ptr(),
-        k_stride, v_new.data_ptr(), v_stride, pos.data_ptr(), n_head, None if q_norm is None else q_norm.data_ptr(),
-        None if k_norm is None else k_norm.data_ptr(), eps, ctypes.addressof(rope), 1 if interleaved else 0,
-        _q_scale(q_scale), q16_out.data_ptr(), None if workspace is None else workspace.data_ptr(),
+        cache._p, desc[0], kind, q.data_ptr(), strides[0] if n_tok > 1 else n_head * hd, k_new.data_ptr(), k_stride,
+        v_new.data_ptr(), v_stride, pos.data_ptr(), n_head, q_weights, k_weights, eps, ctypes.addressof(rope),
+        1 if interleaved else 0, _q_scale(q_scale), q16_out.data_ptr(), None if workspace is None else workspace.data_ptr(),
         _stream_of(stream, cache._index))
     if st:
         _abi.check(st, "fr_qkv_post_paged")
     return q16_out
+
+
+def _weights(w, name, hd):
+    """Address of a norm's weights: f32 [hd]."""
+    if w.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if w.shape != (hd,) or not w.is_contiguous() or not w.is_cuda:
+        raise ValueError(f"{name} must be contiguous [hd] on the GPU")
+    return w.data_ptr()
 
 
 def paged_attn_workspace_size(n_head, n_kv_head, hd):
