@@ -33,7 +33,10 @@ using sm100::cluster_rank;
 using sm100::cluster_sync;
 using sm100::smem_addr;
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32, kMaxCluster = 8;
+// Threads of a CTA: many for large pools and batches; a few sequences are done sooner by
+// few warps, whose instructions one SM has to issue (80 slots, 634 pages, no new rows:
+// 2.4 us by 256 threads, 3.3 by 1024).
+constexpr int kFewThreads = 256, kThreads = 1024, kMaxCluster = 8;
 constexpr int kOwn = kMaxSeq / (kThreads * kMaxCluster);      // sequences of a thread at most
 constexpr unsigned kStatusNoPages = 0x200u;
 constexpr int kMaxPages = 1 << 28;
@@ -95,8 +98,9 @@ __device__ __forceinline__ T peer(const T* p, int rank) {
 struct PageShare {
     int first, end;
 };
+template <int NT>
 __device__ __forceinline__ PageShare page_share(const PoolArgs& a) {
-    const int warps = kWarps * (int)cluster_nrank(), w = (int)cluster_rank() * kWarps + (threadIdx.x >> 5);
+    const int warps = NT / 32 * (int)cluster_nrank(), w = (int)cluster_rank() * (NT / 32) + (threadIdx.x >> 5);
     const int per = (int)((((int64_t)a.n_pages + warps - 1) / warps + 127) / 128 * 128);
     const int64_t first = (int64_t)per * w;
     PageShare s;
@@ -110,11 +114,12 @@ __device__ __forceinline__ void load_refs(const PoolArgs& a, int p, int end, int
     for (int u = 0; u < 4; ++u) r[u] = p + u * 32 < end ? __ldcg(a.refs + p + u * 32) : own;
 }
 // A count of each warp of the cluster, in order: those before this warp, and all.
+template <int NT>
 __device__ __forceinline__ int2 warp_counts(const int* counts) {
     const int lane = threadIdx.x & 31, me = threadIdx.x >> 5, rank = (int)cluster_rank();
     int before = 0, all = 0;
     for (int r = 0; r < (int)cluster_nrank(); ++r) {
-        const int v = peer(counts + lane, r);
+        const int v = lane < NT / 32 ? peer(counts + lane, r) : 0;
         all += v;
         if (r < rank || (r == rank && lane < me)) before += v;
     }
@@ -133,148 +138,210 @@ __device__ __forceinline__ bool step_of(const PoolArgs& a, const int32_t* tok_st
     return true;
 }
 
+// All threads of the cluster meet; a cluster of one CTA by the cheaper barrier.
+__device__ __forceinline__ void meet() {
+    if (cluster_nrank() == 1) __syncthreads();
+    else cluster_sync();
+}
+// The same, and whether x held anywhere (flag: a word of shared memory for this one
+// call, which the others look at until they meet again).
+__device__ __forceinline__ bool meet_any(bool x, int* flag) {
+    int any = __syncthreads_or(x);
+    if (cluster_nrank() == 1) return any != 0;
+    if (threadIdx.x == 0) *flag = any;
+    cluster_sync();
+    any = 0;
+    for (int r = 0; r < (int)cluster_nrank(); ++r) any |= peer(flag, r);
+    return any != 0;
+}
+
 // ---- reserve ------------------------------------------------------------------
-// Phases: (1) every sequence that goes on in a page takes its own count off it;
-// (2) a page that nobody holds any more goes to the last of those (marked in refs
-// as a negative number); (3) the others need a page and a copy: prefix sums of the
-// needs, free pages counted; (4) the lowest free pages listed; (5) tables filled.
-__global__ void __launch_bounds__(kThreads, 1)
+// Phases: (1) what the sequences need, from their numbers, and the free pages
+// counted meanwhile; where some go on in a page that others hold too, all of those
+// take their count off it, and a page that nobody holds any more goes to the last of
+// them (marked in refs as a negative number); (2) prefix sums of the needs; (3) the
+// lowest free pages listed; (4) tables filled: single entries by the thread that asked,
+// several of a sequence by a warp.
+constexpr int kListHere = 2048;           // pages that a single CTA lists in shared memory
+template <int NT>
+__global__ void __launch_bounds__(NT, 1)
 pages_reserve_kernel(const __grid_constant__ PoolArgs a, const int32_t* tok_start) {
-    __shared__ unsigned long long s_scan[kWarps], s_tot[kOwn];       // needs (low 40 bits) and copies
-    __shared__ int s_free[kWarps];
+    constexpr int WARPS = NT / 32;
+    __shared__ unsigned long long s_scan[WARPS], s_tot[kOwn];        // needs (low 40 bits) and copies
+    __shared__ int s_free[WARPS], s_any, s_list[kListHere];
     launch_begins();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)cluster_rank(), ranks = (int)cluster_nrank();
-    const int total_thr = kThreads * ranks, gtid = rank * kThreads + tid;
-    int part[kOwn], i0[kOwn], cnt[kOwn], rows[kOwn];
-    bool bad = false;
+    const int total_thr = NT * ranks, gtid = rank * NT + tid;
+    // (a thread's k-th sequence; most calls have none behind the first)
+    auto none = [&](int k) { return k > 0 && k * total_thr >= a.n_seq; };
+    int first[kOwn], end[kOwn], part[kOwn];          // keys before and after; the page that earlier rows share
+    bool bad = false, shared = false;
+    int t0[kOwn], t1[kOwn];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        part[k] = -1;
-        i0[k] = cnt[k] = rows[k] = 0;
+        end[k] = t0[k] = t1[k] = 0;
+        if (none(k)) continue;
         const int b = k * total_thr + gtid;
-        if (b >= a.n_seq) continue;
-        int first, n;
-        if (!step_of(a, tok_start, b, first, n)) {
-            bad = true;
-            continue;
-        }
-        if (first == n) continue;
-        i0[k] = first >> a.page_shift;
-        cnt[k] = ((n - 1) >> a.page_shift) - i0[k] + 1;
-        rows[k] = first & ((1 << a.page_shift) - 1);
-        if (!rows[k]) continue;
-        const int p = a.table[b * a.table_stride + i0[k]];
-        if (p >= 0 && p < a.n_pages && atomicSub(a.refs + p, 1) > 0) {
-            part[k] = p;
-        } else {
-            bad = true;                               // no such page, or one that counts no holder: the entry is filled anew
-            if (p >= 0 && p < a.n_pages) atomicAdd(a.refs + p, 1);
-        }
+        const bool is = b < a.n_seq;
+        end[k] = is ? a.kv_len[b] : 0;
+        t0[k] = is ? tok_start[b] : 0;
+        t1[k] = is ? tok_start[b + 1] : 0;
     }
-    cluster_sync();
-#pragma unroll
-    for (int k = 0; k < kOwn; ++k)
-        if (part[k] >= 0 && __ldcg(a.refs + part[k]) <= 0) atomicMin(a.refs + part[k], -(k * total_thr + gtid + 1));
-    cluster_sync();
-    // free pages of this warp's share
-    const PageShare sh = page_share(a);
+    // free pages of this warp's share, as bits for the first eight steps
+    const PageShare sh = page_share<NT>(a);
     int n_free = 0;
-    for (int p = sh.first + lane; p - lane < sh.end; p += 128) {
+    unsigned bits = 0u;
+    for (int p = sh.first + lane, step = 0; p - lane < sh.end; p += 128, ++step) {
         int r[4];
         load_refs(a, p, sh.end, 1, r);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) n_free += r[u] == 0;
+        for (int u = 0; u < 4; ++u) {
+            n_free += r[u] == 0;
+            if (step < 8 && r[u] == 0) bits |= 1u << (step * 4 + u);
+        }
     }
     n_free = __reduce_add_sync(~0u, n_free);
     if (lane == 0) s_free[warp] = n_free;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        const int b = k * total_thr + gtid;
+        part[k] = -1;
+        first[k] = 0;
+        if (none(k)) continue;
+        if (end[k] < 0 || end[k] > ((int64_t)a.max_pages << a.page_shift) || t0[k] < 0 || t1[k] < t0[k] || t1[k] - t0[k] > end[k]) {
+            bad = true;
+            end[k] = t1[k] = t0[k] = 0;
+        }
+        first[k] = end[k] - (t1[k] - t0[k]);
+        if (first[k] == end[k] || !(first[k] & ((1 << a.page_shift) - 1))) continue;
+        const int p = a.table[b * a.table_stride + (first[k] >> a.page_shift)];
+        const int holders = p >= 0 && p < a.n_pages ? __ldcg(a.refs + p) : 0;
+        if (holders == 1) {
+            first[k] = min(end[k], (first[k] | ((1 << a.page_shift) - 1)) + 1);       // it goes on in its page
+        } else if (holders > 1) {
+            part[k] = p;
+            shared = true;
+        } else {
+            bad = true;                               // no such page, or one that counts no holder: the entry is filled anew
+        }
+    }
+    if (meet_any(shared, &s_any)) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (!none(k) && part[k] >= 0) atomicSub(a.refs + part[k], 1);
+        meet();
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (!none(k) && part[k] >= 0 && __ldcg(a.refs + part[k]) <= 0) atomicMin(a.refs + part[k], -(k * total_thr + gtid + 1));
+        meet();
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (!none(k) && part[k] >= 0 && __ldcg(a.refs + part[k]) == -(k * total_thr + gtid + 1)) {
+                a.refs[part[k]] = 1;                  // it keeps its page
+                part[k] = -1;
+                first[k] = min(end[k], (first[k] | ((1 << a.page_shift) - 1)) + 1);
+            }
+    }
+    // entries that each needs: of the pages from that of key `first` on
+    auto entry = [&](int k) { return first[k] >> a.page_shift; };
+    auto count = [&](int k) { return first[k] < end[k] ? ((end[k] - 1) >> a.page_shift) - entry(k) + 1 : 0; };
     unsigned long long before[kOwn];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        if (k * total_thr >= a.n_seq) {
-            if (tid == 0) s_tot[k] = 0;
-            continue;
-        }
-        if (part[k] >= 0 && __ldcg(a.refs + part[k]) == -(k * total_thr + gtid + 1)) {
-            a.refs[part[k]] = 1;                      // it keeps its page
-            part[k] = -1;
-            ++i0[k];
-            --cnt[k];
-        }
-        const unsigned long long own = (unsigned long long)cnt[k] | (unsigned long long)(part[k] >= 0) << 40;
+        if (none(k)) continue;
+        const unsigned long long own = (unsigned long long)count(k) | (unsigned long long)(part[k] >= 0) << 40;
         unsigned long long inc = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const unsigned long long x = __shfl_up_sync(~0u, inc, o);
             if (lane >= o) inc += x;
         }
-        __syncthreads();                              // (s_scan has been read)
+        if (k) __syncthreads();                       // (s_scan has been read)
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
-        unsigned long long base = 0, all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) base += s_scan[w];
-            all += s_scan[w];
+        unsigned long long mine = lane < WARPS ? s_scan[lane] : 0, sum = mine;       // of the warps
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long x = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += x;
         }
-        before[k] = base + inc - own;
-        if (tid == 0) s_tot[k] = all;
+        before[k] = __shfl_sync(~0u, sum - mine, warp) + inc - own;
+        if (tid == 31) s_tot[k] = sum;
     }
-    cluster_sync();
-    const int2 free_of = warp_counts(s_free);
+    meet();
+    const int2 free_of = warp_counts<NT>(s_free);
     unsigned long long need = 0;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        if (k * total_thr >= a.n_seq) continue;
+        if (none(k)) continue;
         unsigned long long base = need;
         for (int r = 0; r < ranks; ++r) {
             const unsigned long long v = peer(s_tot + k, r);
             if (r < rank) base += v;
             need += v;
         }
-        const int b = k * total_thr + gtid;
-        if (b >= a.n_seq) continue;
-        const unsigned long long at = base + before[k], first = at & ((1ull << 40) - 1);
-        const int copy = part[k] >= 0 ? (int)(at >> 40) : -1;
-        if (copy >= 0) a.moves[copy] = Move{part[k], -1, rows[k], 0};
-        a.jobs[b] = Job{first < (unsigned long long)a.n_pages ? (int)first : a.n_pages, i0[k], cnt[k], copy};
+        before[k] += base;
     }
     const long long wanted = (long long)(need & ((1ull << 40) - 1));
     if (gtid == 0) *a.n_moves = (int)(need >> 40);
-    if (__any_sync(~0u, bad || (gtid == 0 && wanted > free_of.y))) {
-        const bool any_bad = __any_sync(~0u, bad);
-        if (lane == 0) atomicOr(a.status, (any_bad ? kStatusInput : 0u) | (gtid == 0 && wanted > free_of.y ? kStatusNoPages : 0u));
+    const bool any_bad = __any_sync(~0u, bad), short_of = gtid == 0 && wanted > free_of.y;
+    if (lane == 0 && (any_bad || short_of)) atomicOr(a.status, (any_bad ? kStatusInput : 0u) | (short_of ? kStatusNoPages : 0u));
+    if (wanted == 0) {
+        meet();                                       // (the others have read this CTA's counts)
+        return;
     }
     // the lowest free pages, as many as are wanted
+    int* const list = ranks == 1 && wanted <= kListHere ? s_list : a.list;
     int at = free_of.x;
-    for (int p = sh.first + lane; p - lane < sh.end && at < wanted; p += 128) {
-        int r[4];
-        load_refs(a, p, sh.end, 1, r);
+    for (int p = sh.first + lane, step = 0; p - lane < sh.end && at < wanted; p += 128, ++step) {
+        int r[4] = {1, 1, 1, 1};
+        if (step >= 8) load_refs(a, p, sh.end, 1, r);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const unsigned m = __ballot_sync(~0u, r[u] == 0);
-            if (r[u] == 0) a.list[at + __popc(m & ((1u << lane) - 1u))] = p + u * 32;
+            const bool is = step < 8 ? bits >> (step * 4 + u) & 1u : r[u] == 0;
+            const unsigned m = __ballot_sync(~0u, is);
+            const int place = at + __popc(m & ((1u << lane) - 1u));
+            if (is && place < wanted) list[place] = p + u * 32;
             at += __popc(m);
         }
     }
-    cluster_sync();
-    if (wanted == 0) return;
-    // a few sequences to a warp: entries by all of its lanes, single ones by the sequence's lane
-    const int warps = kWarps * ranks, per = min(32, (a.n_seq + warps - 1) / warps);
-    for (int b0 = (rank * kWarps + warp) * per; b0 < a.n_seq; b0 += warps * per) {
-        const int b = b0 + lane;
-        Job j{0, 0, 0, -1};
-        if (lane < per && b < a.n_seq) {
-            const int4 v = __ldcg(reinterpret_cast<const int4*>(a.jobs + b));
-            j = Job{v.x, v.y, v.z, v.w};
-        }
-        auto put = [&](int seq, int rank0, int entry, int e, int copy) {
-            const int page = rank0 + e < free_of.y ? __ldcg(a.list + rank0 + e) : -1;
-            a.table[seq * a.table_stride + entry + e] = page;
-            if (page >= 0) a.refs[page] = 1;
-            if (e == 0 && copy >= 0) a.moves[copy].to = page;
-        };
-        if (j.z == 1) put(b, j.x, j.y, 0, j.w);
-        for (unsigned many = __ballot_sync(~0u, j.z > 1); many; many &= many - 1) {
-            const int from = __ffs(many) - 1;
+    bool many = false;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        const int b = k * total_thr + gtid;
+        if (none(k) || b >= a.n_seq) continue;
+        const unsigned long long at_page = before[k] & ((1ull << 40) - 1);
+        const int from = at_page < (unsigned long long)a.n_pages ? (int)at_page : a.n_pages, n = count(k);
+        const int copy = part[k] >= 0 ? (int)(before[k] >> 40) : -1;
+        if (copy >= 0) a.moves[copy] = Move{part[k], -1, first[k] & ((1 << a.page_shift) - 1), 0};
+        a.jobs[b] = Job{from, entry(k), n > 1 ? n : 0, copy};
+        many |= n > 1;
+        t0[k] = from;
+        t1[k] = copy;
+    }
+    if (ranks == 1) {
+        many = __syncthreads_or(many);
+    } else {                                          // (no CTA looks into another's memory from here on)
+        cluster_sync();
+        many = true;
+    }
+    auto page_at = [&](int i) { return i >= free_of.y ? -1 : list == s_list ? s_list[i] : __ldcg(a.list + i); };
+    auto put = [&](int seq, int from, int row, int e, int copy) {
+        const int page = page_at(from + e);
+        a.table[seq * a.table_stride + row + e] = page;
+        if (page >= 0) a.refs[page] = 1;
+        if (e == 0 && copy >= 0) a.moves[copy].to = page;
+    };
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+        if (!none(k) && count(k) == 1) put(k * total_thr + gtid, t0[k], entry(k), 0, t1[k]);
+    if (!many) return;
+    const int warps = WARPS * ranks, per = min(32, (a.n_seq + warps - 1) / warps);      // sequences of a warp
+    for (int b0 = (rank * WARPS + warp) * per; b0 < a.n_seq; b0 += warps * per) {
+        int4 j = make_int4(0, 0, 0, -1);
+        if (lane < per && b0 + lane < a.n_seq) j = __ldcg(reinterpret_cast<const int4*>(a.jobs + b0 + lane));
+        for (unsigned left = __ballot_sync(~0u, j.z > 0); left; left &= left - 1) {
+            const int from = __ffs(left) - 1;
             const int x = __shfl_sync(~0u, j.x, from), y = __shfl_sync(~0u, j.y, from), z = __shfl_sync(~0u, j.z, from),
                       w = __shfl_sync(~0u, j.w, from);
 #pragma unroll 4
@@ -284,74 +351,105 @@ pages_reserve_kernel(const __grid_constant__ PoolArgs a, const int32_t* tok_star
 }
 
 // ---- fork ---------------------------------------------------------------------
-// A child is claimed by the first pair that names it: its length, 0 so far, becomes
-// the smallest of the pairs' negative marks.
-__global__ void __launch_bounds__(kThreads, 1)
+// Of several pairs with one child the first counts. Few pairs: every thread looks
+// through the children before its own; many: a child is claimed in its length, 0 so
+// far, which becomes the smallest of the pairs' negative marks.
+constexpr int kFewPairs = kFewThreads;
+template <int NT>
+__global__ void __launch_bounds__(NT, 1)
 pages_fork_kernel(const __grid_constant__ PoolArgs a, const int32_t* parent, const int32_t* child, const int32_t* length, int n) {
+    __shared__ int s_child[kFewPairs];
+    __shared__ Job s_jobs[kFewPairs];
     launch_begins();
     const int tid = threadIdx.x, rank = (int)cluster_rank(), ranks = (int)cluster_nrank();
-    const int total_thr = kThreads * ranks, gtid = rank * kThreads + tid, lane = tid & 31;
-    int len[kOwn], to[kOwn];
+    const int total_thr = NT * ranks, gtid = rank * NT + tid, lane = tid & 31;
+    const bool few = n <= kFewPairs;                   // (each CTA works them out for itself)
+    int len[kOwn], to[kOwn], from[kOwn];
     bool bad = false;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
         len[k] = to[k] = -1;
-        const int i = k * total_thr + gtid;
-        if (i >= n) continue;
-        const int p = parent[i], c = child[i];
+        const int i = k * total_thr + (few ? tid : gtid);
+        if (i >= n || (few && k)) continue;
+        const int p = parent[i], c = child[i], l = length ? length[i] : 0;
         if (p == -1 || c == -1) continue;              // no pair
         if (p < 0 || p >= a.n_seq || c < 0 || c >= a.n_seq || p == c) {
             bad = true;
             continue;
         }
-        const int have = a.kv_len[p], m = length ? length[i] : have;
-        if (have < 0 || have > ((int64_t)a.max_pages << a.page_shift) || m < 0 || m > have || a.kv_len[c] != 0) {
+        const int have = a.kv_len[p], was = a.kv_len[c], m = length ? l : have;
+        if (have < 0 || have > ((int64_t)a.max_pages << a.page_shift) || m < 0 || m > have || was != 0) {
             bad = true;
             continue;
         }
         len[k] = m;
         to[k] = c;
+        from[k] = p;
     }
-    cluster_sync();                                    // lengths have been read
+    auto pages = [&](int k) { return (int)(((int64_t)len[k] + (1 << a.page_shift) - 1) >> a.page_shift); };
+    if (few) {
+        if (tid < n) s_child[tid] = to[0];
+        meet();                                        // (lengths have been read by all CTAs)
+        if (tid < n) {
+            bool mine = to[0] >= 0;
+            for (int i = 0; i < tid && mine; ++i) mine = s_child[i] != to[0];
+            bad |= to[0] >= 0 && !mine;
+            if (mine && rank == 0) a.kv_len[to[0]] = len[0];
+            s_jobs[tid] = mine ? Job{from[0], to[0], pages(0), 0} : Job{0, 0, 0, 0};
+        }
+        __syncthreads();
+    } else {
+        meet();                                        // lengths have been read
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k)
-        if (to[k] >= 0) atomicMin(a.kv_len + to[k], k * total_thr + gtid - n);
-    cluster_sync();
-    bool mine[kOwn];
+        for (int k = 0; k < kOwn; ++k)
+            if (to[k] >= 0) atomicMin(a.kv_len + to[k], k * total_thr + gtid - n);
+        meet();
+        bool mine[kOwn];
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-        mine[k] = to[k] >= 0 && __ldcg(a.kv_len + to[k]) == k * total_thr + gtid - n;
-        bad |= to[k] >= 0 && !mine[k];
-    }
-    cluster_sync();                                    // marks have been read
+        for (int k = 0; k < kOwn; ++k) {
+            mine[k] = to[k] >= 0 && __ldcg(a.kv_len + to[k]) == k * total_thr + gtid - n;
+            bad |= to[k] >= 0 && !mine[k];
+        }
+        meet();                                        // marks have been read
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-        const int i = k * total_thr + gtid;
-        if (i >= n) continue;
-        if (mine[k]) a.kv_len[to[k]] = len[k];
-        a.jobs[i] = Job{mine[k] ? parent[i] : 0, mine[k] ? to[k] : 0, mine[k] ? (len[k] + (1 << a.page_shift) - 1) >> a.page_shift : 0, 0};
+        for (int k = 0; k < kOwn; ++k) {
+            const int i = k * total_thr + gtid;
+            if (i >= n) continue;
+            if (mine[k]) a.kv_len[to[k]] = len[k];
+            a.jobs[i] = mine[k] ? Job{from[k], to[k], pages(k), 0} : Job{0, 0, 0, 0};
+        }
+        meet();
     }
     if (__any_sync(~0u, bad) && lane == 0) atomicOr(a.status, kStatusInput);
-    cluster_sync();
     // pieces of 128 entries of a pair's tables to a warp
-    const int chunks = (a.max_pages + 127) / 128, warps = kWarps * ranks;
+    const int chunks = (a.max_pages + 127) / 128, warps = (NT / 32) * ranks;
     bool odd = false;
-    for (int64_t it = rank * kWarps + (tid >> 5); it < (int64_t)n * chunks; it += warps) {
+    for (int64_t it = rank * (NT / 32) + (tid >> 5); it < (int64_t)n * chunks; it += warps) {
         const int i = (int)(it / chunks), e0 = (int)(it - (int64_t)i * chunks) * 128 + lane;
-        const int4 j = __ldcg(reinterpret_cast<const int4*>(a.jobs + i));
+        Job j;
+        if (few) {
+            j = s_jobs[i];
+        } else {
+            const int4 v = __ldcg(reinterpret_cast<const int4*>(a.jobs + i));
+            j = Job{v.x, v.y, v.z, v.w};
+        }
         const int32_t* src = a.table + j.x * a.table_stride;
         int32_t* dst = a.table + j.y * a.table_stride;
         int p[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) p[u] = e0 + u * 32 < j.z ? src[e0 + u * 32] : -1;
+        int held[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            held[u] = 1;
             if (e0 + u * 32 >= j.z) continue;
             const bool page = p[u] >= 0 && p[u] < a.n_pages;
             odd |= !page && p[u] != -1;                // (-1: trimmed)
             dst[e0 + u * 32] = page ? p[u] : -1;
-            if (page && atomicAdd(a.refs + p[u], 1) <= 0) odd = true;
+            if (page) held[u] = atomicAdd(a.refs + p[u], 1);
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) odd |= held[u] <= 0;
     }
     if (__any_sync(~0u, odd) && lane == 0) atomicOr(a.status, kStatusInput);
 }
@@ -438,12 +536,12 @@ pages_trim_kernel(const __grid_constant__ PoolArgs a, const int32_t* tok_start, 
 // lowest hole before U: their numbers are page - used_before and U - 1 - used_before.
 __global__ void __launch_bounds__(kThreads, 1)
 pages_compact_kernel(const __grid_constant__ PoolArgs a) {
-    __shared__ int s_used[kWarps];
+    __shared__ int s_used[kThreads / 32];
     launch_begins();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gtid = (int)cluster_rank() * kThreads + tid, total_thr = kThreads * (int)cluster_nrank();
     if (gtid == 0) *a.n_moves = 0;
-    const PageShare sh = page_share(a);
+    const PageShare sh = page_share<kThreads>(a);
     int used = 0;
     for (int p = sh.first + lane; p - lane < sh.end; p += 128) {
         int r[4];
@@ -454,7 +552,7 @@ pages_compact_kernel(const __grid_constant__ PoolArgs a) {
     used = __reduce_add_sync(~0u, used);
     if (lane == 0) s_used[warp] = used;
     cluster_sync();
-    const int2 count = warp_counts(s_used);
+    const int2 count = warp_counts<kThreads>(s_used);
     const int U = count.y;
     int at = count.x, holes = 0;
     for (int p = sh.first + lane; p - lane < sh.end; p += 128) {
@@ -615,10 +713,11 @@ static fr_status launch(K kernel, int64_t blocks, int threads, int cluster, cuda
     cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }
+constexpr int kWordsEach = 32768;         // (16384 or 65536 for 32885 pages: the same)
 // CTAs of the cluster for so many sequences (kOwn to a thread) and words of refs or tables.
 static int cluster_for(int64_t seqs, int64_t words) {
     int c = 1;
-    while (c < kMaxCluster && ((int64_t)c * kThreads * kOwn < seqs || (int64_t)c * 16384 < words)) c *= 2;
+    while (c < kMaxCluster && ((int64_t)c * kThreads * kOwn < seqs || (int64_t)c * kWordsEach < words)) c *= 2;
     return c;
 }
 static int chunks_of(const PoolDesc& d) { return (d.max_pages + 1023) / 1024; }
@@ -683,8 +782,10 @@ extern "C" fr_status fr_pages_reserve(const fr_page_pool* pool, const int32_t* t
     const fr_status s = on_device(d->dev);
     if (s != FR_OK) return s;
     if (!device_ptr_ok(tok_start, d->dev)) return FR_ERR_INVALID_ARG;
+    if (d->n_seq <= 2 * kFewThreads && d->n_pages <= 16384)
+        return launch(pages_reserve_kernel<kFewThreads>, 1, kFewThreads, 1, stream, pool_args(*d), tok_start);
     const int c = cluster_for(d->n_seq, d->n_pages);
-    return launch(pages_reserve_kernel, c, kThreads, c, stream, pool_args(*d), tok_start);
+    return launch(pages_reserve_kernel<kThreads>, c, kThreads, c, stream, pool_args(*d), tok_start);
 }
 
 extern "C" fr_status fr_pages_fork(const fr_page_pool* pool, const int32_t* parent, const int32_t* child,
@@ -696,8 +797,11 @@ extern "C" fr_status fr_pages_fork(const fr_page_pool* pool, const int32_t* pare
     if (s != FR_OK) return s;
     if (!device_ptr_ok(parent, d->dev) || !device_ptr_ok(child, d->dev) || (length && !device_ptr_ok(length, d->dev)))
         return FR_ERR_INVALID_ARG;
-    const int c = cluster_for(n, (int64_t)n * d->max_pages * 4);
-    return launch(pages_fork_kernel, c, kThreads, c, stream, pool_args(*d), parent, child, length, n);
+    const int64_t entries = (int64_t)n * d->max_pages;
+    if (n <= kFewPairs && entries <= 2048)
+        return launch(pages_fork_kernel<kFewThreads>, 1, kFewThreads, 1, stream, pool_args(*d), parent, child, length, n);
+    const int c = cluster_for(n, 4 * entries);
+    return launch(pages_fork_kernel<kThreads>, c, kThreads, c, stream, pool_args(*d), parent, child, length, n);
 }
 
 extern "C" fr_status fr_pages_free(const fr_page_pool* pool, const int32_t* seq, const int32_t* keep, int n, cudaStream_t stream) {
@@ -764,6 +868,6 @@ extern "C" fr_status fr_pages_copy(const fr_paged_kv* kv_, const fr_page_pool* p
     a.tiles = (int)((words + kCopyTile - 1) / kCopyTile);
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d->dev) != cudaSuccess) return FR_ERR_CUDA;
-    const int64_t most = (int64_t)n_moves_most(d->n_pages, d->n_seq) * 2 * a.tiles, wave = (int64_t)sms * 8;
+    const int64_t most = (int64_t)n_moves_most(d->n_pages, d->n_seq) * 2 * a.tiles, wave = (int64_t)sms * 4;
     return launch(pages_copy_kernel, most < wave ? most : wave, 256, 0, stream, a);
 }
