@@ -110,6 +110,23 @@ __device__ __forceinline__ void load_q(uint32_t dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(dst), "l"((uint64_t)map), "r"(dim), "r"(head), "r"(tok), "r"(bar) : "memory");
 }
+// One lane of a whole warp, as the compiler can see (with lane == 0 in its place it takes
+// an MMA's operands for those of many threads, and moves them one thread after another).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
+}
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Barrier 5 of the softmax's threads: does x hold for one of them?
+template <int N>
+__device__ __forceinline__ bool any_of(bool x) {
+    uint32_t any;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 5, %2, p; selp.u32 %0, 1, 0, q; }"
+                 : "=r"(any) : "r"((uint32_t)x), "n"(N) : "memory");
+    return any != 0;
+}
 // Does a pair of f16 hold an infinity or NaN?
 __device__ __forceinline__ bool odd_half2(uint32_t x) { return (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u; }
 
@@ -298,7 +315,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             if (nq > 0 && !mbar_wait(bar(C::B_QF), (nq - 1) & 1, kLimit)) atomicOr(a.status, kStatusTimeout);
         }
     } else if (warp == kMma) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_s = idesc_f16_f32(128, kBN, 0, 0), id_o = idesc_f16_f32(128, HD, 0, 1);
             const uint32_t q_base = smem_addr(sm + C::Q);
             auto issue_s = [&](int n) {
@@ -444,11 +461,15 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
 #pragma unroll
                     for (int c = 0; c < HB; ++c) x[c] = __fmul_rn(x[c], E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2);
                     if (edge) {
+                        // the keys of these columns that the row sees, a bit each
+                        const int j = key0 + c_base;
+                        uint32_t seen = below(view.y - j) & ~below(view.x - j);
+                        if (SINK) seen |= below(min(a.sink, view.y) - j);
+                        const uint32_t gone = none >> (c_base >> 4);
+                        seen &= ~((gone & 1u ? 0xffffu : 0u) | (gone & 2u ? 0xffff0000u : 0u));
 #pragma unroll
-                        for (int c = 0; c < HB; ++c) {
-                            const int j = key0 + c_base + c;
-                            if ((j < view.x && P::hidden(j, a)) || j >= view.y || (none >> ((c_base + c) >> 4) & 1u)) x[c] = -INFINITY;
-                        }
+                        for (int c = 0; c < HB; ++c)
+                            if (!(seen >> c & 1u)) x[c] = -INFINITY;
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -536,24 +557,33 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     wait(C::B_VF + n % KS, (n / KS) & 1);
                     unsigned char* v = sm + C::V + n % KS * C::TILE;
                     auto at = [&](int i) { return reinterpret_cast<uint4*>(v + (i >> 9) * C::KV_BOX + (i & 511) * 16); };
-                    auto dead = [&](int j) {
-                        return key0 + j >= end.y || (key0 + j < first.x && P::hidden(key0 + j, a)) || (none >> (j >> 4) & 1u);
-                    };
-                    for (int i = tid; i < kBN * HD / 8; i += kSmax) {
-                        const int j = (i & 511) >> 3;
-                        if (dead(j) || (key0 + j < first.y && (key0 + j >= end.x || P::is_sink(key0 + j, a)))) continue;
-                        const uint4 z = *at(i);
-                        if (odd_half2(z.x) || odd_half2(z.y) || odd_half2(z.z) || odd_half2(z.w)) {
-                            s_odd[(n & 1) * kBN + j] = n + 1;
-                            s_piece[piece & 1] = piece + 1;
+                    // (nearly always there are none, and zero weights times finite values are zeros)
+                    bool any_odd = false;
+#pragma unroll
+                    for (int i = 0; i < kBN * HD / 8 / kSmax; ++i) {
+                        const uint4 z = *at(tid + i * kSmax);
+                        any_odd |= odd_half2(z.x) || odd_half2(z.y) || odd_half2(z.z) || odd_half2(z.w);
+                    }
+                    if (any_of<kSmax>(any_odd)) {
+                        auto dead = [&](int j) {
+                            return key0 + j >= end.y || (key0 + j < first.x && P::hidden(key0 + j, a)) || (none >> (j >> 4) & 1u);
+                        };
+                        for (int i = tid; i < kBN * HD / 8; i += kSmax) {
+                            const int j = (i & 511) >> 3;
+                            if (dead(j) || (key0 + j < first.y && (key0 + j >= end.x || P::is_sink(key0 + j, a)))) continue;
+                            const uint4 z = *at(i);
+                            if (odd_half2(z.x) || odd_half2(z.y) || odd_half2(z.z) || odd_half2(z.w)) {
+                                s_odd[(n & 1) * kBN + j] = n + 1;
+                                s_piece[piece & 1] = piece + 1;
+                            }
                         }
+                        asm volatile("bar.sync 5, 256;" ::: "memory");
+                        for (int i = tid; i < kBN * HD / 8; i += kSmax) {
+                            const int j = (i & 511) >> 3;
+                            if (dead(j) || s_odd[(n & 1) * kBN + j] == n + 1) *at(i) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_cta();
                     }
-                    asm volatile("bar.sync 5, 256;" ::: "memory");
-                    for (int i = tid; i < kBN * HD / 8; i += kSmax) {
-                        const int j = (i & 511) >> 3;
-                        if (dead(j) || s_odd[(n & 1) * kBN + j] == n + 1) *at(i) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_cta();
                 }
                 tc_fence_before();
                 __syncwarp();
