@@ -170,7 +170,16 @@ static bool encode_pages(unsigned char* dst, const KvDesc& d, const void* base, 
 // tiles of 16 rows over few long segments run side by side and meet in L2: hd 256,
 // 32 rows, 65536 keys of 1, 2, 4 heads 27 and 30, 37 and 43, 59 and 64; 16 x 8000
 // keys 29 and 32; 64 x 2000 keys 39 and 37.
-static int many_rows(int hd, int type, int64_t segs) {
+// Those calls keep their choice, and with it their sums' order. With sinks, and the 128-row
+// kernel since faster: window 2048, small tiles and one of 128, us, 64 sequences of 4 heads,
+// 16 of 2, 2 of 8:
+//   f16   hd 128, 16 rows 52 and 67, 19 and 21.5, 13.5 and 16; 20 rows 82 and 67, 22.9 and 21.6,
+//         18.8 and 16.2; 32 rows 87 and 69; hd 64, 20 rows 61 and 61, 36 rows 100 and 63; hd 256,
+//         20 rows 162 and 108, 27.4 and 26.6, 19.5 and 19.8; 36 rows 238 and 113, 34 and 27
+//   e4m3  hd 64, 32 rows 76 and 108, 36 rows 115 and 111; hd 128, 32 rows 111 and 140, 36 rows
+//         166 and 142; hd 256, 36 rows 189 and 182, 37 and 39; 64 rows 246 and 185, 45 and 41
+static int many_rows(int hd, int type, int64_t segs, bool sinks) {
+    if (sinks && hd == 128 && type == FR_KV_F16) return 17;
     return hd < 256 ? 33 : type == FR_KV_E4M3 ? 49 : segs >= 32 ? 17 : 33;
 }
 static int max_nt(int hd) { return hd == 256 ? 2 : 4; }
@@ -311,9 +320,12 @@ extern "C" fr_status fr_paged_attn_sinks(const fr_paged_kv* kv_, const fr_paged_
     const int G = n_head / kv->n_kv_head;
     // Row tile: 8 rows for each MMA column block, as many blocks as an average
     // sequence of the batch fills (a longer one takes several row tiles)
+    const int64_t most_keys = (int64_t)bt->max_pages << kv->page_shift;
+    // a window that no sequence outgrows is none (and positions less it stay in 32 bits)
+    const bool windowed = window > 0 && window < most_keys, sinks = windowed && n_sink > 0;
     const int64_t avg = (int64_t)G * ((bt->n_tok + bt->n_seq - 1) / bt->n_seq);
     const int nt = avg <= 8 ? 1 : avg <= 16 ? 2 : max_nt(kv->hd);
-    const bool many = avg >= many_rows(kv->hd, kv->type, (int64_t)bt->n_seq * kv->n_kv_head) && G <= kTcRows;
+    const bool many = avg >= many_rows(kv->hd, kv->type, (int64_t)bt->n_seq * kv->n_kv_head, sinks) && G <= kTcRows;
     const int rt = many ? kTcRows / G * G : 8 * nt;
     const int part_rows = many ? kTcRows : rt;        // rows of a state in the workspace
     // at most this many segments, and units of work, whatever the lengths say
@@ -353,10 +365,8 @@ extern "C" fr_status fr_paged_attn_sinks(const fr_paged_kv* kv_, const fr_paged_
     if (G > 1 && (int64_t)bt->n_tok * G * G < (int64_t{1} << 32)) a.group_magic = (unsigned)(((uint64_t{1} << 32) + G - 1) / G);
     a.row_tile = rt;
     a.causal = causal ? 1 : 0;
-    // a window that no sequence outgrows is none (and positions less it stay in 32 bits)
-    const int64_t most_keys = (int64_t)bt->max_pages << kv->page_shift;
-    a.window = window >= most_keys ? 0 : window;
-    a.sink = a.window == 0 ? 0 : n_sink < most_keys ? n_sink : (int)most_keys;
+    a.window = windowed ? window : 0;
+    a.sink = !sinks ? 0 : n_sink < most_keys ? n_sink : (int)most_keys;
     a.split_by_segment = segs <= ctas ? 1 : 0;
     a.scale_log2 = scale_log2;
     const fr_status st = many                     ? launch_attn_tc(*kv, a, (int)ctas, stream)

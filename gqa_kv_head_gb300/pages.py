@@ -70,9 +70,10 @@ class PagePool:
 def _slots(pool, name, t, n=None):
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
-    if t.device != pool.device:
+    if t.get_device() != pool._index:                   # (-1: not on a GPU)
         raise ValueError(f"{name} must be on the pool's GPU")
-    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+    shape = t.shape
+    if len(shape) != 1 or not t.is_contiguous() or (n is not None and shape[0] != n):
         raise ValueError(f"{name} must be contiguous, one number a slot" if n is None else f"{name} must be contiguous [{n}]")
     return t.data_ptr()
 
