@@ -25,14 +25,18 @@
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
 //
-// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.97 ms,
-// 540 TFLOP/s (P_lo counted: 810). Four prompts of 2048: 350 us in f16 and 629 us
-// in e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 1.1 us in f16, a
-// chain of S, softmax and PV in which none of the units is busy for more than a
-// third; three S tiles in TMEM in place of two were 3-6 % slower up to hd 128.
-// e4m3 is bound by the conversion: two warps took 752 us for the four prompts,
-// one load at a time 875; the same four with the registers split by warpgroup
-// (144 and 112) spilled more and took 657.
+// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.28 ms,
+// 830 TFLOP/s (P_lo counted: 1240). Four prompts of 2048: 260 us in f16 and 496 us in
+// e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 0.77 us in f16, of which the
+// MMAs have 0.4: the rest is the chain S, softmax, P, PV. One lane issues the MMAs, and
+// the compiler has to see that it is one: behind lane == 0 it moves an instruction's
+// operands as those of many threads (1150 cycles for S of a tile; chunks of 512 with
+// sinks 176 us in place of 152). Masks by bits and a look through V before it is cleared
+// took the tiles at the ends of views from 6000 cycles to 2500 (152 -> 129). Slower were
+// 128-key tiles with P in the place of S (161 in place of 129), 16 softmax warps (148),
+// and two Q tiles with S of the next piece ahead (136 in place of 127). The softmax warps
+// find their next piece while the last PV is awaited (f16: 264 -> 260; e4m3, whose
+// registers spill: 496 -> 546, left out).
 #include <string.h>
 
 #include "fr_paged_work.cuh"
@@ -49,10 +53,11 @@ constexpr int kSmax = 256, kProd = 8, kMma = 9, kConv = 10, kConvThreads = 128; 
 // and moves when a score exceeds it by 15 (P_lo off f16's subnormals, P_hi within f16).
 constexpr float kBelow = 7.0f, kAbove = 15.0f;
 constexpr uint64_t kLimit = 2000000000ull;
-// The MMA's accumulator drops bits at each of a tile's 8 steps, always towards zero: after
-// 264 steps rows are 4e-6 too small. With sinks (calls without keep their sums' order) and
+// The MMA's accumulator drops bits at each step of 16 keys, always towards zero: after
+// 2064 keys rows are 4e-6 too small. With sinks (calls without keep their sums' order) and
 // up to hd 128 the softmax warps add O to sums of their own in TMEM after so many tiles,
-// and it starts anew: 5e-7, for F_COST.
+// and it starts anew. Chunks of 512, window 2048: error 2.0e-6 of 64 bits without, 6.5e-7
+// with sums every 4 tiles, 8.5e-7 every 8; 173.7, 176.2 us then (now 127.4 and 124.9 for 4 and 8).
 constexpr int kSumTiles = 4;
 
 template <int HD, bool E4>
@@ -67,7 +72,7 @@ struct Cfg {
     static constexpr int Q = 0, K = 128 * HD * 2, V = K + KS * TILE, RAW = V + KS * TILE,
                          AUX = RAW + RS * RAW_BYTES;
     // auxiliary area: half-row maxima and sums, walks, scan, tiles' pages, odd rows of V, barriers
-    static constexpr int A_MAX = 0, A_L = 2048, A_WALK = A_L + 1024, A_SCAN = A_WALK + 64 * 17, A_META = A_SCAN + 256,
+    static constexpr int A_MAX = 0, A_L = 2048, A_WALK = A_L + 1024, A_SCAN = A_WALK + 64 * 25, A_META = A_SCAN + 256,
                          A_ODD = A_META + 16 * 64, A_BAR = A_ODD + 528, AUX_BYTES = A_BAR + 512;
     static constexpr int SMEM = AUX + AUX_BYTES + 1024;
     static_assert(SMEM <= 232448, "shared memory");
@@ -117,6 +122,19 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
     return one != 0;
 }
+// Two products and two sums at a time, each rounded as one alone would be.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 // Barrier 5 of the softmax's threads: does x hold for one of them?
@@ -160,7 +178,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     unsigned char* aux = sm + C::AUX;
     float* s_max = reinterpret_cast<float*>(aux + C::A_MAX);             // [2][2][128]
     float* s_l = reinterpret_cast<float*>(aux + C::A_L);                 // [2][128]
-    Walk* walks = reinterpret_cast<Walk*>(aux + C::A_WALK);              // the share's start, then one for each warp
+    Walk* walks = reinterpret_cast<Walk*>(aux + C::A_WALK);              // the share's start, one for each warp, from 17 on a second for the softmax's
     int* scan = reinterpret_cast<int*>(aux + C::A_SCAN);
     Meta* s_meta = reinterpret_cast<Meta*>(aux + C::A_META);             // [16]
     // Odd rows of V, two deep: one warp may be a tile, or a piece, ahead of another
@@ -424,6 +442,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
         const int qd = warp & 3, half = warp >> 2, r = qd * 32 + lane, c_base = half * HB;
         const uint32_t lanes = (uint32_t)(qd * 32) << 16;
         int n = 0, piece = 0;
+        Walk* next = walks + 17 + warp;
         for (;;) {
             const int2 t = walk_tiles<P>(*w, 0);
             const Seg& s = w->s;
@@ -459,7 +478,12 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     tmem_ld_x32(tbase + lanes + C::T_S + (n & 1) * kBN + c_base, reinterpret_cast<uint32_t*>(x));
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < HB; ++c) x[c] = __fmul_rn(x[c], E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2);
+                    for (int c = 0; c < HB; c += 2) {
+                        const float f = E4 ? a.scale_log2 * m.ks[half * 2 + c / 16] : a.scale_log2;
+                        const float2 y = mul2(make_float2(x[c], x[c + 1]), make_float2(f, f));
+                        x[c] = y.x;
+                        x[c + 1] = y.y;
+                    }
                     if (edge) {
                         // the keys of these columns that the row sees, a bit each
                         const int j = key0 + c_base;
@@ -498,6 +522,32 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     v_step[1] *= v_inv;
                 }
                 if (active) {
+                    const float sub = m_new == -INFINITY ? 0.f : m_new;
+                    const float2 less = make_float2(-sub, -sub);
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                    float2 sums[4] = {};
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int c = 0; c < HB; c += 2) {
+                        const float2 y = add2(make_float2(x[c], x[c + 1]), less);
+                        float2 w = make_float2(ex2(y.x), ex2(y.y));
+                        if (SINK) sums[(c >> 1) & 3] = add2(sums[(c >> 1) & 3], w);
+                        else s4[(c >> 1) & 3] += w.x + w.y;
+                        if (E4) w = mul2(w, make_float2(v_step[c / 16], v_step[c / 16]));
+                        hi[c / 2] = pack_half2(w.x, w.y);
+                        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi[c / 2]));
+                        const float2 rest = add2(w, make_float2(-hf.x, -hf.y));
+                        lo[c / 2] = pack_half2(rest.x, rest.y);
+                    }
+                    if (SINK) {
+                        const float2 all = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
+                        l = fmaf(l, alpha, all.x + all.y);
+                    } else {
+                        l = fmaf(l, alpha, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+                    }
+                    tmem_st_x16(tbase + lanes + C::T_P + (n & 1) * HB + half * 16, hi);
+                    tmem_st_x16(tbase + lanes + C::T_PL + (n & 1) * HB + half * 16, lo);
+                    // (behind the weights: PV of the tile before has had their time)
                     const int i = tile - t.x;
                     const bool sum = SUMS && i > 0 && i % kSumTiles == 0;            // O goes into the sums
                     if ((__any_sync(~0u, grown || v_up) || sum) && i > 0) {
@@ -529,26 +579,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                             for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * o_scale);
                             tmem_st_x32(tbase + lanes + C::T_O + half * OH + c, o);
                         }
-                        tmem_wait_st();
                     }
-                    const float sub = m_new == -INFINITY ? 0.f : m_new;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int c = 0; c < HB; c += 2) {
-                        float p0 = ex2(__fsub_rn(x[c], sub)), p1 = ex2(__fsub_rn(x[c + 1], sub));
-                        s4[(c >> 1) & 3] += p0 + p1;
-                        if (E4) {
-                            p0 *= v_step[c / 16];
-                            p1 *= v_step[c / 16];
-                        }
-                        hi[c / 2] = pack_half2(p0, p1);
-                        const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi[c / 2]));
-                        lo[c / 2] = pack_half2(p0 - hf.x, p1 - hf.y);
-                    }
-                    tmem_st_x16(tbase + lanes + C::T_P + (n & 1) * HB + half * 16, hi);
-                    tmem_st_x16(tbase + lanes + C::T_PL + (n & 1) * HB + half * 16, lo);
-                    l = fmaf(l, alpha, (s4[0] + s4[1]) + (s4[2] + s4[3]));
                     tmem_wait_st();
                 }
                 m_ref = m_new;
@@ -591,6 +622,10 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             }
             // ---- the piece's end ------------------------------------------------
             const bool any = t.x < t.y;
+            if (!E4) {
+                if (lane == 0) walk_on<P>(w, next, &a);             // (while PV of the last tile is awaited; see the figures above)
+                __syncwarp();
+            }
             if (any) {
                 wait(C::B_OF, piece & 1);
                 __syncwarp();
@@ -674,8 +709,14 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 ++piece;
             }
             __syncwarp();
-            if (lane == 0) walk_on<P>(w, w, &a);
-            __syncwarp();
+            if (E4) {
+                if (lane == 0) walk_on<P>(w, w, &a);
+                __syncwarp();
+            } else {
+                Walk* const was = w;
+                w = next;
+                next = was;
+            }
             if (!w->more) break;
         }
     }
