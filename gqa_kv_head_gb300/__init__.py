@@ -1,8 +1,9 @@
 """GB300 (sm_103a) decode-attention hot path for a ggml host: qkv_post (NEOX
 RoPE with YaRN, scale, f16 t-major Q rows) and the collapsed GQA decode
 attention over one shared f16 KV head, and the same step over a paged f16 or
-e4m3 K/V cache of several sequences and KV heads, behind the C ABI in
-include/fr_kernels.h.
+e4m3 K/V cache of several sequences and KV heads (rows normed and rotated into the
+pages, attention with windows and sinks, the pages' own bookkeeping), behind the C
+ABI in include/fr_kernels.h.
 
 The kernels live in csrc/ and build into _build/libfr_gb300.so (build.py).
 This Python layer only marshals arguments (ops.py over ctypes, _abi.py).

@@ -1,6 +1,7 @@
 // fr_paged.h -- host-side pieces shared by the paged-cache entry points
 // (fr_paged.cu: descriptors, checks and the merge kernel; fr_paged_append.cu:
-// the append; fr_paged_attn_*.cu: the attention kernels).
+// the append; fr_paged_qkv*.cu: the step's rows; fr_paged_pool.cu: the pages'
+// bookkeeping; fr_paged_attn_*.cu, fr_paged_tc.cu: the attention kernels).
 #pragma once
 
 #include <cuda.h>

@@ -12,12 +12,24 @@
 // same for all its heads, and at about 100 instructions an angle they are what is
 // left to save: a thread keeps the cosines and sines of its place in registers
 // and takes head after head through them.
-//   * Prompts into f16 pages (tokens_kernel): blocks of 256 threads take a tile of
-//     tokens and a part of the list of all heads, queries, keys and values; the
-//     pages of the tokens are looked up by their warps.
-//   * e4m3 pages: a page has its scale from all its rows, so keys and values go by
-//     pieces of pages as in the append (fr_paged_rows.cuh), query heads by tiles of
-//     tokens in the blocks behind.
+//   * Prompts into f16 pages (qkv_post_tokens_kernel): blocks of 64 threads take a
+//     tile of tokens and a part of the list of all heads, queries, keys and values;
+//     the pages of the tokens are looked up by their warps. A thread asks for its part
+//     of the next four heads by cp.async, into places of its own, so that the bytes on
+//     their way need no registers and nobody waits for anybody. 6005 bf16 tokens of 32
+//     query and 8 KV heads of 128 (148 MB): 30.1 us, 4.9 TB/s. On the way there: heads
+//     through registers, keys and values by pieces beside them 36.7; one list through
+//     registers 37 to 46 (too little on its way); the ring in blocks of 256 threads 33
+//     to 34, of 64 threads 31.8, and with registers for ten of them on an SM 29.7 (6
+//     places; 4 places 30.8, 10 places 35.6). Reading and writing the query rows alone
+//     takes 17.4, with norms and rotation 24, of which the angles are 4.2.
+//   * e4m3 pages (qkv_post_prompt_kernel): a page has its scale from all its rows, so
+//     keys and values go by pieces of pages as in the append (fr_paged_rows.cuh), with
+//     as few rows of a thread, and as many heads at a time, as the page allows; query
+//     heads by tiles of tokens through the ring. The two kinds of blocks take turns.
+//     4980 f32 tokens of 15 query and 5 KV heads of 64, 32-row pages (45 MB): 18.5 us
+//     (four rows of a thread, kinds one after the other: 24); queries alone 11.7, keys
+//     and values alone 12 to 13: instructions and the latency of a piece bound it.
 //   * Decode steps: the same two kinds of blocks, of 64 threads, one head each.
 #pragma once
 
