@@ -26,10 +26,15 @@
 //   * e4m3 pages (qkv_post_prompt_kernel): a page has its scale from all its rows, so
 //     keys and values go by pieces of pages as in the append (fr_paged_rows.cuh), with
 //     as few rows of a thread, and as many heads at a time, as the page allows; query
-//     heads by tiles of tokens through the ring. The two kinds of blocks take turns.
-//     4980 f32 tokens of 15 query and 5 KV heads of 64, 32-row pages (45 MB): 18.5 us
+//     heads through the ring by tiles of tokens, a warp to a token, whose lanes share
+//     the angles out and hand them around. The two kinds of blocks take turns.
+//     4980 f32 tokens of 15 query and 5 KV heads of 64, 32-row pages (45 MB): 18.4 us
 //     (four rows of a thread, kinds one after the other: 24); queries alone 11.7, keys
 //     and values alone 12 to 13: instructions and the latency of a piece bound it.
+//     The case of 6005 bf16 tokens above in 64-row e4m3 pages 37.4 (each lane with all
+//     its angles 39.8). 8 or 16 rows of a page to each of 256 threads are blocks of 512
+//     instead, 16 with the angles in shared memory: 128-row pages 48.0 (by pieces of a
+//     head 68.1), and f32, hd 256, 16 query and 2 KV heads 43.7 (50.6).
 //   * Decode steps: the same two kinds of blocks, of 64 threads, one head each.
 #pragma once
 
@@ -305,15 +310,26 @@ __device__ __forceinline__ Place find_tokens(const AppendArgs& a, int t, bool wa
 
 // A tile of tokens and heads h0 .. of the list: queries, and where PAGES (f16) keys and
 // values behind them. NT: threads of a ring in shared memory (0: none).
-template <typename T, int HD, int E, bool PAGES, int NT>
+// SHARE: the lanes of a warp hold one token, 32 / ITEMS heads at a time, work out its
+// angles together and hand them around (PAGES: not so).
+template <typename T, int HD, int E, bool PAGES, int NT, bool SHARE = false>
 __device__ __forceinline__ void token_rows(const QkvArgs& g, const RopeTable& tb, int tile, int h0) {
     constexpr int ITEMS = HD / E, P = E / 2;
     constexpr bool RING = NT > 0;
+    constexpr int EACH = SHARE ? 32 / ITEMS : 1, LANES = ITEMS * EACH;      // heads at a time, lanes of a token
+    static_assert(!SHARE || (RING && !PAGES && P % EACH == 0), "");
     const AppendArgs& a = g.kv;
-    const int c = threadIdx.x % ITEMS, t_ = tile * (int)(blockDim.x / ITEMS) + threadIdx.x / ITEMS, t = min(t_, a.n_tok - 1);
+    const int c = threadIdx.x % ITEMS, nth = threadIdx.x % LANES / ITEMS;
+    const int t_ = tile * (int)(blockDim.x / LANES) + threadIdx.x / LANES, t = min(t_, a.n_tok - 1);
     Angles angles[P / 4];
+    uint64_t turns[P / EACH];
+    if (SHARE) {
 #pragma unroll
-    for (int i = 0; i < P / 4; ++i) angles[i].get(tb, c * (P / 4) + i);
+        for (int i = 0; i < P / EACH; ++i) turns[i] = tb.turns[min(c * P + nth + i * EACH, kMaxPairs - 1)];
+    } else {
+#pragma unroll
+        for (int i = 0; i < P / 4; ++i) angles[i].get(tb, c * (P / 4) + i);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int n_real = a.tok_start[a.n_seq], pos = a.pos[t];
@@ -332,11 +348,17 @@ __device__ __forceinline__ void token_rows(const QkvArgs& g, const RopeTable& tb
     constexpr int PART = P * (int)sizeof(T), STAGE = 2 * PART * NT;
     unsigned char* const mine = ring + threadIdx.x * (PART < 16 ? PART : 16);
     const uint32_t ring_u = RING ? smem_u32(mine) : 0u;
-    int ask_left = here ? h1 - h0 : 0, ask_kind = -1, ask_kind_left = 0, ask_d = 0;   // heads to ask for, in all and of their kind
+    int ask_left = here ? (h1 - h0 - nth + EACH - 1) / EACH : 0, ask_kind = -1, ask_kind_left = 0, ask_d = 0;   // heads to ask for, in all and of their kind
     const T* ask_at = nullptr;
     uint32_t ask_to = 0;
     auto ask = [&]() {
         if (ask_left > 0) {
+            if (ask_kind_left == 0 && SHARE) {
+                const Dims<E> d(c, r.half, r.together);
+                ask_at = source(0) + (int64_t)(h0 + nth) * HD + d.d0;
+                ask_d = d.d1 - d.d0;
+                ask_kind_left = ask_left;
+            }
             if (ask_kind_left == 0) {
                 int head;                                 // the next kind that has some of the heads
                 do {
@@ -350,7 +372,7 @@ __device__ __forceinline__ void token_rows(const QkvArgs& g, const RopeTable& tb
             }
             ring_copy<PART, NT>(ring_u + ask_to, ask_at);
             ring_copy<PART, NT>(ring_u + ask_to + PART * NT, ask_at + ask_d);
-            ask_at += HD;
+            ask_at += EACH * HD;
             ask_to = ask_to == (kStages - 1) * STAGE ? 0 : ask_to + STAGE;
             --ask_left;
             --ask_kind_left;
@@ -377,6 +399,17 @@ __device__ __forceinline__ void token_rows(const QkvArgs& g, const RopeTable& tb
     if (!here) return;
     float2 cs[RING ? 1 : P];
     float2* angle = RING ? reinterpret_cast<float2*>(ring + kStages * STAGE) + threadIdx.x : cs;      // a place of its own too
+    if (SHARE) {
+#pragma unroll
+        for (int i = 0; i < P / EACH; ++i) {
+            const int pair = c * P + nth + i * EACH;
+            float2 x = make_float2(1.f, 0.f);
+            if (pair < tb.half) x = tb.mode == FR_ROPE_GGML_F32 ? rope_cs_f32(pos, pair, &tb) : rope_cs_fixed(pos, turns[i], tb.mscale);
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+                angle[(i * EACH + k) * NT] = make_float2(__shfl_sync(~0u, x.x, k * ITEMS + c), __shfl_sync(~0u, x.y, k * ITEMS + c));
+        }
+    } else
 #pragma unroll
     for (int u = 0; u < P; ++u)
         angle[u * (RING ? NT : 1)] = c * P + u < tb.half ? angles[u / 4].at(pos, c * (P / 4) + u / 4, u % 4, tb) : make_float2(1.f, 0.f);
@@ -393,10 +426,10 @@ __device__ __forceinline__ void token_rows(const QkvArgs& g, const RopeTable& tb
         for (int u = 0; u < P; ++u) own[u] = angle[u * NT];
         const Dims<E> d(c, r.half, r.together);
         const Turner<HD, E, decltype(normed)::value> turner(r, c, d, own);
-        __half* dst = r.dst + from * r.dst_head + d.d0;
+        __half* dst = r.dst + (from + nth) * r.dst_head + d.d0;
         const int dd = d.d1 - d.d0;
 #pragma unroll 1
-        for (int n = to - from; n > 0; --n) {
+        for (int n = to - from - nth; n > 0; n -= EACH) {
             cp_async_wait<kStages - 2>();
             Part<T, P> raw[2];
             raw[0].template shared<NT>(mine + slot);
@@ -409,7 +442,7 @@ __device__ __forceinline__ void token_rows(const QkvArgs& g, const RopeTable& tb
             turner(r, c, y);
             store_halves<P>(dst, y);
             store_halves<P>(dst + dd, y + P);
-            dst += r.dst_head;
+            dst += EACH * r.dst_head;
         }
     };
 #pragma unroll 1
@@ -458,9 +491,10 @@ qkv_post_tokens_kernel(const __grid_constant__ QkvArgs g, const __grid_constant_
     if (sizeof(T) == 2 && g.wide) token_rows<T, HD, 16, true, kTokenThreads>(g, tb, tile, h0);
     else token_rows<T, HD, 8, true, kTokenThreads>(g, tb, tile, h0);
 }
-// Prompts into e4m3 pages: pieces of a page, KR rows of it to a thread.
-template <typename T, int HD, int KR>
-__global__ void __launch_bounds__(256, KR == 1 && sizeof(T) == 4 ? 3 : 2)
+// Prompts into e4m3 pages: pieces of a page, KR rows of it to a thread (0: page too large,
+// its heads one at a time).
+template <typename T, int HD, int KR, int NT>
+__global__ void __launch_bounds__(NT, NT > 256 ? 1 : KR == 1 && sizeof(T) == 4 ? 3 : 2)
 qkv_post_prompt_kernel(const __grid_constant__ QkvArgs g, const __grid_constant__ RopeTable tb) {
     // the two kinds of blocks take turns while there are both: pieces wait, tiles stream
     const int b = blockIdx.x, both = 2 * min(g.kv_blocks, (int)gridDim.x - g.kv_blocks);
@@ -468,12 +502,16 @@ qkv_post_prompt_kernel(const __grid_constant__ QkvArgs g, const __grid_constant_
     const int nth_block = b < both ? b >> 1 : b - both / 2;
     if (piece) {
         const int i = nth_block >> 1, nth = i / g.kv_groups;
-        append_prompt<T, HD, true, true, KR, (sizeof(T) == 4 ? 4 : 8) / KR>(g.kv, tb, g.k_norm, g.kv.page_shift, g.kv_heads,
-                                                                              nth_block & 1, nth, (i - nth * g.kv_groups) * g.kv_heads);
+        const int h0 = (i - nth * g.kv_groups) * g.kv_heads;
+        if (KR > 0)
+            append_prompt<T, HD, true, true, KR ? KR : 1, KR < 8 ? (sizeof(T) == 4 ? 4 : 8) / (KR ? KR : 1) : 1, NT>(
+                g.kv, tb, g.k_norm, g.kv.page_shift, g.kv_heads, nth_block & 1, nth, h0);
+        else
+            append_piece<T, HD, true, 4, true>(g.kv, tb, g.k_norm, nth_block & 1, nth, h0);
     } else {
         const int i = nth_block, tile = i / g.groups, h0 = (i - tile * g.groups) * g.heads;
-        if (sizeof(T) == 2 && g.wide) token_rows<T, HD, 16, false, 256>(g, tb, tile, h0);
-        else token_rows<T, HD, 8, false, 256>(g, tb, tile, h0);
+        if (sizeof(T) == 2 && g.wide) token_rows<T, HD, 16, false, NT, true>(g, tb, tile, h0);
+        else token_rows<T, HD, 8, false, NT, true>(g, tb, tile, h0);
     }
 }
 
@@ -482,27 +520,29 @@ qkv_post_prompt_kernel(const __grid_constant__ QkvArgs g, const __grid_constant_
 template <typename T, int HD, int which, int NT, typename K>
 static fr_status launch_ring(K kernel, int64_t blocks, cudaStream_t st, const QkvArgs& g, const RopeTable& tb) {
     static unsigned long long done = 0ull;
-    constexpr int wide = ring_bytes<T, sizeof(T) == 2 ? 16 : 8, NT>();
+    constexpr int ring = ring_bytes<T, sizeof(T) == 2 ? 16 : 8, NT>(), kept = which == 16 ? 8 * 4 * 8 * NT : 0;      // (angles of eight rows)
+    constexpr int wide = ring > kept ? ring : kept, narrow = ring_bytes<T, 8, NT>() > kept ? ring_bytes<T, 8, NT>() : kept;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FR_ERR_CUDA;
     if (dev >= 64 || !(__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev & 1ull)) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide) != cudaSuccess) return FR_ERR_CUDA;
         if (dev < 64) __atomic_fetch_or(&done, 1ull << dev, __ATOMIC_RELEASE);
     }
-    const cudaError_t e = launch_smem(kernel, blocks, 1, NT, g.wide || sizeof(T) == 4 ? wide : ring_bytes<T, 8, NT>(), st, g, tb);
+    const cudaError_t e = launch_smem(kernel, blocks, 1, NT, g.wide || sizeof(T) == 4 ? wide : narrow, st, g, tb);
     return e == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }
 template <typename T, int HD, bool E4>
 static fr_status launch_qkv(QkvArgs g, const RopeTable& tb, cudaStream_t st) {
     const AppendArgs& a = g.kv;
     const bool decode = a.n_tok <= 2 * a.n_seq, together = g.q_norm.interleaved != 0;
-    // rows of a page that a thread of an e4m3 block has
+    // rows of a page that each of an e4m3 block's 256 threads has
     const int kr = ((HD / 8) << a.page_shift) / 256, rows = kr < 2 ? 1 : kr;
-    const bool prompt = !decode && tb.n_dims % 8 == 0 && (!E4 || rows <= 4);
-    const int threads = decode ? 64 : prompt && !E4 ? kTokenThreads : 256;
+    const bool prompt = !decode && tb.n_dims % 8 == 0;
+    const int threads = decode ? 64 : prompt && !E4 ? kTokenThreads : prompt && (rows == 8 || rows == 16) ? 512 : 256;
     // (16 elements to a thread take fewer shuffles and addresses; a decode step would wait for twice the angles)
     g.wide = prompt && sizeof(T) == 2 && (together || tb.n_dims % 16 == 0);
-    const int per = threads / (HD / (g.wide ? 16 : 8));
+    const int lanes = HD / (g.wide ? 16 : 8), each = prompt && E4 ? 32 / lanes : 1;     // of a token's head; heads at a time
+    const int per = threads / (lanes * each);
     const int64_t tiles = (a.n_tok + per - 1) / per;
     // a block has as many heads as leave enough blocks
     auto cut = [](int64_t pieces, int heads, int64_t blocks, int least, int* of_block, int* groups) {
@@ -513,13 +553,15 @@ static fr_status launch_qkv(QkvArgs g, const RopeTable& tb, cudaStream_t st) {
         *of_block = (heads + *groups - 1) / *groups;
     };
     const int all = g.n_head + (prompt && !E4 ? 2 * a.n_kv_head : 0);
-    cut(tiles, all, kBlocks, decode ? 1 : 4, &g.heads, &g.groups);
+    cut(tiles, all, kBlocks, decode ? 1 : 4 * each, &g.heads, &g.groups);
     int64_t kv_blocks = 0;
     if (!prompt) {
         kv_blocks = 2 * most_pieces(a, a.page_shift) * a.n_kv_head;
     } else if (E4) {
         const int64_t pieces = 2 * most_pieces(a, a.page_shift);
-        cut(pieces, a.n_kv_head, kBlocks / 2, (sizeof(T) == 4 ? 4 : 8) / rows, &g.kv_heads, &g.kv_groups);
+        const int least = rows == 16 ? 1 : (sizeof(T) == 4 ? 4 : 8) / (rows < 4 ? rows : 4);      // heads at a time
+        if (rows <= 16) cut(pieces, a.n_kv_head, kBlocks / 2, least, &g.kv_heads, &g.kv_groups);
+        else g.kv_heads = 1, g.kv_groups = a.n_kv_head;
         kv_blocks = pieces * g.kv_groups;
     }
     const int64_t blocks = kv_blocks + tiles * g.groups;
@@ -529,9 +571,17 @@ static fr_status launch_qkv(QkvArgs g, const RopeTable& tb, cudaStream_t st) {
     if (decode) e = launch(qkv_post_paged_kernel<T, HD, E4, 1>, blocks, 1, threads, st, g, tb);
     else if (!prompt) e = launch(qkv_post_paged_kernel<T, HD, E4, 4>, blocks, 1, threads, st, g, tb);
     else if (!E4) return launch_ring<T, HD, 0, kTokenThreads>(qkv_post_tokens_kernel<T, HD>, blocks, st, g, tb);
-    else if (rows == 1) return launch_ring<T, HD, 1, 256>(qkv_post_prompt_kernel<T, HD, 1>, blocks, st, g, tb);
-    else if (rows == 2) return launch_ring<T, HD, 2, 256>(qkv_post_prompt_kernel<T, HD, 2>, blocks, st, g, tb);
-    else return launch_ring<T, HD, 4, 256>(qkv_post_prompt_kernel<T, HD, 4>, blocks, st, g, tb);
+    else if (rows == 1) return launch_ring<T, HD, 1, 256>(qkv_post_prompt_kernel<T, HD, 1, 256>, blocks, st, g, tb);
+    else if (rows == 2) return launch_ring<T, HD, 2, 256>(qkv_post_prompt_kernel<T, HD, 2, 256>, blocks, st, g, tb);
+    else if (rows == 4) return launch_ring<T, HD, 4, 256>(qkv_post_prompt_kernel<T, HD, 4, 256>, blocks, st, g, tb);
+    else if (rows == 8) return launch_ring<T, HD, 8, 512>(qkv_post_prompt_kernel<T, HD, 4, 512>, blocks, st, g, tb);
+    else {                                // (pages of at most 256 rows)
+        if constexpr (HD >= 128)
+            if (rows == 16) return launch_ring<T, HD, 16, 512>(qkv_post_prompt_kernel<T, HD, 8, 512>, blocks, st, g, tb);
+        if constexpr (HD >= 256)
+            return launch_ring<T, HD, 32, 256>(qkv_post_prompt_kernel<T, HD, 0, 256>, blocks, st, g, tb);
+        return FR_ERR_UNSUPPORTED;
+    }
     return e == cudaSuccess ? FR_OK : FR_ERR_CUDA;
 }
 template <typename T, int HD>

@@ -460,8 +460,8 @@ __device__ __forceinline__ void append_piece(const AppendArgs& a, const RopeTabl
 
 // Prompts, n_dims a multiple of 8. A thread has place c of KR rows and takes the
 // block's heads through them, HC heads' loads at a time; the angles are computed
-// while the first of these are on their way. e4m3: KR = 4 rows, so a page has at
-// most 1024 items (64 rows at hd 128). Measured on 5000 tokens of 8 heads of hd
+// while the first of these are on their way. The append into e4m3: KR = 4 rows, so a
+// page has at most 1024 items (64 rows at hd 128). Measured on 5000 tokens of 8 heads of hd
 // 128 in 64-row pages, f16 rows: 15.7 us with 256 threads of 4 rows, two heads at
 // a time; 17.7 with 512 threads of 2 rows and 4 heads, 22 with 1024 of one row.
 template <typename T, bool E4>
@@ -470,11 +470,12 @@ struct Prompt {
     static constexpr int HC = (E4 ? 2 : 8) / (sizeof(T) == 4 ? 2 : 1);
 };
 // Piece `nth` (of 2^shift rows) of heads h0 .. h0 + heads - 1.
-// KR rows of a thread, HC heads at a time.
-template <typename T, int HD, bool E4, bool EXT, int KR, int HC>
+// KR rows of a thread, HC heads at a time, NTH threads; of more than four rows the angles
+// lie in shared memory, 32 KR bytes a thread.
+template <typename T, int HD, bool E4, bool EXT, int KR, int HC, int NTH = Prompt<T, E4>::THREADS>
 __device__ __forceinline__ void append_prompt(const AppendArgs& a, const RopeTable& tb, const Norm& nm, int shift, int heads,
                                               bool is_v, int nth, int h0) {
-    constexpr int ITEMS = HD / 8, NTH = Prompt<T, E4>::THREADS;
+    constexpr int ITEMS = HD / 8;
     using V = typename Raw<T>::V;
     __shared__ float red[2][HC][NTH / 32];
     Angles angles;
@@ -520,12 +521,20 @@ __device__ __forceinline__ void append_prompt(const AppendArgs& a, const RopeTab
     const bool bad_page = page < 0 || page >= a.n_pages;
     if (bad_page && tid == 0 && a.status) atomicOr(a.status, kStatusInput);
     if (bad_page) return;
-    float2 cs[KR][4];
+    // (of more than four rows: in places of the thread's own in shared memory)
+    constexpr bool KEPT = KR <= 4;
+    extern __shared__ __align__(16) unsigned char prompt_sm[];
+    float2 cs[KEPT ? KR : 1][4], *const cs_at = reinterpret_cast<float2*>(prompt_sm) + tid;
     if (rot)
 #pragma unroll
         for (int k = 0; k < KR; ++k)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) cs[k][u] = angles.at(pos[k], c, u, tb);
+            for (int u = 0; u < 4; ++u) {
+                const float2 x = angles.at(pos[k], c, u, tb);
+                if (KEPT) cs[KEPT ? k : 0][u] = x;
+                else cs_at[(k * 4 + u) * NTH] = x;
+            }
+    auto angle = [&](int k, int u) { return KEPT ? cs[KEPT ? k : 0][u] : cs_at[(k * 4 + u) * NTH]; };
     float rms[EXT ? HC : 1][EXT ? KR : 1];                 // the rows' factors, taken once
     unsigned small = 0u;
     auto values = [&](int j, int k, float* y, bool again = false) {
@@ -544,11 +553,11 @@ __device__ __forceinline__ void append_prompt(const AppendArgs& a, const RopeTab
         if (!rot) return;
         if (EXT && together) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) rotate(y[2 * u], y[2 * u + 1], cs[k][u]);
+            for (int u = 0; u < 4; ++u) rotate(y[2 * u], y[2 * u + 1], angle(k, u));
             return;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) rotate(y[u], y[4 + u], cs[k][u]);
+        for (int u = 0; u < 4; ++u) rotate(y[u], y[4 + u], angle(k, u));
     };
     const int64_t p_base = page * (is_v ? a.v_page : a.k_page);
     for (int h = h0; h < h1; h += HC) {

@@ -162,6 +162,15 @@ def test_page_sizes_and_layouts(kind, ps, nhd, hd):
     run_case(kind, "bf16", hd, 2, 2, ps, [90, 1, 300], [200, 33, 310], seed=ps, nhd=nhd, pad=64)
 
 
+# 8, 16 and 32 rows of a page to a thread of 256, pages begun by earlier rows, odd numbers of heads
+@pytest.mark.parametrize("rows", ["f32", "f16"])
+@pytest.mark.parametrize("hd,ps", [(64, 256), (128, 128), (128, 256), (256, 64), (256, 128), (256, 256)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_large_pages(rows, hd, ps, interleaved):
+    run_case("e4m3", rows, hd, 3, 3, ps, [5, 0, 290, 77], [ps + 8, 40, 290 + ps // 2, 77], {"n_dims": hd // 2}, seed=hd + ps,
+             interleaved=interleaved, pad=8)
+
+
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("H,G", [(1, 1), (1, 7), (5, 1), (8, 4), (1, 64)])
 def test_head_counts(kind, H, G):
