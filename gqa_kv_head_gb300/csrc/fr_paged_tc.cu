@@ -25,8 +25,8 @@
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
 //
-// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.28 ms,
-// 830 TFLOP/s (P_lo counted: 1240). Four prompts of 2048: 260 us in f16 and 496 us in
+// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.29 ms,
+// 830 TFLOP/s (P_lo counted: 1240). Four prompts of 2048: 244 us in f16 and 495 us in
 // e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 0.77 us in f16, of which the
 // MMAs have 0.4: the rest is the chain S, softmax, P, PV. One lane issues the MMAs, and
 // the compiler has to see that it is one: behind lane == 0 it moves an instruction's
@@ -36,7 +36,9 @@
 // 128-key tiles with P in the place of S (161 in place of 129), 16 softmax warps (148),
 // and two Q tiles with S of the next piece ahead (136 in place of 127). The softmax warps
 // find their next piece while the last PV is awaited (f16: 264 -> 260; e4m3, whose
-// registers spill: 496 -> 546, left out).
+// registers spill: 496 -> 546, left out). Results leave 32 bytes at a time: a thread
+// has a row, so each store of a warp is 32 accesses (16 bytes at a time: 260 -> 244;
+// e4m3 of hd 256 567 -> 536, of hd 64 and 128 spills moved into the loop: 496 -> 537).
 #include <string.h>
 
 #include "fr_paged_work.cuh"
@@ -121,6 +123,11 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
     return one != 0;
+}
+// 32 bytes, a whole sector, at once.
+__device__ __forceinline__ void store_8(float* p, const float* x) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" :: "l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
+                 "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]) : "memory");
 }
 // Two products and two sums at a time, each rounded as one alone would be.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -693,10 +700,21 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                                 for (int u = 0; u < 32; ++u) o[u] = fmaf(p, page_value<E4>(pg.v, v + half * OH + c + u), o[u]);
                             }
                         }
+float* const to = dst + half * OH + c;
+                        if ((E4 && HD < 256) || ((uintptr_t)to & 31)) {
 #pragma unroll
-                        for (int u = 0; u < 32; u += 4)
-                            *reinterpret_cast<float4*>(dst + half * OH + c + u) =
-                                make_float4(o[u] * f_v * f, o[u + 1] * f_v * f, o[u + 2] * f_v * f, o[u + 3] * f_v * f);
+                            for (int u = 0; u < 32; u += 4)
+                                *reinterpret_cast<float4*>(to + u) =
+                                    make_float4(o[u] * f_v * f, o[u + 1] * f_v * f, o[u + 2] * f_v * f, o[u + 3] * f_v * f);
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 32; u += 8) {
+                                float y[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[i] = o[u + i] * f_v * f;
+                                store_8(to + u, y);
+                            }
+                        }
                     }
                     __syncwarp();
                 }

@@ -224,3 +224,21 @@ def test_refusals():
         with pytest.raises(fr.FrError):
             fr.paged_attn(cache, batch, q, 1, **kw)
     assert torch.equal(fr.paged_attn(cache, batch, q, 1, window=4, sinks=2 ** 40), fr.paged_attn(cache, batch, q, 1))
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("sinks", [0, 9])
+@pytest.mark.parametrize("off", [4, 8, 12])
+def test_output_begins_anywhere_on_16_bytes(kind, hd, sinks, off):
+    """Whole and split pieces of 128-row tiles, stored 32 or 16 bytes at a time: the same bits, and nothing beside them."""
+    new, kv, H, G = [40, 70], [3000, 170], 2, 4
+    n_pages = sum(-(-n // 32) for n in kv) + 2
+    cache = make_cache(kind, n_pages, H, 32, hd, 3)[1]
+    batch, q = make_batch(new, kv, make_tables(kv, 32, n_pages, 3)), rand_q(sum(new), H * G, hd, 4).cuda()
+    want = fr.paged_attn(cache, batch, q, H * G, window=1500, sinks=sinks)
+    buf = torch.full((want.numel() + 24,), 7.0, device="cuda")
+    out = buf[off:off + want.numel()].view(want.shape)
+    fr.paged_attn(cache, batch, q, H * G, window=1500, sinks=sinks, out=out)
+    assert torch.equal(out, want)
+    assert bool((buf[:off] == 7).all()) and bool((buf[off + want.numel():] == 7).all())
