@@ -28,17 +28,16 @@
 // Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.29 ms,
 // 830 TFLOP/s (P_lo counted: 1240). Four prompts of 2048: 244 us in f16 and 495 us in
 // e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 0.77 us in f16, of which the
-// MMAs have 0.4: the rest is the chain S, softmax, P, PV. One lane issues the MMAs, and
-// the compiler has to see that it is one: behind lane == 0 it moves an instruction's
-// operands as those of many threads (1150 cycles for S of a tile; chunks of 512 with
-// sinks 176 us in place of 152). Masks by bits and a look through V before it is cleared
+// MMAs have 0.4: the rest is the chain S, softmax, P, PV. One lane issues the MMAs, chosen
+// by elect.sync (by lane == 0: chunks of 512 with sinks 176 us in place of 152). Masks by
+// bits and a look through V before it is cleared
 // took the tiles at the ends of views from 6000 cycles to 2500 (152 -> 129). Slower were
 // 128-key tiles with P in the place of S (161 in place of 129), 16 softmax warps (148),
 // and two Q tiles with S of the next piece ahead (136 in place of 127). The softmax warps
-// find their next piece while the last PV is awaited (f16: 264 -> 260; e4m3, whose
-// registers spill: 496 -> 546, left out). Results leave 32 bytes at a time: a thread
+// find their next piece while the last PV is awaited (f16: 264 -> 260; e4m3, which has
+// no registers left: 496 -> 546, left out). Results leave 32 bytes at a time: a thread
 // has a row, so each store of a warp is 32 accesses (16 bytes at a time: 260 -> 244;
-// e4m3 of hd 256 567 -> 536, of hd 64 and 128 spills moved into the loop: 496 -> 537).
+// e4m3 of hd 256 567 -> 536, of hd 64 and 128 496 -> 537, left out).
 #include <string.h>
 
 #include "fr_paged_work.cuh"
@@ -117,8 +116,7 @@ __device__ __forceinline__ void load_q(uint32_t dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(dst), "l"((uint64_t)map), "r"(dim), "r"(head), "r"(tok), "r"(bar) : "memory");
 }
-// One lane of a whole warp, as the compiler can see (with lane == 0 in its place it takes
-// an MMA's operands for those of many threads, and moves them one thread after another).
+// One lane of a whole warp (lane == 0 in its place took longer, see the figures above).
 __device__ __forceinline__ bool elect_one() {
     uint32_t one;
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
