@@ -45,6 +45,7 @@ using sm100::smem_addr;
 constexpr int kFewThreads = 256, kThreads = 1024, kMaxCluster = 8;
 constexpr int kOwn = kMaxSeq / (kThreads * kMaxCluster);      // sequences of a thread at most
 constexpr unsigned kStatusNoPages = 0x200u;
+static_assert(((kStatusInput | kStatusNoPages) & ~0xff00u) == 0, "fr_pages_check sets them by their byte");
 constexpr int kMaxPages = 1 << 28;
 
 struct Move {                             // rows 0 .. rows - 1 of page `from` belong into page `to`
@@ -778,8 +779,13 @@ extern "C" fr_status fr_pages_check(const fr_page_pool* pool, cudaStream_t strea
     if (cudaMemcpyAsync(&word, d->ws, sizeof(word), cudaMemcpyDeviceToHost, stream) != cudaSuccess) return FR_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return FR_ERR_CUDA;
     if (word == 0) return FR_OK;
+    // One state a call, and only that is cleared: pages that ran out first, then the numbers
+    // that did not fit (byte 1 of the word holds both bits)
+    const bool pages = (word & kStatusNoPages) != 0;
+    const int left = pages ? (int)((word & kStatusInput) >> 8) : 0;
     if (cudaMemsetAsync(d->ws, 0, sizeof(word), stream) != cudaSuccess) return FR_ERR_CUDA;
-    return word & kStatusInput ? FR_ERR_DEVICE_INPUT : FR_ERR_DEVICE_PAGES;
+    if (left && cudaMemsetAsync(d->ws + 1, left, 1, stream) != cudaSuccess) return FR_ERR_CUDA;
+    return pages ? FR_ERR_DEVICE_PAGES : FR_ERR_DEVICE_INPUT;
 }
 
 extern "C" fr_status fr_pages_reserve(const fr_page_pool* pool, const int32_t* tok_start, cudaStream_t stream) {

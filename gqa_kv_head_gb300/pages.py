@@ -134,6 +134,7 @@ def pages_copy(cache, pool, stream=None):
 
 
 def pages_check(pool, stream=None):
-    """fr_pages_check: raise FrError if an earlier call on the pool met bad numbers
-    (FR_ERR_DEVICE_INPUT) or ran out of pages (FR_ERR_DEVICE_PAGES)."""
+    """fr_pages_check: raise FrError if an earlier call on the pool ran out of pages
+    (FR_ERR_DEVICE_PAGES) or met bad numbers (FR_ERR_DEVICE_INPUT); of both the first
+    now, the second by the next check."""
     _done(pool._lib.fr_pages_check(pool._p, _stream_of(stream, pool._index)), "fr_pages_check")

@@ -608,9 +608,10 @@ fr_status fr_pages_compact(const fr_page_pool* pool, cudaStream_t stream);
 fr_status fr_pages_copy(const fr_paged_kv* kv, const fr_page_pool* pool, cudaStream_t stream);
 
 /*
- * Reads the pool's status word (synchronises `stream`), clears it and returns
- * FR_ERR_DEVICE_INPUT or FR_ERR_DEVICE_PAGES (above) if an earlier call on this pool met
- * that, else FR_OK.
+ * Reads the pool's status word (synchronises `stream`) and returns FR_ERR_DEVICE_PAGES or
+ * FR_ERR_DEVICE_INPUT (above) if an earlier call on this pool met that, else FR_OK. What
+ * it returns it clears; where both were met it returns FR_ERR_DEVICE_PAGES, and the next
+ * check FR_ERR_DEVICE_INPUT.
  */
 fr_status fr_pages_check(const fr_page_pool* pool, cudaStream_t stream);
 
