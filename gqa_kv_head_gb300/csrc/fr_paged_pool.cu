@@ -445,18 +445,17 @@ pages_fork_kernel(const __grid_constant__ PoolArgs a, const int32_t* parent, con
         int p[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) p[u] = e0 + u * 32 < j.z ? src[e0 + u * 32] : -1;
+        // (counts only grow here, and only those above 0: what is read here decides the same for every child)
         int held[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            held[u] = 1;
-            if (e0 + u * 32 >= j.z) continue;
-            const bool page = p[u] >= 0 && p[u] < a.n_pages;
-            odd |= !page && p[u] != -1;                // (-1: trimmed)
-            dst[e0 + u * 32] = page ? p[u] : -1;
-            if (page) held[u] = atomicAdd(a.refs + p[u], 1);
-        }
+        for (int u = 0; u < 4; ++u) held[u] = p[u] >= 0 && p[u] < a.n_pages ? __ldcg(a.refs + p[u]) : 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) odd |= held[u] <= 0;
+        for (int u = 0; u < 4; ++u) {
+            if (e0 + u * 32 >= j.z) continue;
+            odd |= held[u] <= 0 && p[u] != -1;         // no page, or one that counts no holder (-1: trimmed)
+            dst[e0 + u * 32] = held[u] > 0 ? p[u] : -1;
+            if (held[u] > 0) atomicAdd(a.refs + p[u], 1);
+        }
     }
     if (__any_sync(~0u, odd) && lane == 0) atomicOr(a.status, kStatusInput);
 }

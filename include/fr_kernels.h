@@ -570,7 +570,8 @@ fr_status fr_pages_reserve(const fr_page_pool* pool, const int32_t* tok_start, c
  * parent[i] (all of them where length is NULL) by holding the same pages, the last one
  * in part. The child has to be empty (kv_len 0). Pairs with -1 are none; of several
  * pairs with one child the first counts, the others are reported. Lengths are those
- * before the call.  1 <= n <= n_seq.
+ * before the call. A page that counts no holder is not held: the child's entry is -1.
+ * 1 <= n <= n_seq.
  */
 fr_status fr_pages_fork(const fr_page_pool* pool, const int32_t* parent, const int32_t* child, const int32_t* length,
                         int n, cudaStream_t stream);

@@ -1,5 +1,5 @@
-"""What the page pool reports when more than one thing went wrong: against values
-written out by hand."""
+"""What the page pool reports when more than one thing went wrong, and pages that the
+tables name though nobody counts them: against values written out by hand."""
 import pytest
 import torch
 
@@ -48,3 +48,29 @@ def test_reports_of_several_calls():
     pool.kv_len[2] = 1
     fr.pages_reserve(pool, ints([0, 0, 0, 1]))
     assert [status(pool) for _ in range(2)] == [7, 0]
+
+
+@pytest.mark.parametrize("n_seq,n_child", [(6, 1), (6, 4), (400, 300)])
+@pytest.mark.parametrize("max_pages", [4, 700])
+def test_fork_skips_a_page_without_holders(n_seq, n_child, max_pages):
+    """A page that counts no holder is free, whatever an entry says: the children do not
+    hold it (their entry is -1), it stays free, and the next reserve hands it out once."""
+    pool = make_pool(40, n_seq, max_pages)
+    pool.kv_len[0] = 50
+    fr.pages_reserve(pool, ints([0] + [50] * n_seq))     # pages 0 .. 3
+    assert status(pool) == 0
+    pool.refs[1], pool.refs[3] = 0, -2
+    children = list(range(1, 1 + n_child))
+    fr.pages_fork(pool, ints([0] * n_child), ints(children))
+    assert status(pool) == 6
+    rows = pool.page_table.tolist()
+    assert rows[0] == [0, 1, 2, 3] + [-1] * (max_pages - 4)
+    for c in children:
+        assert rows[c] == [0, -1, 2] + [-1] * (max_pages - 3)
+    assert pool.kv_len.tolist() == [50] * (1 + n_child) + [0] * (n_seq - 1 - n_child)
+    assert pool.refs.tolist() == [1 + n_child, 0, 1 + n_child, -2] + [0] * 36
+    last = n_seq - 1
+    pool.kv_len[last] = 16
+    fr.pages_reserve(pool, ints([0] * n_seq + [16]))
+    assert pool.page_table[last, 0].item() == 1 and pool.refs[1].item() == 1
+    assert status(pool) == 0
