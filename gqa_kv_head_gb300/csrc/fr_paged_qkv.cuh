@@ -152,11 +152,11 @@ struct Turner {
     __device__ __forceinline__ void operator()(const HeadRows& r, int c, float* y) const {
         float a = r.scale;
         if (NORMED) {
-            bool small;
-            const float inv = row_rms<ITEMS, E>(y, r.eps, small);
-            if (__builtin_expect(small, 0)) {
+            int scaled;
+            const float inv = row_rms<ITEMS, E>(y, r.eps, scaled);
+            if (__builtin_expect(scaled != 0, 0)) {
 #pragma unroll
-                for (int u = 0; u < E; ++u) y[u] *= kSmall;
+                for (int u = 0; u < E; ++u) y[u] *= resize(scaled);
             }
             a *= inv;
         }
@@ -258,9 +258,9 @@ __device__ __noinline__ void query_heads_odd(const QkvArgs* g, const RopeTable* 
             y[4 + u] = Raw<T>::one(src + q[u]);
         }
         if (nm.w) {
-            bool small;
-            const float inv = row_rms<ITEMS>(y, nm.eps, small);
-            scale_row(y, inv, small, make_float4(nm.w[p[0]], nm.w[p[1]], nm.w[p[2]], nm.w[p[3]]),
+            int scaled;
+            const float inv = row_rms<ITEMS>(y, nm.eps, scaled);
+            scale_row(y, inv, scaled, make_float4(nm.w[p[0]], nm.w[p[1]], nm.w[p[2]], nm.w[p[3]]),
                       make_float4(nm.w[q[0]], nm.w[q[1]], nm.w[q[2]], nm.w[q[3]]));
         }
 #pragma unroll

@@ -225,9 +225,13 @@ __device__ __forceinline__ void slot_dims(int c, const RopeTable& tb, const Norm
     }
 }
 // 1 / sqrt(mean of squares + eps) of a row whose elements the ITEMS lanes of an
-// aligned group hold, E each. Squares past fp32's range: the elements at 2^-70,
-// which `small` says (eps is nothing beside them).
-constexpr float kSmall = 0x1p-70f;
+// aligned group hold, E each. Rows whose squares leave fp32's range are taken at
+// another scale, which `scaled` names and resize applies:
+//   1  squares past the largest number: the elements at 2^-70 (eps is nothing beside them);
+//   2  a sum below 2^-102, of which squares below the normal range would leave no 24 bits, beside
+//      an eps below 2^-118 (one above hides them): the elements at 2^90, eps at 2^180.
+constexpr float kDown = 0x1p-70f, kUp = 0x1p90f;
+__device__ __forceinline__ float resize(int scaled) { return scaled == 1 ? kDown : kUp; }
 template <int ITEMS>
 __device__ __forceinline__ float row_sum(float x) {
     const unsigned group = (ITEMS == 32 ? ~0u : (1u << (ITEMS & 31)) - 1u) << (threadIdx.x & 31 & ~(ITEMS - 1));
@@ -236,7 +240,7 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 template <int ITEMS, int E = 8>
-__device__ __forceinline__ float row_rms(const float* y, float eps, bool& small) {
+__device__ __forceinline__ float row_rms(const float* y, float eps, int& scaled) {
     float s = 0.f, s1 = 0.f;
 #pragma unroll
     for (int u = 0; u < E; u += 2) {
@@ -244,21 +248,24 @@ __device__ __forceinline__ float row_rms(const float* y, float eps, bool& small)
         s1 = fmaf(y[u + 1], y[u + 1], s1);
     }
     s = row_sum<ITEMS>(s + s1);
-    small = !(s <= 3.402823466e38f);
-    if (__builtin_expect(small, 0)) {     // (the group's lanes agree)
+    const float low = eps < 0x1p-118f ? 0x1p-102f : 0.f;
+    scaled = 0;
+    if (__builtin_expect(!(s <= 3.402823466e38f && s >= low), 0)) {        // (the group's lanes agree)
+        scaled = s < low ? 2 : 1;
+        const float f = resize(scaled);
         s = 0.f;
 #pragma unroll
-        for (int u = 0; u < E; ++u) s = fmaf(y[u] * kSmall, y[u] * kSmall, s);
+        for (int u = 0; u < E; ++u) s = fmaf(y[u] * f, y[u] * f, s);
         s = row_sum<ITEMS>(s);
-        eps = 0.f;
+        eps = scaled == 1 ? 0.f : eps * kUp * kUp;
     }
     return rsqrtf(fmaf(s, 1.f / (E * ITEMS), eps));      // (off by 2^-22.9 at most)
 }
 // y times the row's factor and the weights of its dims (d0 .. d0 + 3 and d1 .. d1 + 3).
-__device__ __forceinline__ void scale_row(float* y, float inv, bool small, const float4& w0, const float4& w1) {
-    if (__builtin_expect(small, 0)) {
+__device__ __forceinline__ void scale_row(float* y, float inv, int scaled, const float4& w0, const float4& w1) {
+    if (__builtin_expect(scaled != 0, 0)) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) y[u] *= kSmall;
+        for (int u = 0; u < 8; ++u) y[u] *= resize(scaled);
     }
     y[0] *= inv * w0.x; y[1] *= inv * w0.y; y[2] *= inv * w0.z; y[3] *= inv * w0.w;
     y[4] *= inv * w1.x; y[5] *= inv * w1.y; y[6] *= inv * w1.z; y[7] *= inv * w1.w;
@@ -346,9 +353,9 @@ __device__ __forceinline__ void append_piece(const AppendArgs& a, const RopeTabl
             }
         }
         if (normed) {
-            bool small;
-            const float inv = row_rms<ITEMS>(y, nm.eps, small);
-            scale_row(y, inv, small, w0, w1);
+            int scaled;
+            const float inv = row_rms<ITEMS>(y, nm.eps, scaled);
+            scale_row(y, inv, scaled, w0, w1);
         }
         if (!rot) return;
         if (together) {
@@ -536,19 +543,20 @@ __device__ __forceinline__ void append_prompt(const AppendArgs& a, const RopeTab
             }
     auto angle = [&](int k, int u) { return KEPT ? cs[KEPT ? k : 0][u] : cs_at[(k * 4 + u) * NTH]; };
     float rms[EXT ? HC : 1][EXT ? KR : 1];                 // the rows' factors, taken once
-    unsigned small = 0u;
+    unsigned scaled = 0u;                                  // two bits each
+    static_assert(2 * HC * KR <= 32, "");
     auto values = [&](int j, int k, float* y, bool again = false) {
         const float4 p = Raw<T>::floats(raw[j][k][0]), q = Raw<T>::floats(raw[j][k][1]);
         y[0] = p.x; y[1] = p.y; y[2] = p.z; y[3] = p.w;
         y[4] = q.x; y[5] = q.y; y[6] = q.z; y[7] = q.w;
         if (EXT && normed) {
-            const unsigned bit = 1u << (j * KR + k);
+            const int at = 2 * (j * KR + k);
             if (!again) {
-                bool s;
+                int s;
                 rms[j][k] = row_rms<ITEMS>(y, nm.eps, s);
-                small = s ? small | bit : small & ~bit;
+                scaled = (scaled & ~(3u << at)) | (unsigned)s << at;
             }
-            scale_row(y, rms[j][k], small & bit, w0, w1);
+            scale_row(y, rms[j][k], scaled >> at & 3u, w0, w1);
         }
         if (!rot) return;
         if (EXT && together) {

@@ -433,7 +433,8 @@ fr_status fr_kv_append_paged(const fr_paged_kv* kv, const fr_paged_batch* batch,
  *   q16_out  = f16(q_scale * RoPE(n(q), pos)),  K = RoPE(n(k_new), pos),  V = v_new,
  * K and V as fr_kv_append_paged writes them. Norms, rotation and scale in fp32, one
  * rounding at the end; without weights and with pairs (i, i + n_dims/2) the bits are
- * those of the two calls. A row whose squares pass fp32's range is normed all the same.
+ * those of the two calls. A row whose squares pass fp32's range, or fall below it, is
+ * normed all the same.
  * Rows of q from tok_start[n_seq] on are padding: not used, their q16_out left as it was.
  *   row_type    FR_ROWS_F32, FR_ROWS_F16 or FR_ROWS_BF16: type of q, k_new and v_new
  *               (bf16 and f32 values beyond f16's range become infinite in f16)
