@@ -227,7 +227,7 @@ __device__ __forceinline__ void slot_dims(int c, const RopeTable& tb, const Norm
 // 1 / sqrt(mean of squares + eps) of a row whose elements the ITEMS lanes of an
 // aligned group hold, E each. Rows whose squares leave fp32's range are taken at
 // another scale, which `scaled` names and resize applies:
-//   1  squares past the largest number: the elements at 2^-70 (eps is nothing beside them);
+//   1  squares past the largest number: the elements at 2^-70, eps at 2^-140;
 //   2  a sum below 2^-102, of which squares below the normal range would leave no 24 bits, beside
 //      an eps below 2^-118 (one above hides them): the elements at 2^90, eps at 2^180.
 constexpr float kDown = 0x1p-70f, kUp = 0x1p90f;
@@ -257,7 +257,7 @@ __device__ __forceinline__ float row_rms(const float* y, float eps, int& scaled)
 #pragma unroll
         for (int u = 0; u < E; ++u) s = fmaf(y[u] * f, y[u] * f, s);
         s = row_sum<ITEMS>(s);
-        eps = scaled == 1 ? 0.f : eps * kUp * kUp;
+        eps = eps * f * f;
     }
     return rsqrtf(fmaf(s, 1.f / (E * ITEMS), eps));      // (off by 2^-22.9 at most)
 }

@@ -68,3 +68,23 @@ def test_zeros(kind, new, kv):
         if kind == "f16":
             first = cache.k_pages[int(table[0, (kv[0] - new[0]) // ps]), :, (kv[0] - new[0]) % ps]
             assert bool(torch.isnan(first).all()) if eps == 0.0 else not bool(first.any())
+
+
+@pytest.mark.parametrize("kind", ["f16", "e4m3"])
+@pytest.mark.parametrize("new,kv", [([1, 1], [3, 17]), ([40], [55])])
+@pytest.mark.parametrize("size,eps", [(1.0e19, 1.0e37), (2.0 ** 64, 2.0 ** 124)])
+def test_large_rows_beside_a_large_eps(kind, new, kv, size, eps):
+    """Squares past fp32's range, and an eps that counts beside their mean."""
+    n_tok, hd, H, G, ps = sum(new), 128, 2, 2, 16
+    (k, ks, v, vs), cache = make_cache(kind, 12, H, ps, hd, 1)
+    table = make_tables(kv, ps, 12, 1)
+    (q, kn, vn), (dq, dk, dv) = make_rows("f32", n_tok, H, G, hd, 2, size=size)
+    dv.copy_(torch.ones_like(dv))
+    wq, wk = make_weights(hd, 3)
+    pos, rope = positions(new, kv), {"n_dims": hd}
+    out = fr.qkv_post_paged(cache, make_batch(new, kv, table), dq, dk, dv, torch.tensor(pos, dtype=torch.int32).cuda(), fr.rope_params(**rope),
+                            q_norm=wq.cuda(), k_norm=wk.cuda(), eps=eps)
+    y, tol = qref.rows(q, pos, rope, wq, float(torch.tensor(eps)), False, hd ** -0.5)
+    check_f16(out.view(n_tok, G * H, hd), y, tol, "q")
+    y, tol = qref.rows(kn, pos, rope, wk, float(torch.tensor(eps)))
+    check_pages(kind, y, tol, new, kv, table, k, ks, cache.k_pages, cache.k_scale, "K")
