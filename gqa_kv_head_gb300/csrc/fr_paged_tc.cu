@@ -25,15 +25,14 @@
 // Waits are bounded; one that gives up sets the status word, and the CTA still
 // drains its copies and MMAs and frees its TMEM.
 //
-// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.29 ms,
-// 830 TFLOP/s (P_lo counted: 1240). Four prompts of 2048: 244 us in f16 and 495 us in
-// e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 0.77 us in f16, of which the
+// Measured: 2048 new tokens at the end of 32768 keys, 32 heads on 8, hd 128, f16: 1.33 ms,
+// 800 TFLOP/s (P_lo counted: 1200). Four prompts of 2048: 249 us in f16 and 515 us in
+// e4m3 (1344 and 1619 us in tiles of 32 rows). A tile takes 0.78 us in f16, of which the
 // MMAs have 0.4: the rest is the chain S, softmax, P, PV. One lane issues the MMAs, chosen
 // by elect.sync (by lane == 0: chunks of 512 with sinks 176 us in place of 152). Masks by
-// bits and a look through V before it is cleared
-// took the tiles at the ends of views from 6000 cycles to 2500 (152 -> 129). Slower were
-// 128-key tiles with P in the place of S (161 in place of 129), 16 softmax warps (148),
-// and two Q tiles with S of the next piece ahead (136 in place of 127). The softmax warps
+// bits and a look through V before it is cleared took the tiles at the ends of views from
+// 6000 cycles to 2500 (152 -> 129). Slower were 128-key tiles with P in the place of S
+// (161 in place of 129), 16 softmax warps (148), and two Q tiles with S of the next piece ahead (136 in place of 127). The softmax warps
 // find their next piece while the last PV is awaited (f16: 264 -> 260; e4m3, which has
 // no registers left: 496 -> 546, left out). Results leave 32 bytes at a time: a thread
 // has a row, so each store of a warp is 32 accesses (16 bytes at a time: 260 -> 244;
@@ -54,12 +53,19 @@ constexpr int kSmax = 256, kProd = 8, kMma = 9, kConv = 10, kConvThreads = 128; 
 // and moves when a score exceeds it by 15 (P_lo off f16's subnormals, P_hi within f16).
 constexpr float kBelow = 7.0f, kAbove = 15.0f;
 constexpr uint64_t kLimit = 2000000000ull;
-// The MMA's accumulator drops bits at each step of 16 keys, always towards zero: after
-// 2064 keys rows are 4e-6 too small. With sinks (calls without keep their sums' order) and
-// up to hd 128 the softmax warps add O to sums of their own in TMEM after so many tiles,
-// and it starts anew. Chunks of 512, window 2048: error 2.0e-6 of 64 bits without, 6.5e-7
-// with sums every 4 tiles, 8.5e-7 every 8; 173.7, 176.2 us then (now 127.4 and 124.9 for 4 and 8).
-constexpr int kSumTiles = 4;
+// The MMA's accumulator drops bits at each step of 16 keys, always towards zero: where
+// values have one sign, rows were too small by 1.4e-5 of themselves after 2048 keys and by 2.0e-4
+// after 32768 (e4m3 3.8e-6 and 1.4e-4). So the softmax warps add O to fp32 sums of their own
+// after so many tiles, and it starts anew; the loss then stays the same at any length:
+//   f16   4 tiles 1.4e-6, 8 3.2e-6, 16 6.9e-6, 32 1.4e-5;  e4m3  4 3e-7, 16 1.5e-6, 32 3.8e-6, 48 6.5e-6
+// Times, us, without sums and with 16 tiles (e4m3 48): four prompts of 2048 244 and 249, 495 and 515;
+// 2048 tokens of 32768 keys 1305 and 1332, 1981 and 2153; 8 x 512 tokens at hd 256 395 and 437,
+// 534 and 585. With sinks, whose windows are short, every 4 (chunks of 512, 8 or 4: even).
+// Up to hd 128 the sums lie in TMEM. At hd 256 O, S and P fill it: there they lie in global
+// memory (L2), in the CTA's own part of the workspace, four columns of all rows in turn so that a
+// warp's accesses are whole lines, and O is added without waiting (read, added and written in the
+// order of the rows: 8 x 512 tokens 650 in place of 437).
+constexpr int kSinkTiles = 4, kSumTiles = 16, kCodeTiles = 48;
 
 template <int HD, bool E4>
 struct Cfg {
@@ -85,7 +91,7 @@ struct Cfg {
     // TMEM columns: O, two S tiles, two tiles of P_hi and of P_lo words (two keys a column)
     static constexpr int T_O = 0, T_S = HD, T_P = HD + 2 * kBN, T_PL = T_P + kBN, T_A = T_PL + kBN;
     static_assert(T_PL + kBN <= 512, "TMEM");
-    static constexpr bool SUMS = T_A + HD <= 512;             // room for sums of O (kSumTiles)
+    static constexpr bool NEAR = T_A + HD <= 512;             // room for the sums of O
 };
 
 struct TcMaps {
@@ -126,6 +132,23 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void store_8(float* p, const float* x) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" :: "l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
                  "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]) : "memory");
+}
+// Four numbers in memory and x: their sums (nobody waits for them).
+__device__ __forceinline__ void add_4(float4* p, const uint32_t* x) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" :: "l"(p), "f"(__uint_as_float(x[0])),
+                 "f"(__uint_as_float(x[1])), "f"(__uint_as_float(x[2])), "f"(__uint_as_float(x[3])) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* x) {
+    if (N == 8) tmem_ld_x8(at, x);
+    else if (N == 16) tmem_ld_x16(at, x);
+    else tmem_ld_x32(at, x);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* x) {
+    if (N == 8) tmem_st_x8(at, x);
+    else if (N == 16) tmem_st_x16(at, x);
+    else tmem_st_x32(at, x);
 }
 // Two products and two sums at a time, each rounded as one alone would be.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -177,7 +200,8 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
     using C = Cfg<HD, E4>;
     using P = Units<0, kBN, 1, kTcSegCost, SINK>;
     constexpr int KS = C::KS, RS = E4 ? C::RS : 1, HB = kBN / 2, OH = HD / 2;
-    constexpr bool SUMS = SINK && C::SUMS;
+    constexpr int EACH = SINK && C::NEAR ? kSinkTiles : E4 ? kCodeTiles : kSumTiles;
+    constexpr int SW = E4 ? 8 : 16;              // columns at a time, where registers are few
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     unsigned char* aux = sm + C::AUX;
@@ -378,7 +402,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                             // P words: [buffer][half of the keys][16 columns]
                             const uint32_t col = (m & 1) * HB + ks * 8;
                             const uint64_t vd = sdesc_sw128(v_base + ks * 2048, C::KV_BOX, 1024);
-                            mma_ts(tbase + C::T_O, tbase + C::T_P + col, vd, id_o, (SUMS ? i % kSumTiles : i) > 0 || ks > 0 ? 1u : 0u);
+                            mma_ts(tbase + C::T_O, tbase + C::T_P + col, vd, id_o, i % EACH > 0 || ks > 0 ? 1u : 0u);
                             mma_ts(tbase + C::T_O, tbase + C::T_PL + col, vd, id_o, 1u);
                         }
                         mma_commit(bar(C::B_OD + (m & 1)));
@@ -459,6 +483,12 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
             const int2 view = r < rows ? row_view(s, row0 + r, a) : make_int2(0, 0);
             const bool active = qd * 32 < rows;
             if (tid == 0) put_split(a, share, cta, *w, row0, rows);
+            // (hd 256) place of this thread's sums of columns c .. c + 3 of its half, four columns of all rows in turn:
+            // where a state is to lie that this CTA has not written yet, or that this piece writes once they are read
+            auto far_sums = [&](int c) {
+                return reinterpret_cast<float4*>(a.part_o + (int64_t)(2 * cta + (w->ua == 0 ? 1 : 0)) * 128 * HD) +
+                       (half * OH + c) / 4 * 128 + r;
+            };
             float m_ref = -INFINITY, l = 0.f, v_ref = 0.f;
             for (int tile = t.x; tile < t.y; ++tile, ++n) {
                 wait(C::B_SF + (n & 1), (n >> 1) & 1);
@@ -554,35 +584,61 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     tmem_st_x16(tbase + lanes + C::T_PL + (n & 1) * HB + half * 16, lo);
                     // (behind the weights: PV of the tile before has had their time)
                     const int i = tile - t.x;
-                    const bool sum = SUMS && i > 0 && i % kSumTiles == 0;            // O goes into the sums
+                    const bool sum = i > 0 && i % EACH == 0;                         // O goes into the sums
                     if ((__any_sync(~0u, grown || v_up) || sum) && i > 0) {
                         wait(C::B_OD + ((n - 1) & 1), ((n - 1) >> 1) & 1);           // O holds PV up to the tile before
                         __syncwarp();
                         tc_fence_after();
-                        if (SUMS && i >= kSumTiles) {
+                        if (C::NEAR && i >= EACH) {
 #pragma unroll 1
-                            for (int c = 0; c < OH; c += 16) {
-                                uint32_t o[16], s[16];
-                                tmem_ld_x16(tbase + lanes + C::T_O + half * OH + c, o);
-                                tmem_ld_x16(tbase + lanes + C::T_A + half * OH + c, s);
+                            for (int c = 0; c < OH; c += SW) {
+                                uint32_t o[SW], s[SW];
+                                tmem_ld<SW>(tbase + lanes + C::T_O + half * OH + c, o);
+                                tmem_ld<SW>(tbase + lanes + C::T_A + half * OH + c, s);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int u = 0; u < 16; ++u) {
-                                    const float was = i > kSumTiles ? __uint_as_float(s[u]) : 0.f;   // (nothing so far)
+                                for (int u = 0; u < SW; ++u) {
+                                    const float was = i > EACH ? __uint_as_float(s[u]) : 0.f;        // (nothing so far)
                                     s[u] = __float_as_uint((sum ? was + __uint_as_float(o[u]) : was) * o_scale);
                                 }
-                                tmem_st_x16(tbase + lanes + C::T_A + half * OH + c, s);
+                                tmem_st<SW>(tbase + lanes + C::T_A + half * OH + c, s);
                             }
                         }
-                        if (!sum)
+                        if (!C::NEAR && sum) {
 #pragma unroll 1
-                        for (int c = 0; c < OH; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld_x32(tbase + lanes + C::T_O + half * OH + c, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < OH; c += 16) {
+                                alignas(16) uint32_t o[16];
+                                tmem_ld<16>(tbase + lanes + C::T_O + half * OH + c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * o_scale);
-                            tmem_st_x32(tbase + lanes + C::T_O + half * OH + c, o);
+                                for (int u = 0; u < 16; u += 4) {
+                                    if (i > EACH) add_4(far_sums(c + u), o + u);
+                                    else __stcg(far_sums(c + u), *reinterpret_cast<const float4*>(o + u));
+                                }
+                            }
+                        }
+                        if (!C::NEAR && i >= EACH && __any_sync(~0u, o_scale != 1.f)) {
+#pragma unroll 1
+                            for (int c = 0; c < OH; c += 32) {
+                                float4 x[8];
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) x[u] = __ldcg(far_sums(c + 4 * u));
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    __stcg(far_sums(c + 4 * u), make_float4(x[u].x * o_scale, x[u].y * o_scale, x[u].z * o_scale,
+                                                                            x[u].w * o_scale));
+                            }
+                        }
+                        if (!sum) {
+#pragma unroll 1
+                            for (int c = 0; c < OH; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld_x32(tbase + lanes + C::T_O + half * OH + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * o_scale);
+                                tmem_st_x32(tbase + lanes + C::T_O + half * OH + c, o);
+                            }
                         }
                     }
                     tmem_wait_st();
@@ -635,6 +691,28 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                 wait(C::B_OF, piece & 1);
                 __syncwarp();
                 tc_fence_after();
+                if (t.y - t.x > EACH) {                       // O is what the last tiles made: the sums join it
+                    constexpr int EW = C::NEAR ? SW : 16;
+                    if (active) {
+#pragma unroll 1
+                        for (int c = 0; c < OH; c += EW) {
+                            alignas(16) uint32_t o[EW], s[EW];
+                            if (C::NEAR) {
+                                tmem_ld<EW>(tbase + lanes + C::T_A + half * OH + c, s);
+                            } else {
+#pragma unroll
+                                for (int u = 0; u < EW; u += 4) *reinterpret_cast<float4*>(s + u) = __ldcg(far_sums(c + u));
+                            }
+                            tmem_ld<EW>(tbase + lanes + C::T_O + half * OH + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < EW; ++u) o[u] = __float_as_uint(__uint_as_float(s[u]) + __uint_as_float(o[u]));
+                            tmem_st<EW>(tbase + lanes + C::T_O + half * OH + c, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    if (!C::NEAR) asm volatile("bar.sync 5, 256;" ::: "memory");     // (all sums are read: a state may take their place)
+                }
             }
             s_l[half * 128 + r] = l;
             asm volatile("bar.sync %0, 64;" :: "r"(qd + 1) : "memory");
@@ -655,16 +733,6 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                     if (any) {
                         tmem_ld_x32(tbase + lanes + C::T_O + half * OH + c, reinterpret_cast<uint32_t*>(o));
                         tmem_wait_ld();
-                        if (SUMS && t.y - t.x > kSumTiles) {
-#pragma unroll
-                            for (int h = 0; h < 32; h += 16) {
-                                uint32_t s[16];
-                                tmem_ld_x16(tbase + lanes + C::T_A + half * OH + c + h, s);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) o[h + u] += __uint_as_float(s[u]);
-                            }
-                        }
                     }
                     if (r < rows) {
                         if (!any || l == 0.f) {
@@ -698,7 +766,7 @@ paged_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ TcMa
                                 for (int u = 0; u < 32; ++u) o[u] = fmaf(p, page_value<E4>(pg.v, v + half * OH + c + u), o[u]);
                             }
                         }
-float* const to = dst + half * OH + c;
+                        float* const to = dst + half * OH + c;
                         if ((E4 && HD < 256) || ((uintptr_t)to & 31)) {
 #pragma unroll
                             for (int u = 0; u < 32; u += 4)
