@@ -63,6 +63,14 @@ constexpr float kVMin = 0x1p-120f;                   // a V reference at least: 
 // 2^-24 of the row's largest weight at most, beside 2^-22 of each.
 constexpr float kVSlack = 16.0f;
 constexpr uint64_t kWaitNs = 2000000000ull;
+// An MMA drops bits of the sum that it adds to, always towards zero: with values of one
+// sign, rows were too small by 2.5e-6 of themselves where a warp had 512 keys of a piece and
+// by 4.8e-5 where it had 8192 (hd 256 and 32 rows 3.0e-5, e4m3 2.1e-5 and 1.0e-5). A warp with more than
+// so many therefore takes the products of each tile by themselves and adds them to O in
+// fp32 (2e-7 at any length): 64 sequences of ..8192 keys 163.8 and 164.7 us, e4m3 93.4 and
+// 93.3. For all pieces it would cost the short ones (1 x 968 keys of hd 256 8.3 and 8.6 us, 65536
+// 26.5 and 28.3, e4m3 131072 61.3 and 64.4; from 512 keys on 64.9 there).
+constexpr int kChainKeys = 1024;
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int row, int head, int page,
                                             uint32_t bar) {
@@ -158,6 +166,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
     using C = Cfg<HD, TYPE, NT>;
     constexpr int W = C::W, RT = C::RT, MT = C::MT, NS = C::NS, KT = C::KT, SUB = C::SUB;
     constexpr bool E4 = C::E4;
+    constexpr int MV = E4 ? 2 : 1;                          // 16-dim blocks of one load of V
     using P = Units<RT, KT, W, kSegCost, SINK>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -425,6 +434,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
 
         const int2 tiles = walk_tiles<P>(cw, warp);
         const int first_tiles = sink_tiles<P>(cw.s, a), tile0 = cw.s.tile0 - first_tiles;
+        const bool tile_sums = (tiles.y - tiles.x) * KT > kChainKeys * W;
         for (int t = tiles.x; t < tiles.y; t += W) {
             // ---- S^T = K Q^T ------------------------------------------------
             wait_slot();
@@ -721,31 +731,63 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CU
                 __syncwarp();
             }
             const uint32_t v_base = v_lane + c_slot * C::SLOT;
+            // V^T of step u: dims m * 16 .. (e4m3: two blocks of 16)
+            auto v_frags = [&](int m, int u, uint32_t (*r)[4]) {
+                uint32_t x[4];
+                ldsm_x4_t(at_chunk(v_base, u, E4 ? m : 2 * m), x[0], x[1], x[2], x[3]);
 #pragma unroll
-            for (int m = 0; m < MT; m += E4 ? 2 : 1)
-#pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    uint32_t r[4];
-                    ldsm_x4_t(at_chunk(v_base, u, E4 ? m : 2 * m), r[0], r[1], r[2], r[3]);
+                for (int i = 0; i < 4; ++i) {
                     if (E4) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
-                        const uint32_t a0[4] = {e4m3_lo(r[0]), e4m3_hi(r[0]), e4m3_lo(r[1]), e4m3_hi(r[1])};
-                        const uint32_t a1[4] = {e4m3_lo(r[2]), e4m3_hi(r[2]), e4m3_lo(r[3]), e4m3_hi(r[3])};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma(o[m][n], a0, ph[u][n][0], ph[u][n][1]);
-                            mma(o[m + 1][n], a1, ph[u][n][0], ph[u][n][1]);
-                            mma(o[m][n], a0, pl[u][n][0], pl[u][n][1]);
-                            mma(o[m + 1][n], a1, pl[u][n][0], pl[u][n][1]);
-                        }
+                        x[i] = __byte_perm(x[i], 0, 0x3120);
+                        r[E4 ? i >> 1 : 0][2 * (i & 1)] = e4m3_lo(x[i]);
+                        r[E4 ? i >> 1 : 0][2 * (i & 1) + 1] = e4m3_hi(x[i]);
                     } else {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma(o[m][n], r, ph[u][n][0], ph[u][n][1]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma(o[m][n], r, pl[u][n][0], pl[u][n][1]);
+                        r[0][i] = x[i];
                     }
                 }
+            };
+            if (!tile_sums) {
+#pragma unroll
+                for (int m = 0; m < MT; m += MV)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        uint32_t r[MV][4];
+                        v_frags(m, u, r);
+                        if (E4) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int i = 0; i < 2 * MV; ++i)
+                                    mma(o[m + i % MV][n], r[i % MV], i < MV ? ph[u][n][0] : pl[u][n][0],
+                                        i < MV ? ph[u][n][1] : pl[u][n][1]);
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma(o[m][n], r[0], ph[u][n][0], ph[u][n][1]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma(o[m][n], r[0], pl[u][n][0], pl[u][n][1]);
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; m += MV) {
+                    uint32_t r[SUB][MV][4];
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) v_frags(m, u, r[u]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < MV; ++i) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u) {
+                                mma(d, r[u][i], ph[u][n][0], ph[u][n][1]);
+                                mma(d, r[u][i], pl[u][n][0], pl[u][n][1]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[m + i][n][e] += d[e];
+                        }
+                }
+            }
             pass_slot(t + W >= tiles.y);        // the piece's last slot takes O first
             c_tile = (c_tile + 1) % C::ENTRIES;
         }

@@ -483,6 +483,11 @@ size_t fr_paged_attn_workspace_size(int n_head, int n_kv_head, int hd);
  * Scores (times log2 e) and sums of weights times values, each weight up to 2^15,
  * are held in fp32: beyond its range, which e4m3 pages can reach with scales whose
  * values pass 2^80, they are infinite, and the result is infinite or NaN.
+ * The matrix units' accumulators drop up to 2^-23 of a sum towards zero at each step of
+ * 16 keys (two for each: P enters as two terms). They hold 1024 keys at most (f16 pages
+ * in tiles of 128 rows, and pieces of short sequences; e4m3 in tiles of 128 rows 3072)
+ * before their sum joins others in fp32, so that a row is too small by the same share of
+ * sum |w v| at any length (measured: 7e-6).
  * The result does not depend on timing: same inputs, same bits.
  * Supported: n_head <= 65536, and fewer than 2^31 units of work (64 keys of a row
  * tile each) in the largest batch of these sizes.

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 PS = 64
 # Keys that one accumulator takes at most, in 16-key steps of two products (P_hi V and P_lo V): each
 # step drops less than 2^-23 of what it holds, which is less than the final sum.
-STEPS = {("wide", "f16"): 2 * 16 * 4, ("wide", "e4m3"): 2 * 48 * 4}
+STEPS = {("wide", "f16"): 2 * 16 * 4, ("wide", "e4m3"): 2 * 48 * 4, ("few", "f16"): 2 * 64, ("few", "e4m3"): 2 * 64}
 
 
 def long_case(kind, hd, H, G, n, n_seq, kv, window, sinks, k, v, v_scale=1.0, q=None, seed=0):
@@ -59,7 +59,7 @@ def long_case(kind, hd, H, G, n, n_seq, kv, window, sinks, k, v, v_scale=1.0, q=
 @pytest.mark.parametrize("kind", ["f16", "e4m3"])
 @pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (32900, 4)])
-@pytest.mark.parametrize("form,G,n,n_seq", [("wide", 8, 16, 40)])
+@pytest.mark.parametrize("form,G,n,n_seq", [("wide", 8, 16, 40), ("few", 4, 1, 160), ("few", 4, 3, 160)])
 def test_values_of_one_sign(form, G, n, n_seq, kind, hd, window, sinks):
     """Weights about equal, values in 0.5 .. 1.5. Beside the drops (see STEPS) a result errs in its weights,
     by 2^-21 each at most, and in roundings to nearest, neither to one side: 2^-20 for their mean."""
@@ -79,7 +79,8 @@ def test_values_of_one_sign(form, G, n, n_seq, kind, hd, window, sinks):
 @pytest.mark.parametrize("kind", ["f16", "e4m3"])
 @pytest.mark.parametrize("hd", [64, 128, 256])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (5900, 70)])
-@pytest.mark.parametrize("G,n,n_seq,kv", [(8, 16, 40, 6001), (8, 16, 3, 30011), (5, 20, 50, 4100)])
+@pytest.mark.parametrize("G,n,n_seq,kv", [(8, 16, 40, 6001), (8, 16, 3, 30011), (5, 20, 50, 4100), (4, 1, 170, 9001), (4, 7, 120, 5003),
+                                            (3, 4, 2, 30011)])
 def test_references_that_move_late(kind, hd, window, sinks, G, n, n_seq, kv):
     """Scores grow along the keys, and with them the scales of V's pages, so that what was summed
     up is scaled again and again. The tolerance is that of paged_ref.attention, with one dim that makes
