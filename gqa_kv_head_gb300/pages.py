@@ -15,8 +15,13 @@ from .paged import _stream_of
 _INT_MAX = 2 ** 31 - 1
 
 
+def _int(n):
+    """n, or -1 or the largest C int in its place (a C int would keep the low 32 bits of what does not fit it)."""
+    return max(-1, min(n, _INT_MAX))
+
+
 def pages_workspace_size(n_pages, n_seq):
-    return int(_abi.load().fr_pages_workspace_size(n_pages, n_seq))
+    return int(_abi.load().fr_pages_workspace_size(_int(n_pages), _int(n_seq)))
 
 
 class PagePool:
@@ -57,7 +62,7 @@ class PagePool:
         with torch.cuda.device(self.device), torch.cuda.stream(stream):
             self.workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
             _abi.check(self._lib.fr_page_pool_init(
-                self._p, refs.data_ptr(), n_pages, page_size, kv_len.data_ptr(), page_table.data_ptr(), row, n_seq, max_pages,
+                self._p, refs.data_ptr(), n_pages, _int(page_size), kv_len.data_ptr(), page_table.data_ptr(), row, n_seq, max_pages,
                 self.workspace.data_ptr(), n), "fr_page_pool_init")
             _abi.check(self._lib.fr_workspace_init(self.workspace.data_ptr(), n, _stream_of(stream, self._index)),
                        "fr_workspace_init")
@@ -117,8 +122,7 @@ def pages_trim(pool, window, sinks=0, tok_start=None, stream=None):
     sinks=) does not look up any more, from the step of tok_start on (None: from
     the next key on)."""
     ts = None if tok_start is None else _slots(pool, "tok_start", tok_start, pool.kv_len.shape[0] + 1)
-    window, sinks = max(-1, min(window, _INT_MAX)), max(-1, min(sinks, _INT_MAX))
-    _done(pool._lib.fr_pages_trim(pool._p, ts, window, sinks, _stream_of(stream, pool._index)), "fr_pages_trim")
+    _done(pool._lib.fr_pages_trim(pool._p, ts, _int(window), _int(sinks), _stream_of(stream, pool._index)), "fr_pages_trim")
 
 
 def pages_compact(pool, stream=None):
