@@ -16,12 +16,13 @@
 // pass through distributed shared memory. Free and trim need no meeting.
 // Copies are bound by bytes: one 16-byte word after another, four of a thread in
 // flight, any strides. Four blocks of 256 threads an SM: with nothing to copy 2.1 us
-// (eight 2.7); a compaction's 176 MB move at 7.4 TB/s.
+// (eight 2.7); a compaction's 176 MB take 29 (26 on cold caches: 88 MB read from DRAM; of the
+// 88 written 40 arrive there meanwhile, the rest stays in L2).
 //
 // In a captured graph, one call among others: reserve 2.4 us for 80 slots without new
 // rows, about 6 in a pool of 32885 pages; fork of 64 children of 63 pages about 5.
 // What a step of serving takes (free, fork, lengths, reserve, copy for 64 children of
-// one prompt): 18.5 us; with CTAs of 1024 threads for all sizes it took 24.3.
+// one prompt): 18.9 us; with CTAs of 1024 threads for all sizes it took 24.3.
 //
 // Results do not depend on timing: where several callers meet (a page that all
 // its holders go on in, a child named twice) the order of the sequences decides.

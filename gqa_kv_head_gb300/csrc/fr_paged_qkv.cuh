@@ -28,7 +28,7 @@
 //     as few rows of a thread, and as many heads at a time, as the page allows; query
 //     heads through the ring by tiles of tokens, a warp to a token, whose lanes share
 //     the angles out and hand them around. The two kinds of blocks take turns.
-//     4980 f32 tokens of 15 query and 5 KV heads of 64, 32-row pages (45 MB): 18.4 us
+//     4980 f32 tokens of 15 query and 5 KV heads of 64, 32-row pages (45 MB): 18.0 us
 //     (four rows of a thread, kinds one after the other: 24); queries alone 11.7, keys
 //     and values alone 12 to 13: instructions and the latency of a piece bound it.
 //     The case of 6005 bf16 tokens above in 64-row e4m3 pages 37.4 (each lane with all
@@ -36,6 +36,11 @@
 //     instead, 16 with the angles in shared memory: 128-row pages 48.0 (by pieces of a
 //     head 68.1), and f32, hd 256, 16 query and 2 KV heads 43.7 (50.6).
 //   * Decode steps: the same two kinds of blocks, of 64 threads, one head each.
+//   * Prompts with n_dims no multiple of 8: the same, of 256 threads. The dims of a thread's pairs
+//     are no vectors there (interleaved: they are, but a pair that turns may be beside one that does
+//     not), so that elements come and go one by one, and angles are worked out for each head again: the
+//     bf16 prompts above with n_dims 100 90 us (interleaved 51; n_dims 96 31 and 38), f32 to e4m3 with
+//     28 37 (25). Heads rotate multiples of 8 dims as a rule, and the vector forms keep their registers.
 #pragma once
 
 #include <type_traits>
