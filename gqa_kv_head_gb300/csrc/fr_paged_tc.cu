@@ -32,9 +32,9 @@
 // by elect.sync (by lane == 0: chunks of 512 with sinks 176 us in place of 152). Masks by
 // bits and a look through V before it is cleared took the tiles at the ends of views from
 // 6000 cycles to 2500 (152 -> 129). Slower were 128-key tiles with P in the place of S
-// (161 in place of 129), 16 softmax warps (148), and two Q tiles with S of the next piece ahead (136 in place of 127). The softmax warps
-// find their next piece while the last PV is awaited (f16: 264 -> 260; e4m3, which has
-// no registers left: 496 -> 546, left out). Results leave 32 bytes at a time: a thread
+// (161 in place of 129), 16 softmax warps (148), and two Q tiles with S of the next piece
+// ahead (136 in place of 127). The softmax warps find their next piece while the last PV is
+// awaited (f16: 264 -> 260; e4m3, which has no registers left: 496 -> 546, left out). Results leave 32 bytes at a time: a thread
 // has a row, so each store of a warp is 32 accesses (16 bytes at a time: 260 -> 244;
 // e4m3 of hd 256 567 -> 536, of hd 64 and 128 496 -> 537, left out).
 #include <string.h>
@@ -138,6 +138,7 @@ __device__ __forceinline__ void add_4(float4* p, const uint32_t* x) {
     asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" :: "l"(p), "f"(__uint_as_float(x[0])),
                  "f"(__uint_as_float(x[1])), "f"(__uint_as_float(x[2])), "f"(__uint_as_float(x[3])) : "memory");
 }
+// N columns of TMEM.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t* x) {
     if (N == 8) tmem_ld_x8(at, x);
